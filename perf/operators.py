@@ -303,7 +303,7 @@ def _quantise(x, u, square):
     b = _to_blocks(x)
     top = b.abs().amax(1)
     scale = top / Q_MAX
-    inv = torch.where(top > 0, Q_MAX / top, torch.zeros_like(top))
+    inv = torch.where(top > 2.0 ** -100, Q_MAX / top, torch.zeros_like(top))
     y = (b.abs() * inv[:, None]).clamp(max=Q_MAX).view(-1)[:n]
     low, high = _grid(y)
     if square:
