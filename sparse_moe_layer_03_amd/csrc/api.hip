@@ -12,6 +12,7 @@
 #include "common.h"
 #include "internal.h"
 #include "plan.h"
+#include "train.h"
 
 namespace moe {
 
@@ -64,7 +65,7 @@ int stream_cu_count(hipStream_t st) {
 
 static int elem_size(int dtype) { return dtype == MOE_BF16 ? 2 : 4; }
 
-static int check_shape(const moe_shape* s) {
+int check_shape(const moe_shape* s) {
   if (s == nullptr) return MOE_EINVAL;
   if (s->T < 1 || s->n_ffn < 1 || s->n_zero < 0 || s->top_k < 1 || s->d_model < 1 || s->d_ff < 1)
     return MOE_EINVAL;
@@ -391,7 +392,7 @@ int moe_debug_checks(uint32_t* flags, int clear) {
     return MOE_EHIP;
   }
   unsigned (*const words[])(bool) = {check_word_route, check_word_dispatch, check_word_gemm,
-                                     check_word_gemm_big, check_word_combine};
+                                     check_word_gemm_big, check_word_combine, check_word_layer_bwd};
   uint32_t v = 0;
   for (auto* fn : words) {
     const unsigned w = fn(clear != 0);

@@ -1,0 +1,242 @@
+// The layer's backward pass beside its grouped products: SwiGLU's backward
+// step, the gradients at the gates and logits, and the sum of the row
+// gradients per token.  All of it moves data once and is bound by HBM; sums
+// are fp32 in a fixed order, no atomics.
+
+#include "common.h"
+#include "train.h"
+
+namespace moe {
+
+// Sum over a block of 256 threads, the same in every thread.
+__device__ __forceinline__ float block_sum(float v, float* s) {
+  v = wave_sum(v);
+  __syncthreads();
+  if (lane_id() == 0) s[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+__device__ __forceinline__ float block_max(float v, float* s) {
+  v = wave_max(v);
+  __syncthreads();
+  if (lane_id() == 0) s[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+swiglu_bwd_kernel(const float* __restrict__ zu, const float* __restrict__ dh0,
+                  const int32_t* __restrict__ perm, const float* __restrict__ gate,
+                  const int32_t* __restrict__ offsets, int n_ffn, int f, T* __restrict__ dzu,
+                  T* __restrict__ hs, float* __restrict__ part) {
+  __shared__ float s[4];
+  const int p = blockIdx.x;  // gridDim.x = T * top_k
+  if (p >= offsets[n_ffn]) return;
+  if (!MOE_GUARD((unsigned)perm[p] < gridDim.x, MOE_CHECK_GEMM_ROW)) return;
+  const float gt = gate[perm[p]];
+  const float* zr = zu + (size_t)p * 2 * f;
+  const float* dr = dh0 + (size_t)p * f;
+  T* o = dzu + (size_t)p * 2 * f;
+  float sum = 0.f;
+  for (int c = threadIdx.x * 4; c < f; c += 1024) {
+    const f32x4_t z = *reinterpret_cast<const f32x4_t*>(zr + c);
+    const f32x4_t u = *reinterpret_cast<const f32x4_t*>(zr + f + c);
+    const f32x4_t dh = *reinterpret_cast<const f32x4_t*>(dr + c);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float sg = 1.f / (1.f + expf(-z[k]));
+      const float si = z[k] * sg;
+      sum += dh[k] * (si * u[k]);
+      const float d = gt * dh[k];
+      o[c + k] = ElemOps<T>::from_f(d * u[k] * (sg * (1.f + z[k] * (1.f - sg))));
+      o[f + c + k] = ElemOps<T>::from_f(d * si);
+      hs[(size_t)p * f + c + k] = ElemOps<T>::from_f(gt * (si * u[k]));
+    }
+  }
+  sum = block_sum(sum, s);
+  if (threadIdx.x == 0) part[p] = sum;
+}
+
+int launch_swiglu_bwd(int dtype, const float* zu, const float* dh, const int32_t* perm,
+                      const float* gate, const int32_t* offsets, int n_ffn, int Tk, int f,
+                      void* dzu, void* hs, float* dgate_part, hipStream_t st) {
+  if (dtype == MOE_BF16)
+    hipLaunchKernelGGL(swiglu_bwd_kernel<__bf16>, dim3(Tk), dim3(256), 0, st, zu, dh, perm, gate,
+                       offsets, n_ffn, f, (__bf16*)dzu, (__bf16*)hs, dgate_part);
+  else
+    hipLaunchKernelGGL(swiglu_bwd_kernel<float>, dim3(Tk), dim3(256), 0, st, zu, dh, perm, gate,
+                       offsets, n_ffn, f, (float*)dzu, (float*)hs, dgate_part);
+  return check_launch();
+}
+
+// One workgroup per token.
+template <typename T>
+__global__ void __launch_bounds__(256) token_bwd_kernel(TokenArgs a) {
+  constexpr int CE = 16 / sizeof(T);
+  constexpr int MAXE = 1024;
+  __shared__ float s[4];
+  __shared__ float s_dp[MAXE];   // gradient at p, by expert
+  __shared__ float s_dg[16];
+  __shared__ int s_e[16];
+  const int t = blockIdx.x, tid = threadIdx.x;
+  if (t == 0 && a.logits) {
+    if (tid < 2) a.route_offs[tid] = tid ? a.T : 0;
+    if (tid <= a.nsplit) a.split_offs[tid] = (int)((long)tid * a.T / a.nsplit);
+  }
+  for (int e = tid; e < a.E; e += 256) s_dp[e] = 0.f;
+  bool identity = false;
+  if (tid < a.k) {
+    const int e = a.idx[t * a.k + tid];
+    const int row = a.inv_perm[t * a.k + tid];
+    s_e[tid] = e;
+    float dg = 0.f;
+    if (e < a.n_ffn && MOE_GUARD((unsigned)row < (unsigned)(a.T * a.k), MOE_CHECK_COMBINE_ROW))
+      for (int q = 0; q < a.parts; ++q) dg += a.part[(size_t)row * a.parts + q];
+    s_dg[tid] = dg;
+    identity = e >= a.n_ffn;
+  }
+  if (__syncthreads_or(identity)) {
+    const T* x = (const T*)a.x + (size_t)t * a.d;
+    const T* dy = (const T*)a.dy + (size_t)t * a.d;
+    float dot = 0.f;
+    for (int c = tid * CE; c < a.d; c += 256 * CE) {
+      float fx[CE], fd[CE];
+      unpack16(ld16(x + c), fx, (T*)nullptr);
+      unpack16(ld16(dy + c), fd, (T*)nullptr);
+#pragma unroll
+      for (int k = 0; k < CE; ++k) dot += fx[k] * fd[k];
+    }
+    dot = block_sum(dot, s);
+    if (identity) s_dg[tid] = dot;
+  }
+  __syncthreads();
+  if (tid < a.k) {
+    a.dgate[t * a.k + tid] = s_dg[tid];
+    const int e = s_e[tid];
+    if ((unsigned)e < (unsigned)a.E) s_dp[e] = a.scaling * s_dg[tid];
+  }
+  if (!a.logits) return;
+  __syncthreads();
+  const float* lg = a.logits + (size_t)t * a.E;
+  float p[MAXE / 256];
+  float top = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < MAXE / 256; ++q) {
+    const int e = tid + q * 256;
+    p[q] = e < a.E ? lg[e] : -INFINITY;
+    top = fmaxf(top, p[q]);
+  }
+  top = block_max(top, s);
+  float sum = 0.f;
+#pragma unroll
+  for (int q = 0; q < MAXE / 256; ++q) {
+    const int e = tid + q * 256;
+    p[q] = e < a.E ? expf(p[q] - top) : 0.f;
+    sum += p[q];
+  }
+  sum = block_sum(sum, s);
+  float dot = 0.f;
+#pragma unroll
+  for (int q = 0; q < MAXE / 256; ++q) {
+    const int e = tid + q * 256;
+    p[q] /= sum;
+    if (e < a.E) dot += p[q] * s_dp[e];
+  }
+  dot = block_sum(dot, s);
+#pragma unroll
+  for (int q = 0; q < MAXE / 256; ++q) {
+    const int e = tid + q * 256;
+    const float v = e < a.E ? p[q] * (s_dp[e] - dot) : 0.f;
+    if (e < a.ep) ((T*)a.dl)[(size_t)t * a.ep + e] = ElemOps<T>::from_f(v);
+    if (a.dlogits && e < a.E) a.dlogits[(size_t)t * a.E + e] = v;
+  }
+}
+
+int launch_token_bwd(int dtype, const TokenArgs& a, hipStream_t st) {
+  if (dtype == MOE_BF16)
+    hipLaunchKernelGGL(token_bwd_kernel<__bf16>, dim3(a.T), dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL(token_bwd_kernel<float>, dim3(a.T), dim3(256), 0, st, a);
+  return check_launch();
+}
+
+MOE_CHECK_ACCESSOR(check_word_layer_bwd)
+
+// One workgroup per token: its FFN rows, the identity gates' share of dy and
+// the router's share, summed in that order.
+template <typename T>
+__global__ void __launch_bounds__(256)
+dx_kernel(const T* __restrict__ dx_perm, const T* __restrict__ dy, const float* __restrict__ dxr,
+          const int32_t* __restrict__ idx, const float* __restrict__ gate,
+          const int32_t* __restrict__ inv_perm, int d, int k, int n_ffn, T* __restrict__ dx) {
+  constexpr int CE = 16 / sizeof(T);
+  __shared__ int s_row[16];
+  __shared__ float s_gz;
+  __shared__ int s_n;
+  const int t = blockIdx.x, tid = threadIdx.x;
+  if (tid < 64) {
+    int e = n_ffn, row = 0;
+    float g = 0.f;
+    if (tid < k) {
+      e = idx[t * k + tid];
+      g = gate[t * k + tid];
+      row = inv_perm[t * k + tid];
+      // gridDim.x = T
+      if (e < n_ffn && !MOE_GUARD((unsigned)row < gridDim.x * (unsigned)k, MOE_CHECK_COMBINE_ROW))
+        row = 0;
+    }
+    const bool ffn = tid < k && e < n_ffn;
+    const uint64_t fb = __ballot(ffn);
+    if (ffn) s_row[__popcll(fb & lanemask_lt())] = row;
+    const float gid = (tid < k && !ffn) ? g : 0.f;
+    float gz = 0.f;
+    for (int j = 0; j < k; ++j) gz += __shfl(gid, j, kWave);
+    if (tid == 0) {
+      s_n = __popcll(fb);
+      s_gz = gz;
+    }
+  }
+  __syncthreads();
+  const int n = s_n;
+  const float gz = s_gz;
+  const bool ident = n < k;
+  for (int c = tid * CE; c < d; c += 256 * CE) {
+    float acc[CE], v[CE];
+#pragma unroll
+    for (int i = 0; i < CE; ++i) acc[i] = 0.f;
+    for (int q = 0; q < n; ++q) {
+      unpack16(ld16(dx_perm + (size_t)s_row[q] * d + c), v, (T*)nullptr);
+#pragma unroll
+      for (int i = 0; i < CE; ++i) acc[i] += v[i];
+    }
+    if (ident) {
+      unpack16(ld16(dy + (size_t)t * d + c), v, (T*)nullptr);
+#pragma unroll
+      for (int i = 0; i < CE; ++i) acc[i] += gz * v[i];
+    }
+    if (dxr) {
+#pragma unroll
+      for (int i = 0; i < CE; i += 4) {
+        const f32x4_t r = *reinterpret_cast<const f32x4_t*>(dxr + (size_t)t * d + c + i);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[i + q] += r[q];
+      }
+    }
+    st16(dx + (size_t)t * d + c, pack16(acc, (T*)nullptr));
+  }
+}
+
+int launch_dx(int dtype, const void* dx_perm, const void* dy, const float* dxr, const int32_t* idx,
+              const float* gate, const int32_t* inv_perm, int T, int d, int k, int n_ffn, void* dx,
+              hipStream_t st) {
+  if (dtype == MOE_BF16)
+    hipLaunchKernelGGL(dx_kernel<__bf16>, dim3(T), dim3(256), 0, st, (const __bf16*)dx_perm,
+                       (const __bf16*)dy, dxr, idx, gate, inv_perm, d, k, n_ffn, (__bf16*)dx);
+  else
+    hipLaunchKernelGGL(dx_kernel<float>, dim3(T), dim3(256), 0, st, (const float*)dx_perm,
+                       (const float*)dy, dxr, idx, gate, inv_perm, d, k, n_ffn, (float*)dx);
+  return check_launch();
+}
+
+}  // namespace moe

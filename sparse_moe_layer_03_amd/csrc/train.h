@@ -1,0 +1,85 @@
+// Internal host-side interface of the training operators' kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/moe_train.h"
+#include "internal.h"
+
+namespace moe {
+
+// One grouped product in the kernels' terms: out[i, j] = sum_r A(i, r) B(j, r)
+// for every group.  FWD and DX: i runs over the group's rows, r over R.  DW:
+// r runs over the group's rows, i over I.  j runs over J.
+struct GmmArgs {
+  const void* a;
+  const void* b;
+  void* out;
+  const int32_t* offsets;  // [ngroups + 1]
+  float* part;             // split reductions: fp32 partial outputs, split-major
+  int64_t lda, ldb, ldo;   // elements between rows of the arrays
+  int64_t b_group;         // elements between groups of b (FWD, DX)
+  int64_t out_group;       // elements between groups of out (DW)
+  int64_t part_stride;     // elements between splits in `part`
+  int ngroups;
+  int M;                   // rows that the row arrays hold
+  int I, J, R;             // extents (I: DW; R: FWD and DX)
+  int accumulate;
+  int nsplit;
+};
+
+// Any sizes, strides and element types.  vec: every row of a, b and out is
+// 16-byte aligned.
+int launch_gmm_general(int form, int dtype, int out_dtype, bool vec, const GmmArgs& g,
+                       hipStream_t st);
+// Sums `part` into out (rounded, added to when accumulating).
+int launch_gmm_join(int form, int out_dtype, const GmmArgs& g, hipStream_t st);
+
+// The layer's shape checks (moe.h's limits).
+int check_shape(const moe_shape* s);
+
+int launch_adamw(const moe_adamw_params* hp, const moe_adamw_tensor* tensors, int n_tensors,
+                 moe_adamw_state* state, const float* grad_scale, const float* lr_scale,
+                 hipStream_t st);
+uint64_t adamw_max_elements();
+
+// ---- the layer's backward pass beside its products
+
+unsigned check_word_layer_bwd(bool clear);  // as the accessors of internal.h
+
+// Per FFN row p: h, dz, du from z, u and dh (fp32 [rows, f], z and u in
+// `zu` [rows, 2 f]), the row's gate applied; dzu [rows, 2 f] and hs
+// [rows, f] in dtype, dgate_part[p] = <dh, h>.
+int launch_swiglu_bwd(int dtype, const float* zu, const float* dh, const int32_t* perm,
+                      const float* gate, const int32_t* offsets, int n_ffn, int Tk, int f,
+                      void* dzu, void* hs, float* dgate_part, hipStream_t st);
+
+// Per token: dgate (parts: partial sums per FFN row), then, with logits, dlogits (fp32 if not
+// null, and in dtype with rows of ep elements, zeros behind E) and the row
+// bounds of the router's products: route_offs[0..1] = 0, T and
+// split_offs[s] = s * T / nsplit.
+struct TokenArgs {
+  const void* x;
+  const void* dy;
+  const float* logits;
+  const int32_t* idx;
+  const int32_t* inv_perm;
+  const float* part;
+  float* dgate;
+  float* dlogits;
+  void* dl;
+  int32_t* route_offs;
+  int32_t* split_offs;
+  float scaling;
+  int T, d, E, k, n_ffn, parts, ep, nsplit;
+};
+int launch_token_bwd(int dtype, const TokenArgs& a, hipStream_t st);
+
+// dx[t] = sum over FFN slots of dx_perm rows + (identity gates) dy[t] + dxr[t]
+// (dxr fp32, may be null).
+int launch_dx(int dtype, const void* dx_perm, const void* dy, const float* dxr, const int32_t* idx,
+              const float* gate, const int32_t* inv_perm, int T, int d, int k, int n_ffn, void* dx,
+              hipStream_t st);
+
+}  // namespace moe

@@ -1,0 +1,348 @@
+// C ABI of the training operators: argument checks, workspace layout and the
+// launch sequence of each call.  Every check runs on the host before any
+// work is enqueued; no call allocates, frees or synchronises.
+
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "common.h"
+#include "train.h"
+
+namespace moe {
+
+static bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+static bool al4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+static size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+static long cdiv(long a, long b) { return (a + b - 1) / b; }
+static int elem_size(int dtype) { return dtype == MOE_BF16 ? 2 : 4; }
+
+static int check_gmm(const moe_gmm_shape* s) {
+  if (s == nullptr) return MOE_EINVAL;
+  if (s->form < MOE_GMM_FWD || s->form > MOE_GMM_DW || s->n_groups < 1 || s->M < 0 || s->N < 1 ||
+      s->K < 1 || s->lda < s->K || s->ldc < s->N)
+    return MOE_EINVAL;
+  if (s->dtype != MOE_F32 && s->dtype != MOE_BF16) return MOE_EUNSUPPORTED;
+  if (s->out_dtype != s->dtype && s->out_dtype != MOE_F32) return MOE_EUNSUPPORTED;
+  if (s->n_groups > 1024 || s->N > (1 << 20) || s->K > (1 << 20) || s->lda >= (1 << 24) ||
+      s->ldc >= (1 << 24))
+    return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+// A product with too few output tiles to fill the chip has its reduction cut
+// into this many ranges, each at least 256 long, whose fp32 partial outputs
+// are joined by a second kernel.  A function of the sizes and the device's CU
+// count only: it sizes the workspace (at most a tile per CU: 16 MiB).
+static int gmm_nsplit(int form, long G, long M, long I, long J, long R, int cus) {
+  const long jt = cdiv(J, 128);
+  const long tiles = form == MOE_GMM_DW ? G * cdiv(I, 128) * jt : (M / 128 + std::min(G, M)) * jt;
+  const long red = form == MOE_GMM_DW ? M / G : R;
+  if (tiles < 1) return 1;
+  return (int)std::max(1l, std::min({64l, cus / tiles, red / 256}));
+}
+
+static int gmm_splits_of(const moe_gmm_shape* s, int cus) {
+  const bool fwd = s->form == MOE_GMM_FWD;
+  return gmm_nsplit(s->form, s->n_groups, s->M, s->N, fwd ? s->N : s->K, fwd ? s->K : s->N, cus);
+}
+
+static size_t gmm_part_bytes(const moe_gmm_shape* s, int nsplit) {
+  if (nsplit <= 1) return 0;
+  const size_t out = s->form == MOE_GMM_DW ? (size_t)s->n_groups * s->N * s->K
+                                           : (size_t)s->M * (s->form == MOE_GMM_FWD ? s->N : s->K);
+  return up256(out * nsplit * sizeof(float));
+}
+
+// Runs one product, its split reduction joined.
+static int run_gmm(int form, int dtype, int out_dtype, const GmmArgs& g, hipStream_t st) {
+  const int es = elem_size(dtype);
+  const bool vec = g.lda % 4 == 0 && g.ldb % 4 == 0 && g.b_group % 4 == 0 && al16(g.a) && al16(g.b) &&
+                   es > 0;
+  int rc = launch_gmm_general(form, dtype, out_dtype, vec, g, st);
+  if (rc || g.nsplit <= 1) return rc;
+  return launch_gmm_join(form, out_dtype, g, st);
+}
+
+// ---- the layer's backward pass: workspace
+
+constexpr int kRouteSplits = 16;  // token ranges of the router's weight gradient
+
+struct BwdLayout {
+  size_t xp, dyp, zu, dh, dzu, hs, part, dl, offs, dxr, drp, total;
+  int ep, nsplit;
+};
+
+static BwdLayout bwd_layout(const moe_shape* s) {
+  const size_t es = elem_size(s->dtype);
+  const size_t E = (size_t)s->n_ffn + s->n_zero, rows = (size_t)s->T * s->top_k;
+  const size_t d = s->d_model, f = s->d_ff;
+  BwdLayout w;
+  w.ep = (int)((E + 7) & ~(size_t)7);
+  w.nsplit = (int)std::max(1l, std::min((long)kRouteSplits, (long)s->T / 256));
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = up256(off + bytes);
+    return at;
+  };
+  w.xp = take(rows * d * es);
+  w.dyp = take(rows * d * es);
+  w.zu = take(rows * 2 * f * 4);
+  w.dh = take(rows * f * 4);
+  w.dzu = take(rows * 2 * f * es);
+  w.hs = take(rows * f * es);
+  w.part = take(rows * 4);
+  w.dl = take((size_t)s->T * w.ep * es);
+  w.offs = take((2 + kRouteSplits + 1) * sizeof(int32_t));
+  w.dxr = take((size_t)s->T * d * 4);
+  w.drp = take(E * d * 4 * w.nsplit);
+  w.total = off;
+  return w;
+}
+
+static int check_backward(const moe_shape* s, const moe_backward_io* io) {
+  const int rc = check_shape(s);
+  if (rc) return rc;
+  if (!io) return MOE_EINVAL;
+  if (!io->x || !io->topk_idx || !io->topk_gate || !io->offsets || !io->perm || !io->inv_perm ||
+      !io->w_gate || !io->w_up || !io->w_down || !io->dy || !io->dx || !io->dgate ||
+      !io->dw_gate || !io->dw_up || !io->dw_down || io->reserved != 0)
+    return MOE_EINVAL;
+  if (io->logits ? (!io->w_router || !io->dw_router)
+                 : (io->w_router || io->dw_router || io->dlogits))
+    return MOE_EINVAL;
+  if (!al16(io->x) || !al16(io->w_router) || !al16(io->w_gate) || !al16(io->w_up) ||
+      !al16(io->w_down) || !al16(io->dy) || !al16(io->dx) || !al16(io->dw_router) ||
+      !al16(io->dw_gate) || !al16(io->dw_up) || !al16(io->dw_down) || !al4(io->logits) ||
+      !al4(io->topk_idx) || !al4(io->topk_gate) || !al4(io->offsets) || !al4(io->perm) ||
+      !al4(io->inv_perm) || !al4(io->dgate) || !al4(io->dlogits))
+    return MOE_EALIGN;
+  return MOE_OK;
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_grouped_matmul_workspace_bytes(const moe_gmm_shape* s) {
+  if (check_gmm(s) != MOE_OK) return 0;
+  const int cus = device_cu_count();
+  return cus > 0 ? gmm_part_bytes(s, gmm_splits_of(s, cus)) : 0;
+}
+
+int moe_grouped_matmul(const moe_gmm_shape* s, const int32_t* offsets, const void* lhs,
+                       const void* rhs, void* out, void* ws, void* stream) {
+  const int rc = check_gmm(s);
+  if (rc) return rc;
+  const bool dw = s->form == MOE_GMM_DW;
+  // with no rows, arrays that have one row per token may be null
+  const bool none = s->M == 0;
+  if (!offsets || (!lhs && !none) || (!rhs && !(none && dw)) || (!out && !(none && !dw)))
+    return MOE_EINVAL;
+  if (!al4(offsets) || !al16(lhs) || !al16(rhs) || !al16(out) || !al16(ws)) return MOE_EALIGN;
+  const int cus = device_cu_count();
+  if (cus <= 0) return MOE_EHIP;
+  GmmArgs g{};
+  g.a = lhs;
+  g.b = rhs;
+  g.out = out;
+  g.offsets = offsets;
+  g.ngroups = s->n_groups;
+  g.M = s->M;
+  g.I = s->N;
+  g.accumulate = s->accumulate != 0;
+  g.nsplit = gmm_splits_of(s, cus);
+  if (g.nsplit > 1 && !ws) return MOE_EINVAL;
+  g.part = (float*)ws;
+  if (s->form == MOE_GMM_FWD) {
+    g.lda = s->lda;
+    g.ldb = s->K;
+    g.ldo = s->ldc;
+    g.b_group = (int64_t)s->N * s->K;
+    g.J = s->N;
+    g.R = s->K;
+    g.part_stride = (int64_t)s->M * s->N;
+  } else if (s->form == MOE_GMM_DX) {
+    g.lda = s->ldc;
+    g.ldb = s->K;
+    g.ldo = s->lda;
+    g.b_group = (int64_t)s->N * s->K;
+    g.J = s->K;
+    g.R = s->N;
+    g.part_stride = (int64_t)s->M * s->K;
+  } else {
+    g.lda = s->ldc;
+    g.ldb = s->lda;
+    g.ldo = s->K;
+    g.out_group = (int64_t)s->N * s->K;
+    g.J = s->K;
+    g.part_stride = (int64_t)s->n_groups * s->N * s->K;
+  }
+  if (none && !dw) return MOE_OK;
+  return run_gmm(s->form, s->dtype, s->out_dtype, g, (hipStream_t)stream);
+}
+
+size_t moe_layer_backward_workspace_bytes(const moe_shape* s) {
+  if (check_shape(s) != MOE_OK) return 0;
+  return bwd_layout(s).total;
+}
+
+int moe_layer_backward(const moe_shape* s, const moe_backward_io* io, void* ws, void* stream) {
+  int rc = check_backward(s, io);
+  if (rc) return rc;
+  if (!ws) return MOE_EINVAL;
+  if (!al16(ws)) return MOE_EALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  const BwdLayout w = bwd_layout(s);
+  char* base = (char*)ws;
+  const int E = s->n_ffn + s->n_zero, Tk = s->T * s->top_k;
+  const int d = s->d_model, f = s->d_ff, dt = s->dtype, es = elem_size(dt);
+  char *xp = base + w.xp, *dyp = base + w.dyp, *dzu = base + w.dzu, *hs = base + w.hs;
+  float *zu = (float*)(base + w.zu), *dh = (float*)(base + w.dh), *part = (float*)(base + w.part);
+  float *dxr = (float*)(base + w.dxr), *drp = (float*)(base + w.drp);
+  char* dl = base + w.dl;
+  int32_t *route_offs = (int32_t*)(base + w.offs), *split_offs = route_offs + 2;
+
+  // the FFN rows of x and dy, grouped by expert
+  if ((rc = launch_gather(dt, io->x, io->perm, io->offsets, s->n_ffn, Tk, s->top_k, d, xp, st)))
+    return rc;
+  if ((rc = launch_gather(dt, io->dy, io->perm, io->offsets, s->n_ffn, Tk, s->top_k, d, dyp, st)))
+    return rc;
+
+  GmmArgs g{};
+  g.offsets = io->offsets;
+  g.ngroups = s->n_ffn;
+  g.M = Tk;
+  g.nsplit = 1;
+  auto product = [&](int form, int out_dtype, const void* a, int64_t lda, const void* b, int64_t ldb,
+                     void* out, int64_t ldo, int I, int J, int R, int accumulate) {
+    g.a = a;
+    g.lda = lda;
+    g.b = b;
+    g.ldb = ldb;
+    g.out = out;
+    g.ldo = ldo;
+    g.b_group = (int64_t)d * f;
+    g.out_group = (int64_t)d * f;
+    g.I = I;
+    g.J = J;
+    g.R = R;
+    g.accumulate = accumulate;
+    return run_gmm(form, dt, out_dtype, g, st);
+  };
+  // z and u again, and the gradient at H
+  if ((rc = product(MOE_GMM_FWD, MOE_F32, xp, d, io->w_gate, d, zu, 2 * f, 0, f, d, 0))) return rc;
+  if ((rc = product(MOE_GMM_FWD, MOE_F32, xp, d, io->w_up, d, zu + f, 2 * f, 0, f, d, 0))) return rc;
+  if ((rc = product(MOE_GMM_DX, MOE_F32, dyp, d, io->w_down, f, dh, f, 0, f, d, 0))) return rc;
+  if ((rc = launch_swiglu_bwd(dt, zu, dh, io->perm, io->topk_gate, io->offsets, s->n_ffn, Tk, f,
+                              dzu, hs, part, st)))
+    return rc;
+  // gradients of the experts' weights
+  const int acc = io->accumulate != 0;
+  if ((rc = product(MOE_GMM_DW, dt, dzu, 2 * f, xp, d, io->dw_gate, d, f, d, 0, acc))) return rc;
+  if ((rc = product(MOE_GMM_DW, dt, dzu + (size_t)f * es, 2 * f, xp, d, io->dw_up, d, f, d, 0, acc)))
+    return rc;
+  if ((rc = product(MOE_GMM_DW, dt, dyp, d, hs, f, io->dw_down, f, d, f, 0, acc))) return rc;
+  // gradients of the rows, over x's rows, which are not needed any more
+  char* dx_perm = xp;
+  if ((rc = product(MOE_GMM_DX, dt, dzu, 2 * f, io->w_gate, d, dx_perm, d, 0, d, f, 0))) return rc;
+  if ((rc = product(MOE_GMM_DX, dt, dzu + (size_t)f * es, 2 * f, io->w_up, d, dx_perm, d, 0, d, f, 1)))
+    return rc;
+
+  // gradients at the gates and logits, and the router's products
+  TokenArgs a{};
+  a.x = io->x;
+  a.dy = io->dy;
+  a.logits = io->logits;
+  a.idx = io->topk_idx;
+  a.inv_perm = io->inv_perm;
+  a.part = part;
+  a.dgate = io->dgate;
+  a.dlogits = io->dlogits;
+  a.dl = dl;
+  a.route_offs = route_offs;
+  a.split_offs = split_offs;
+  a.scaling = s->routed_scaling;
+  a.T = s->T;
+  a.d = d;
+  a.E = E;
+  a.k = s->top_k;
+  a.n_ffn = s->n_ffn;
+  a.parts = 1;
+  a.ep = w.ep;
+  a.nsplit = w.nsplit;
+  if ((rc = launch_token_bwd(dt, a, st))) return rc;
+  if (io->logits) {
+    GmmArgs r{};
+    r.a = dl;
+    r.lda = w.ep;
+    r.M = s->T;
+    r.nsplit = 1;
+    // dlogits W_router, fp32
+    r.b = io->w_router;
+    r.ldb = d;
+    r.out = dxr;
+    r.ldo = d;
+    r.offsets = route_offs;
+    r.ngroups = 1;
+    r.J = d;
+    r.R = E;
+    if ((rc = run_gmm(MOE_GMM_DX, dt, MOE_F32, r, st))) return rc;
+    // dlogits^T x over ranges of the tokens, joined
+    r.b = io->x;
+    r.out = drp;
+    r.out_group = (int64_t)E * d;
+    r.offsets = split_offs;
+    r.ngroups = w.nsplit;
+    r.I = E;
+    if ((rc = run_gmm(MOE_GMM_DW, dt, MOE_F32, r, st))) return rc;
+    r.part = drp;
+    r.part_stride = (int64_t)E * d;
+    r.nsplit = w.nsplit;
+    r.ngroups = 1;
+    r.out = io->dw_router;
+    r.accumulate = acc;
+    if ((rc = launch_gmm_join(MOE_GMM_DW, dt, r, st))) return rc;
+  }
+  return launch_dx(dt, dx_perm, io->dy, io->logits ? dxr : nullptr, io->topk_idx, io->topk_gate,
+                   io->inv_perm, s->T, d, s->top_k, s->n_ffn, io->dx, st);
+}
+
+int moe_adamw(const moe_adamw_params* hp, const moe_adamw_tensor* tensors, int32_t n_tensors,
+              moe_adamw_state* state, const float* grad_scale, const float* lr_scale,
+              void* stream) {
+  if (!hp || !tensors || !state || n_tensors < 1) return MOE_EINVAL;
+  if (!isfinite(hp->lr) || !isfinite(hp->beta1) || !isfinite(hp->beta2) || !isfinite(hp->eps))
+    return MOE_ENONFINITE;
+  if (hp->lr < 0 || hp->beta1 < 0 || hp->beta1 >= 1 || hp->beta2 < 0 || hp->beta2 >= 1 ||
+      !((float)hp->eps > 0.f))
+    return MOE_EINVAL;
+  if (hp->state_bits != 32 && hp->state_bits != 8) return MOE_EUNSUPPORTED;
+  if (!al16(state) || !al4(grad_scale) || !al4(lr_scale)) return MOE_EALIGN;
+  uint64_t n = 0;
+  for (int k = 0; k < n_tensors; ++k) {
+    const moe_adamw_tensor& t = tensors[k];
+    if (t.n < 0) return MOE_EINVAL;
+    if (!isfinite(t.weight_decay)) return MOE_ENONFINITE;
+    if (t.weight_decay < 0) return MOE_EINVAL;
+    if ((t.param_dtype != MOE_F32 && t.param_dtype != MOE_BF16) ||
+        (t.grad_dtype != MOE_F32 && t.grad_dtype != MOE_BF16))
+      return MOE_EUNSUPPORTED;
+    if ((uint64_t)t.n > adamw_max_elements() || (n += (uint64_t)t.n) > adamw_max_elements())
+      return MOE_EUNSUPPORTED;
+    if (t.n == 0) continue;
+    const bool q8 = hp->state_bits == 8;
+    if (!t.param || !t.grad || !t.m || !t.v || (q8 && (!t.m_scale || !t.v_scale)))
+      return MOE_EINVAL;
+    if (!al16(t.param) || !al16(t.grad) || !al16(t.master) || !al16(t.m) || !al16(t.v) ||
+        (q8 && (!al4(t.m_scale) || !al4(t.v_scale))))
+      return MOE_EALIGN;
+  }
+  return launch_adamw(hp, tensors, n_tensors, state, grad_scale, lr_scale, (hipStream_t)stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,293 @@
+"""moe_layer_backward against the layer's gradients in 64 bits (by automatic
+differentiation of the definition and by differences), on the selections that
+moe_route makes; experts without rows, identity experts only, accumulation, a
+frozen router; the whole training step; streams and captured graphs."""
+
+import pytest
+import torch
+
+from sparse_moe_layer_03_amd import binding as B
+from sparse_moe_layer_03_amd import train as T
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+class Case:
+    """One layer with its forward pass done by the library."""
+
+    def __init__(self, dtype, Tn, d, n_ffn, n_zero, ff, k, scaling=1.0, skew=0.0, bias=None, seed=0):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        E, dt = n_ffn + n_zero, DT[dtype]
+
+        def normal(shape, std):
+            return (torch.randn(shape, generator=g, device="cuda") * std).to(dt)
+
+        self.k, self.n_ffn, self.scaling = k, n_ffn, scaling
+        self.x, self.dy = normal((Tn, d), 1.0), normal((Tn, d), 1.0)
+        self.wr = normal((E, d), d ** -0.5)
+        self.wg, self.wu = normal((n_ffn, ff, d), d ** -0.5), normal((n_ffn, ff, d), d ** -0.5)
+        self.wd = normal((n_ffn, d, ff), ff ** -0.5)
+        self.lb = torch.randn(E, generator=g, device="cuda") * skew
+        self.bias = torch.zeros(E, device="cuda") if bias is None else bias.cuda()
+        self.shape = B.make_shape(Tn, d, n_ffn, n_zero, ff, k, dtype, scaling)
+        self.buf, self.tb = B.LayerBuffers(self.shape), T.TrainBuffers(self.shape)
+        self.forward()
+
+    def forward(self):
+        B.layer_forward(self.buf, self.x, self.wr, self.bias, self.wg, self.wu, self.wd,
+                        logit_bias=self.lb, logits_out=self.tb.logits)
+
+    def backward(self, **kw):
+        T.layer_backward(self.buf, self.tb, self.x, self.wr, self.wg, self.wu, self.wd, self.dy, **kw)
+        torch.cuda.synchronize()
+        return self.tb
+
+    def loss(self, x, wr, wg, wu, wd):
+        """<y, dy> in 64 bits on the library's selection, y as the forward pass defines it."""
+        idx = self.buf.topk_idx.long()
+        p = torch.softmax(x @ wr.t() + self.lb.double(), 1)
+        gate = self.scaling * p.gather(1, idx)
+        y = (gate * (idx >= self.n_ffn)).sum(1, keepdim=True) * x
+        for e in range(self.n_ffn):
+            t, j = (idx == e).nonzero(as_tuple=True)
+            h = torch.nn.functional.silu(x[t] @ wg[e].t()) * (x[t] @ wu[e].t())
+            y = y.index_add(0, t, gate[t, j][:, None] * (h @ wd[e].t()))
+        return (y * self.dy.double()).sum()
+
+    def leaves(self):
+        return [v.double().requires_grad_() for v in (self.x, self.wr, self.wg, self.wu, self.wd)]
+
+    def reference(self):
+        leaves = self.leaves()
+        self.loss(*leaves).backward()
+        return dict(zip(("dx", "dw_router", "dw_gate", "dw_up", "dw_down"),
+                        [v.grad if v.grad is not None else torch.zeros_like(v) for v in leaves]))
+
+
+# Relative error allowed in the 2-norm of a gradient.  bf16: a product's
+# operands carry up to three roundings by half a step (dz, du or gate h; the
+# rows' gradients; the result), each at most 2^-8 of its value, and rounding
+# errors of many terms are independent, so the norms add to at most
+# sqrt(3) 2^-8 < 7e-3.  fp32: sums of up to some thousand terms, each
+# addition off by 2^-23 of the running sum, which in the norm is below
+# sqrt(n) 2^-23 a term: 64 * 2^-23 < 1e-5.
+TOL = {"bf16": 7e-3, "f32": 1e-5}
+
+
+def far(a, b):
+    n = b.double().norm().item()
+    d = (a.double() - b.double()).norm().item()
+    return d / n if n else d
+
+
+CASES = [
+    # dtype, T, d, n_ffn, n_zero, d_ff, top_k, scaling, skew
+    ("f32", 64, 128, 8, 4, 256, 2, 1.0, 0.0),
+    ("f32", 33, 64, 5, 0, 64, 3, 2.5, 1.0),
+    ("f32", 1, 64, 1, 0, 64, 1, 1.0, 0.0),
+    ("f32", 257, 192, 17, 9, 128, 7, 9.0, 2.0),
+    ("bf16", 64, 128, 8, 4, 256, 2, 1.0, 0.0),
+    ("bf16", 1, 64, 3, 2, 64, 2, 1.0, 0.0),
+    ("bf16", 130, 192, 16, 8, 192, 4, 2.5, 2.0),
+    ("bf16", 1000, 256, 6, 3, 320, 4, 1.0, 1.0),
+    ("bf16", 777, 512, 100, 28, 64, 12, 9.0, 2.0),
+    ("bf16", 300, 64, 1, 0, 128, 1, 1.0, 0.0),
+    ("bf16", 2048, 320, 4, 4, 448, 2, 1.0, 0.0),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
+def test_gradients(case):
+    say("[layer]", case)
+    c = Case(*case)
+    tb, ref = c.backward(), c.reference()
+    for name, want in ref.items():
+        got = getattr(tb, name)
+        assert torch.isfinite(got.double()).all(), name
+        err = far(got, want)
+        say(f"  {name} {err:.2e}")
+        assert err <= TOL[case[0]], (name, err)
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
+def test_gradients_at_gates_and_logits(case):
+    c = Case(*case)
+    tb = c.backward()
+    idx, x, dy = c.buf.topk_idx.long(), c.x.double(), c.dy.double()
+    want = (x * dy).sum(1, keepdim=True).expand(-1, c.k).clone()
+    for e in range(c.n_ffn):
+        t, j = (idx == e).nonzero(as_tuple=True)
+        h = torch.nn.functional.silu(x[t] @ c.wg[e].double().t()) * (x[t] @ c.wu[e].double().t())
+        want[t, j] = ((dy[t] @ c.wd[e].double()) * h).sum(1)
+    # fp32 from end to end whatever the type: see the fp32 bound above
+    assert far(tb.dgate, want) <= 1e-5
+    p = torch.softmax(tb.logits.double(), 1)
+    dp = torch.zeros_like(p).scatter_(1, idx, c.scaling * want)
+    wl = p * (dp - (p * dp).sum(1, keepdim=True))
+    scale = (p * dp).norm().item()          # the difference cancels against this
+    assert (tb.dlogits.double() - wl).norm().item() <= 1e-5 * scale
+
+
+def test_gradients_against_differences():
+    c = Case("f32", 40, 64, 6, 3, 64, 3, 1.5, 1.0)
+    tb, leaves = c.backward(), [v.detach() for v in c.leaves()]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for i, name in enumerate(("dx", "dw_router", "dw_gate", "dw_up", "dw_down")):
+        way = torch.randn(leaves[i].shape, generator=g, device="cuda", dtype=torch.float64)
+        h = 1e-5
+        up, down = list(leaves), list(leaves)
+        up[i], down[i] = leaves[i] + h * way, leaves[i] - h * way
+        diff = (c.loss(*up) - c.loss(*down)).item() / (2 * h)
+        got = getattr(tb, name).double()
+        # 1e-5 of the gradient's norm along the direction, and h^2 of the curvature
+        assert abs((got * way).sum().item() - diff) <= 1e-5 * got.norm().item() * way.norm().item() + 1e-6
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_only_identity_experts_are_selected(dtype):
+    bias = torch.tensor([-float("inf")] * 4 + [0.0] * 3)
+    c = Case(dtype, 50, 128, 4, 3, 128, 2, 1.5, 1.0, bias=bias)
+    assert int(c.buf.offsets[4]) == 0
+    tb, ref = c.backward(), c.reference()
+    for name in ("dw_gate", "dw_up", "dw_down"):
+        assert (getattr(tb, name) == 0).all(), name
+    for name in ("dx", "dw_router"):
+        assert far(getattr(tb, name), ref[name]) <= TOL[dtype]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_experts_without_rows_get_zero_gradients(dtype):
+    bias = torch.tensor([0.0, -float("inf"), 0.0, -float("inf"), 0.0])
+    c = Case(dtype, 70, 64, 4, 1, 192, 2, 1.0, 0.0, bias=bias)
+    for t in (c.tb.dw_gate, c.tb.dw_up, c.tb.dw_down):
+        t.fill_(float("nan"))
+    tb, ref = c.backward(), c.reference()
+    for name, want in ref.items():
+        assert far(getattr(tb, name), want) <= TOL[dtype], name
+    for t in (tb.dw_gate, tb.dw_up, tb.dw_down):
+        assert (t[1] == 0).all() and (t[3] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_accumulated_weight_gradients(dtype):
+    c = Case(dtype, 200, 128, 5, 2, 192, 3, 1.0, 1.0)
+    c.backward()
+    names = ("dw_router", "dw_gate", "dw_up", "dw_down")
+    once = {n: getattr(c.tb, n).clone() for n in names}
+    dx = c.tb.dx.clone()
+    c.backward(accumulate=True)
+    for n in names:
+        # the sum of two equal values is exact up to the first one's rounding
+        assert far(getattr(c.tb, n), 2 * once[n].double()) <= (2 ** -8 if dtype == "bf16" else 2 ** -23), n
+    assert torch.equal(c.tb.dx, dx)
+
+
+def test_frozen_router():
+    c = Case("bf16", 100, 128, 6, 3, 128, 3, 1.0, 1.0)
+    tb = c.backward()
+    full = tb.dx.double()
+    share = tb.dlogits.double() @ c.wr.double()
+    io = T.BackwardIO(x=c.x, w_router=None, logits=None, topk_idx=c.buf.topk_idx,
+                      topk_gate=c.buf.topk_gate, offsets=c.buf.offsets, perm=c.buf.perm,
+                      inv_perm=c.buf.inv_perm, w_gate=c.wg, w_up=c.wu, w_down=c.wd, dy=c.dy, dx=tb.dx,
+                      dgate=tb.dgate, dlogits=None, dw_router=None, dw_gate=tb.dw_gate, dw_up=tb.dw_up,
+                      dw_down=tb.dw_down)
+    T.moe_layer_backward(c.shape, io, tb.ws)
+    torch.cuda.synchronize()
+    assert far(tb.dx.double() + share, full) <= TOL["bf16"]
+
+
+def test_same_bits_again_on_another_stream_and_in_a_graph():
+    c = Case("bf16", 600, 256, 12, 6, 192, 4, 1.0, 1.0)
+    names = ("dx", "dgate", "dlogits", "dw_router", "dw_gate", "dw_up", "dw_down")
+    c.backward()
+    want = {n: getattr(c.tb, n).clone() for n in names}
+
+    def same(tag):
+        torch.cuda.synchronize()
+        for n in names:
+            assert torch.equal(getattr(c.tb, n), want[n]), (tag, n)
+            getattr(c.tb, n).fill_(7.0)
+        c.tb.ws.fill_(255)
+        torch.cuda.synchronize()
+
+    same("first")
+    c.backward()
+    same("again")
+    side = torch.cuda.Stream()
+    c.backward(stream=side)
+    same("stream")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        T.layer_backward(c.buf, c.tb, c.x, c.wr, c.wg, c.wu, c.wd, c.dy)
+    for k in range(3):
+        graph.replay()
+        same(f"replay {k}")
+
+
+@pytest.mark.parametrize("dtype,bits", [("f32", 32), ("bf16", 32), ("bf16", 8)])
+def test_training_steps_together(dtype, bits):
+    # forward, backward and AdamW by the library; each step's update is held
+    # against the step in 64 bits from that step's own gradients, and the
+    # gradients against automatic differentiation at that step's weights
+    c = Case(dtype, 96, 128, 6, 3, 128, 3, 1.0, 0.5)
+    ws = {"wr": "dw_router", "wg": "dw_gate", "wu": "dw_up", "wd": "dw_down"}
+    entries = []
+    for w, dw in ws.items():
+        p = getattr(c, w).view(-1)
+        n, nb = p.numel(), -(-p.numel() // 256)
+        z = lambda k=n: torch.zeros(k, device="cuda")  # noqa: E731
+        t = {"param": p, "grad": getattr(c.tb, dw).view(-1), "weight_decay": 0.1}
+        if dtype == "bf16":
+            t["master"] = p.float()
+        if bits == 32:
+            t.update(m=z(), v=z())
+        else:
+            t.update(m=z().to(torch.float8_e4m3fn), v=z().to(torch.float8_e4m3fn), m_scale=z(nb), v_scale=z(nb))
+        entries.append(t)
+    params, tensors, state = T.make_adamw_params(1e-3, state_bits=bits), T.AdamwTensors(entries), T.new_adamw_state()
+    for step in range(1, 4):
+        olds = [{k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in t.items()} for t in entries]
+        weights = {w: getattr(c, w).clone() for w in ws}
+        y, dx = T.train_step(c.buf, c.tb, c.x, c.wr, c.bias, c.wg, c.wu, c.wd, lambda y: c.dy, params, tensors,
+                             state, logit_bias=c.lb)
+        torch.cuda.synchronize()
+        assert int(state[0]) == step
+        new = {w: getattr(c, w).clone() for w in ws}
+        for w in ws:
+            getattr(c, w).copy_(weights[w])
+        ref = c.reference()
+        for w in ws:
+            getattr(c, w).copy_(new[w])
+        assert far(dx, ref["dx"]) <= TOL[dtype]
+        for (w, dw), old, t in zip(ws.items(), olds, entries):
+            assert far(getattr(c.tb, dw), ref[dw]) <= TOL[dtype], (step, w)
+            from tests.test_gpu_adamw import EPS, reference
+            old["grad"] = t["grad"]
+            p, _, _, up = reference(old, step, h=dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8))
+            got = (t["master"] if "master" in t else t["param"]).double()
+            assert ((got - p).abs() <= EPS * (p.abs() + up.abs() + got.abs())).all(), (step, w)
+
+
+def test_refusals():
+    c = Case("bf16", 20, 64, 3, 1, 64, 2)
+    small = torch.empty(64, dtype=torch.uint8, device="cuda")
+    io = dict(x=c.x, w_router=c.wr, logits=c.tb.logits, topk_idx=c.buf.topk_idx, topk_gate=c.buf.topk_gate,
+              offsets=c.buf.offsets, perm=c.buf.perm, inv_perm=c.buf.inv_perm, w_gate=c.wg, w_up=c.wu,
+              w_down=c.wd, dy=c.dy, dx=c.tb.dx, dgate=c.tb.dgate, dlogits=c.tb.dlogits,
+              dw_router=c.tb.dw_router, dw_gate=c.tb.dw_gate, dw_up=c.tb.dw_up, dw_down=c.tb.dw_down)
+    with pytest.raises(ValueError, match="ws"):
+        T.moe_layer_backward(c.shape, T.BackwardIO(**io), small)
+    for name in io:
+        t = io[name]
+        with pytest.raises(ValueError, match=name):
+            T.moe_layer_backward(c.shape, T.BackwardIO(**{**io, name: t.reshape(-1)[:-1]}), c.tb.ws)
+        with pytest.raises(ValueError, match=name):
+            T.moe_layer_backward(c.shape, T.BackwardIO(**{**io, name: t.double()}), c.tb.ws)
+    with pytest.raises(B.MoeError, match="EINVAL"):
+        T.moe_layer_backward(c.shape, T.BackwardIO(**{**io, "logits": None}), c.tb.ws)

@@ -1,0 +1,173 @@
+"""Host-side checks of the training operators: the library exports what
+moe_train.h declares, sizes its workspaces, and refuses bad arguments before
+it touches the GPU (no compute call is made here)."""
+
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+from sparse_moe_layer_03_amd import binding as B
+from sparse_moe_layer_03_amd import train as T
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, EINVAL, EUNSUPPORTED, EHIP, ENONFINITE, EALIGN = 0, -1, -2, -3, -4, -5
+A = 0x1000                                  # an aligned address that is never followed
+P = ctypes.c_void_p
+
+
+def header():
+    return open(os.path.join(ROOT, "include", "moe_train.h")).read()
+
+
+def test_library_exports_every_declared_symbol():
+    text = re.sub(r"/\*.*?\*/", "", header(), flags=re.S)
+    names = set(re.findall(r"^\s*[a-z_0-9]+\s*\*?\s*(moe_[a-z_]+)\s*\(", text, flags=re.M))
+    assert names == set(T.ENTRY_POINTS)
+    for path in (B.LIB_PATH, B.LIB_CHECKS_PATH):
+        L = ctypes.CDLL(path)
+        for n in names:
+            assert hasattr(L, n), (path, n)
+
+
+def test_struct_sizes_match_the_header(tmp_path):
+    src = tmp_path / "s.c"
+    src.write_text('#include <stdio.h>\n#include "moe_train.h"\nint main(void) { printf("%zu %zu %zu %zu %zu",'
+                   " sizeof(moe_gmm_shape), sizeof(moe_backward_io), sizeof(moe_adamw_params),"
+                   " sizeof(moe_adamw_tensor), sizeof(moe_adamw_state)); return 0; }\n")
+    exe = tmp_path / "s"
+    import subprocess
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True,
+                                          check=True).stdout.split()]
+    assert got == [ctypes.sizeof(c) for c in (T.MoeGmmShape, T.MoeBackwardIO, T.MoeAdamwParams,
+                                              T.MoeAdamwTensor)] + [16]
+
+
+def gmm(form="fwd", **kw):
+    s = T.make_gmm_shape("fwd", "bf16", 4, 16, 8, 24)
+    s.form = T.FORMS.get(form, form)
+    for k, v in kw.items():
+        setattr(s, k, v)
+    return s
+
+
+def call_gmm(s, offsets=A, lhs=A, rhs=A, out=A, ws=A):
+    return T.lib().moe_grouped_matmul(ctypes.byref(s), P(offsets), P(lhs), P(rhs), P(out), P(ws), None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(form=3), EINVAL), (dict(form=-1), EINVAL), (dict(n_groups=0), EINVAL), (dict(M=-1), EINVAL),
+    (dict(N=0), EINVAL), (dict(K=0), EINVAL), (dict(lda=23), EINVAL), (dict(ldc=7), EINVAL),
+    (dict(dtype=2), EUNSUPPORTED), (dict(out_dtype=5), EUNSUPPORTED),
+    (dict(dtype=B.MOE_F32, out_dtype=B.MOE_BF16), EUNSUPPORTED), (dict(n_groups=1025), EUNSUPPORTED),
+    (dict(K=(1 << 20) + 1, lda=(1 << 20) + 1), EUNSUPPORTED), (dict(lda=1 << 24), EUNSUPPORTED),
+])
+def test_grouped_matmul_refuses_bad_shapes(change, code):
+    s = gmm(**change)
+    assert call_gmm(s) == code
+    assert T.moe_grouped_matmul_workspace_bytes(s) == 0
+
+
+@pytest.mark.parametrize("form", ["fwd", "dx", "dw"])
+def test_grouped_matmul_refuses_null_and_misaligned_pointers(form):
+    s = gmm(form)
+    for name in ("offsets", "lhs", "rhs", "out"):
+        assert call_gmm(s, **{name: 0}) == EINVAL, name
+        assert call_gmm(s, **{name: A + 2}) == EALIGN, name
+    assert call_gmm(s, ws=A + 4) == EALIGN
+    assert T.lib().moe_grouped_matmul(None, *[P(A)] * 5, None) == EINVAL
+
+
+def shape(**kw):
+    a = dict(T=64, d_model=128, n_ffn=8, n_zero=4, d_ff=64, top_k=2, dtype="bf16")
+    a.update(kw)
+    return B.make_shape(*[a[k] for k in ("T", "d_model", "n_ffn", "n_zero", "d_ff", "top_k", "dtype")])
+
+
+def backward(s, ws=A, **change):
+    io = T.MoeBackwardIO(*[A] * len(T._IO_IN + T._IO_OUT), 0, 0)
+    for k, v in change.items():
+        setattr(io, k, v or None if k not in ("accumulate", "reserved") else v)
+    return T.lib().moe_layer_backward(ctypes.byref(s), ctypes.byref(io), P(ws), None)
+
+
+def test_layer_backward_refuses_bad_arguments():
+    s = shape()
+    for name in T._IO_IN + T._IO_OUT:
+        if name != "dlogits":
+            assert backward(s, **{name: 0}) == EINVAL, name
+        assert backward(s, **{name: A + 2}) == EALIGN, name
+    assert backward(s, ws=0) == EINVAL
+    assert backward(s, ws=A + 4) == EALIGN
+    assert backward(s, reserved=1) == EINVAL
+    # the router is there whole or not at all
+    assert backward(s, logits=0, w_router=0, dw_router=0) == EINVAL          # dlogits given
+    assert backward(s, logits=0, w_router=0, dlogits=0) == EINVAL
+    assert backward(shape(d_ff=100)) == EUNSUPPORTED
+    assert backward(shape(T=0)) == EINVAL
+    assert T.lib().moe_layer_backward(ctypes.byref(s), None, P(A), None) == EINVAL
+    assert T.moe_layer_backward_workspace_bytes(shape(T=0)) == 0
+    assert T.moe_layer_backward_workspace_bytes(s) > 0
+
+
+def adamw(params=None, n=1, state=A, grad_scale=None, lr_scale=None, bits=32, **change):
+    p = T.make_adamw_params(1e-3, state_bits=bits)
+    for k, v in (params or {}).items():
+        setattr(p, k, v)
+    t = T.MoeAdamwTensor(A, A, A, A, A, A, A, 100, 0, 0, 0.0)
+    for k, v in change.items():
+        setattr(t, k, v)
+    arr = (T.MoeAdamwTensor * 1)(t)
+    return T.lib().moe_adamw(ctypes.byref(p), arr, n, P(state), P(grad_scale), P(lr_scale), None)
+
+
+def test_adamw_refuses_bad_arguments():
+    nan, inf = float("nan"), float("inf")
+    for k in ("lr", "beta1", "beta2", "eps"):
+        assert adamw({k: nan}) == ENONFINITE, k
+        assert adamw({k: inf}) == ENONFINITE, k
+        assert adamw({k: -0.1}) == EINVAL, k
+    assert adamw({"beta1": 1.0}) == EINVAL
+    assert adamw({"eps": 0.0}) == EINVAL
+    assert adamw({"eps": 1e-60}) == EINVAL                  # zero in fp32
+    assert adamw({"state_bits": 16}) == EUNSUPPORTED
+    assert adamw(n=0) == EINVAL
+    assert adamw(state=0) == EINVAL
+    assert adamw(state=A + 4) == EALIGN
+    assert adamw(grad_scale=A + 2) == EALIGN
+    assert adamw(lr_scale=A + 2) == EALIGN
+    for k in ("param", "grad", "m", "v"):
+        assert adamw(**{k: None}) == EINVAL, k
+        assert adamw(**{k: A + 8}) == EALIGN, k
+    assert adamw(master=A + 4) == EALIGN
+    for k in ("m_scale", "v_scale"):
+        assert adamw(bits=8, **{k: None}) == EINVAL, k
+        assert adamw(bits=8, **{k: A + 2}) == EALIGN, k
+    assert adamw(n=1, weight_decay=nan) == ENONFINITE
+    assert adamw(weight_decay=-1.0) == EINVAL
+    assert adamw(param_dtype=2) == EUNSUPPORTED
+    assert adamw(grad_dtype=-1) == EUNSUPPORTED
+    t = (T.MoeAdamwTensor * 1)(T.MoeAdamwTensor(A, A, A, A, A, A, A, -1, 0, 0, 0.0))
+    p = T.make_adamw_params(1e-3)
+    assert T.lib().moe_adamw(ctypes.byref(p), t, 1, P(A), None, None, None) == EINVAL
+    t[0].n = 1 << 62
+    assert T.lib().moe_adamw(ctypes.byref(p), t, 1, P(A), None, None, None) == EUNSUPPORTED
+
+
+def test_binding_refuses_tensors_that_the_call_cannot_read():
+    s = T.make_gmm_shape("fwd", "bf16", 2, 4, 8, 8)
+    cpu = torch.zeros(64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="offsets"):
+        T.moe_grouped_matmul(s, torch.zeros(3, dtype=torch.int32), cpu, cpu, cpu)
+    with pytest.raises(ValueError, match="param"):
+        T.AdamwTensors([{"param": cpu, "grad": cpu, "m": cpu.float(), "v": cpu.float()}])
+    with pytest.raises(ValueError, match="no tensors"):
+        T.AdamwTensors([])
+    names = {n: None for n in T._IO_IN + T._IO_OUT}
+    with pytest.raises(ValueError, match="x:"):
+        T.BackwardIO(**names).check(shape())
+    with pytest.raises(ValueError, match="dtype"):
+        T.make_gmm_shape("fwd", torch.float16, 2, 4, 8, 8)
