@@ -129,7 +129,7 @@ int moe_layer_backward(const moe_shape* shape, const moe_backward_io* io, void* 
 typedef struct {
   double lr;           /* learning rate, >= 0                                */
   double beta1, beta2; /* decay of the moments, in [0, 1)                    */
-  double eps;          /* > 0                                                */
+  double eps;          /* >= 1e-30                                           */
   int32_t state_bits;  /* 32: fp32 moments; 8: e4m3 codes with block scales  */
   uint32_t seed;       /* of the 8-bit states' random rounding               */
 } moe_adamw_params;

@@ -19,11 +19,16 @@
 // mean of the square is kept, for a rounding that kept the root's mean would
 // raise v by the rounding's variance at every step.  Random bits: two rounds
 // of multiply and xor-shift ("lowbias32", C. Wellons) of the element's place.
+// What a code follows from (the moments, their largest, the comparison) is
+// computed operation by operation, each rounded by itself: contracted sums
+// would move one code in a million, and a code is an eighth of its value.
 
 #include <math.h>
 
 #include "common.h"
 #include "train.h"
+
+#pragma clang fp contract(off)
 
 namespace moe {
 
@@ -193,6 +198,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(AdamArgs a) {
   const float ic1 = s_c[0], ic2 = s_c[1];
   const uint32_t base = s_base;
   const float lr = a.lr_scale ? a.lr * *a.lr_scale : a.lr;
+  const float sic2 = sqrtf(ic2), lrc1 = lr * ic1;
   const uint32_t chunks = skip ? 0u : a.t[a.n_tensors - 1].chunk_end;
 
   int at = 0;
@@ -241,13 +247,21 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(AdamArgs a) {
       vk = a.b2 * vk + a.nb2 * gk * gk;
       m[k] = mk;
       v[k] = vk;
-      p[k] = p[k] * keep - lr * (mk * ic1) / (sqrtf(vk * ic2) + a.eps);
-      if (Q8) r[k] = sqrtf(vk);
+      // the update itself takes the hardware's root and reciprocal (an ulp each)
+      float root;
+      if (Q8) {
+        r[k] = sqrtf(vk);
+        root = r[k] * sic2;
+      } else {
+        root = __builtin_amdgcn_sqrtf(vk * ic2);
+      }
+      p[k] = p[k] * keep - (mk * lrc1) * __builtin_amdgcn_rcpf(root + a.eps);
     }
     if (Q8) {
       // elements behind the tensor's end are zeros here: they leave the top alone
       const float tm = block_top(m), tv = block_top(r);
-      const float im = tm > 0x1p-100f ? kQMax / tm : 0.f, iv = tv > 0x1p-100f ? kQMax / tv : 0.f;
+      const float im = tm > 0x1p-100f ? (1.f / tm) * kQMax : 0.f;
+      const float iv = tv > 0x1p-100f ? (1.f / tv) * kQMax : 0.f;
       const uint32_t key = mix32(base + (uint32_t)(a.first + at)) + (uint32_t)i +
                            0x9E3779B9u * (uint32_t)((uint64_t)i >> 32);
 #pragma unroll
@@ -260,8 +274,8 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(AdamArgs a) {
         store_codes((uint8_t*)w.m + i, left, m);
         store_codes((uint8_t*)w.v + i, left, r);
         if ((tid & 31) == 0) {
-          w.m_scale[blk] = tm / kQMax;
-          w.v_scale[blk] = tv / kQMax;
+          w.m_scale[blk] = tm * (1.f / kQMax);
+          w.v_scale[blk] = tv * (1.f / kQMax);
         }
       }
     } else if (left > 0) {

@@ -319,7 +319,7 @@ int moe_adamw(const moe_adamw_params* hp, const moe_adamw_tensor* tensors, int32
   if (!isfinite(hp->lr) || !isfinite(hp->beta1) || !isfinite(hp->beta2) || !isfinite(hp->eps))
     return MOE_ENONFINITE;
   if (hp->lr < 0 || hp->beta1 < 0 || hp->beta1 >= 1 || hp->beta2 < 0 || hp->beta2 >= 1 ||
-      !((float)hp->eps > 0.f))
+      (float)hp->eps < 1e-30f)
     return MOE_EINVAL;
   if (hp->state_bits != 32 && hp->state_bits != 8) return MOE_EUNSUPPORTED;
   if (!al16(state) || !al4(grad_scale) || !al4(lr_scale)) return MOE_EALIGN;
