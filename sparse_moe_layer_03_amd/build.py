@@ -23,7 +23,8 @@ OBJ_CHECKS = os.path.join(PKG, "_build_checks")
 ARCH = "gfx950"
 
 SOURCES = ["api.hip", "gemm.hip", "gemm_big.hip", "route.hip", "dispatch.hip", "combine.hip", "pid.hip",
-           "noalloc.hip", "eplb.hip", "train_api.hip", "gmm_general.hip", "layer_bwd.hip", "adamw.hip"]
+           "noalloc.hip", "eplb.hip", "train_api.hip", "gmm_general.hip",
+           "gmm_mfma.hip", "layer_bwd.hip", "adamw.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

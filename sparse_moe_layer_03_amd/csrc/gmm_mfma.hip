@@ -1,0 +1,617 @@
+// Grouped bf16 matrix products on bf16 MFMAs: forward, gradient of the rows,
+// gradient of the weights (the three forms of gmm_general.hip), for rows that
+// are multiples of 16 bytes.
+//
+// The operands differ from the forward layer's in how they lie in memory.  An
+// operand is RED when its reduction dimension is contiguous (a lane's 8
+// reduction values are one 16-byte chunk), OUT when its output dimension is:
+// the weights in the gradient of the rows, both operands in the gradient of
+// the weights.  OUT tiles are brought into LDS as they lie (64 reduction
+// rows, each the tile's width) and transposed on the way to the registers by
+// ds_read_b64_tr_b16: 16 lanes read 4 reduction rows x 16 columns and each
+// gets one column's 4 values; two reads make an MFMA operand.  No transposed
+// copy of the weights or rows exists anywhere.
+//
+//  * Tiles move HBM -> LDS with direct-to-LDS buffer loads.  Each tile (OUT:
+//    each step) has a descriptor that ends where the group's rows or the
+//    reduction end, and what lies behind reads as zero: ragged reductions,
+//    short tiles and refills past the end need no other masking.
+//  * LDS slots are swizzled through the global address a lane fetches: RED
+//    rows as in gemm_big.hip; OUT rows in 32-byte pairs of chunks, pair index
+//    XOR (row & 3 | row >> 1 & 4), so that the 8 rows half a wave reads lie
+//    on different banks.
+//  * Rings of two A and three B stages of 64 reduction values: one barrier a
+//    step, B two steps ahead, as in gemm_big.hip.
+//  * FWD, DX: a persistent grid walks over the groups' row tiles, which are
+//    balanced in height; only blocks of 16 rows that exist run MFMAs.  DW:
+//    one workgroup per tile, so that the hardware evens out hot experts;
+//    chunks of 32 neighbouring tiles go to one XCD and share its L2.
+
+#include <type_traits>
+
+#include "common.h"
+#include "train.h"
+
+namespace moe {
+
+typedef __attribute__((address_space(3))) void lds_void_t;
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+
+constexpr int kMfmaMaxGroups = 1024;
+constexpr uint32_t kOutside = 0x7ffffff0u;  // a buffer offset behind every descriptor's end
+enum { EPI_STORE = 0, EPI_SWIGLU = 1 };
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+}
+__device__ __forceinline__ void barrier_all() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ const char* uni(const char* p) {
+  const uint64_t v = (uint64_t)p;
+  const uint32_t lo = (uint32_t)uni((int)(uint32_t)v), hi = (uint32_t)uni((int)(v >> 32));
+  return (const char*)(((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t descriptor(const char* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, 0x00020000);
+}
+
+// Rows [lo, hi) of a group, inside [0, M] whatever the offsets hold.
+__device__ __forceinline__ void rows_of(const int32_t* offsets, int e, int M, int& lo, int& hi) {
+  lo = min(max(offsets[e], 0), M);
+  hi = min(max(offsets[e + 1], lo), M);
+}
+
+// One operand's tile geometry: W rows or columns of the output side.
+template <bool OUT, int W, int NW>
+struct Tile {
+  static constexpr int RB = OUT ? W * 2 : 128;   // bytes per LDS row
+  static constexpr int RPI = 1024 / RB;          // LDS rows per DMA instruction
+  static constexpr int PW = W / 8 / NW;          // DMA instructions per wave and step
+  static constexpr int BYTES = W * 128;
+  // Instructions q and q + P of a wave fetch the same chunks of rows that lie
+  // (P NW RPI) apart: their lane offsets differ by a wave-uniform amount.
+  static constexpr int P = OUT ? (NW * RPI >= 16 ? 1 : 16 / (NW * RPI)) : (NW >= 8 ? 1 : 8 / NW);
+  static constexpr int NP = P < PW ? P : PW;
+  static_assert(!OUT || W >= 128, "OUT tiles are 128 or 256 wide");
+  // LDS row and logical 16-byte chunk that lane `lane` of instruction q of
+  // wave `wave` fills
+  static __device__ __forceinline__ int row(int q, int wave, int lane) {
+    return (wave + q * NW) * RPI + lane / (RB / 16);
+  }
+  static __device__ __forceinline__ int chunk(int q, int wave, int lane) {
+    const int r = row(q, wave, lane), slot = lane % (RB / 16);
+    if (OUT) return slot ^ (flip(r) << 1);
+    return slot ^ ((r ^ (r >> 3)) & 7);
+  }
+  static __device__ __forceinline__ int flip(int r) { return (r & 3) | ((r >> 1) & 4); }
+  // Fragments: block b covers 16 outputs, slice kk 32 reduction values.  The
+  // block's wave-dependent part goes into the lane's base address, the rest
+  // (with no bit in common) into constants.
+  static __device__ __forceinline__ int lane_base(int lane, int b) {
+    const int l16 = lane & 15, l4 = lane >> 4;
+    if (OUT) {
+      const int r = l4 * 8 + (l16 >> 2);
+      return r * RB + ((b ^ flip(r)) << 5) + (l16 & 3) * 8;
+    }
+    // chunk (4 kk + l4) of row 16 b + l16, under the row's swizzle
+    const int s = (l16 ^ (l16 >> 3)) & 7;
+    return b * 2048 + l16 * 128 + ((l4 ^ s ^ ((2 * b) & 6)) << 4);
+  }
+  static __device__ __forceinline__ bf16x8_t frag(const char* s, int base, int b, int kk) {
+    if constexpr (OUT) {
+      const char* p = s + kk * 32 * RB + (base ^ (b << 5));
+      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)p);
+      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + 4 * RB));
+      return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      return *reinterpret_cast<const bf16x8_t*>(s + b * 2048 + (base ^ (((4 * kk) ^ ((2 * b) & 6)) << 4)));
+    }
+  }
+};
+
+__device__ __forceinline__ uint2 bf16x4(const f32x4_t& v) {
+  const uint32_t lo = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[0]) |
+                      ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[1]) << 16);
+  const uint32_t hi = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2]) |
+                      ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[3]) << 16);
+  return make_uint2(lo, hi);
+}
+
+template <int FORM, int EPI, typename TO, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN, 2)
+gmm_mfma_kernel(MfmaArgs g) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int NW = WM * WN, NT = 64 * NW;
+  constexpr bool DW = FORM == MOE_GMM_DW, SW = EPI == EPI_SWIGLU;
+  using TA = Tile<DW, BM, NW>;
+  using TB = Tile<FORM != MOE_GMM_FWD, BN, NW>;
+  constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
+  constexpr int A_PW = TA::PW, B_PW = TB::PW;
+  constexpr int HN = SW ? BN / 2 : BN;  // output columns per tile
+  constexpr int MG = 4;
+  static_assert(A_PW >= 1 && B_PW >= 1 && (!SW || (NB % 2 == 0 && B_PW % 2 == 0)), "tile");
+
+  // one array per stage: the compiler then sees that the stage being read is
+  // not one being filled
+  __shared__ __attribute__((aligned(1024))) char s_a0[TA::BYTES];
+  __shared__ __attribute__((aligned(1024))) char s_a1[TA::BYTES];
+  __shared__ __attribute__((aligned(1024))) char s_b0[TB::BYTES];
+  __shared__ __attribute__((aligned(1024))) char s_b1[TB::BYTES];
+  __shared__ __attribute__((aligned(1024))) char s_b2[TB::BYTES];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = uni(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int l16 = lane & 15, l4 = lane >> 4;
+  // DW: a wave's row blocks are one stretch; else they interleave with the
+  // other waves', so that a short tile loads all of them
+  const int a_lane = TA::lane_base(lane, DW ? wm * MB : wm);
+  const int b_lane = TB::lane_base(lane, SW ? wn * (NB / 2) : wn * NB);
+
+  const int G = gridDim.x, bid = blockIdx.x;
+  const int jt = DW ? 1 : (g.s[0].J + HN - 1) / HN;
+  // FWD, DX: tiles that run together on an XCD are neighbours
+  const int vid = (!DW && G % 8 == 0) ? (bid % 8) * (G / 8) + bid / 8 : bid;
+
+  // FWD, DX: (first row tile << 10 | group) of this workgroup's next 64 tiles,
+  // one per lane, and the number of tiles
+  uint32_t desc = 0;
+  long tiles = 0;
+  auto describe = [&](int k0) {
+    int* s_pref = reinterpret_cast<int*>(s_a0);
+    int* s_scan = reinterpret_cast<int*>(s_a1);
+    constexpr int PER = (kMfmaMaxGroups + NT - 1) / NT;
+    int loc[PER], run = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int e = tid * PER + k;
+      if (e < g.ngroups) {
+        int lo, hi;
+        rows_of(g.offsets, e, g.M, lo, hi);
+        run += (hi - lo + BM - 1) / BM;
+      }
+      loc[k] = run;
+    }
+    const int base = block_inclusive_scan<NT>(run, s_scan) - run;
+    if (tid == 0) s_pref[0] = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+      if (tid * PER + k < g.ngroups) s_pref[tid * PER + k + 1] = base + loc[k];
+    __syncthreads();
+    tiles = (long)uni(s_pref[g.ngroups]) * jt;
+    const long t = (vid + (long)(k0 + lane) * G) / g.nsplit;
+    desc = 0;
+    if (t < tiles) {
+      const int m = (int)(t / jt);
+      int lo = 0, hi = g.ngroups - 1;  // last group with s_pref <= m
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_pref[mid] <= m) lo = mid; else hi = mid - 1;
+      }
+      desc = ((uint32_t)s_pref[lo] << 10) | (uint32_t)lo;
+    }
+    __syncthreads();
+  };
+
+  for (int k = 0;; ++k) {
+    int e, i0, i_end, j0, split = 0;
+    long row0;
+    int rows;
+    GmmSub sub = g.s[0];
+    if constexpr (DW) {
+      if (k > 0) break;
+      // chunks of 32 tiles deal over the XCDs (workgroup b runs on XCD b % 8)
+      const int x = bid % 8, y = bid / 8;
+      long t = ((long)(y / 32) * 8 + x) * 32 + y % 32;
+      split = (int)(t % g.nsplit);
+      t /= g.nsplit;
+      auto count = [](const GmmSub& s) { return ((s.I + BM - 1) / BM) * ((s.J + BN - 1) / BN); };
+      const int per_group = count(g.s[0]) + (g.nsub > 1 ? count(g.s[1]) : 0) +
+                            (g.nsub > 2 ? count(g.s[2]) : 0);
+      if (t >= (long)per_group * g.ngroups) break;
+      e = (int)(t / per_group);
+      int local = (int)(t - (long)e * per_group);
+      const int n0 = count(g.s[0]);
+      if (local >= n0) {
+        local -= n0;
+        sub = g.s[1];
+        const int n1 = g.nsub > 1 ? count(g.s[1]) : 0;
+        if (local >= n1) {
+          local -= n1;
+          sub = g.s[2];
+        }
+      }
+      const int nj = (sub.J + BN - 1) / BN;
+      // bands of 4 rows of tiles, column by column
+      const int ni = (sub.I + BM - 1) / BM;
+      const int band = local / (4 * nj), in = local - band * 4 * nj;
+      const int high = min(4, ni - band * 4);
+      i0 = (band * 4 + in % high) * BM;
+      j0 = (in / high) * BN;
+      i_end = min(sub.I, i0 + BM);
+      int lo, hi;
+      rows_of(g.offsets, e, g.M, lo, hi);
+      row0 = lo;
+      rows = hi - lo;
+    } else {
+      if ((k & 63) == 0) {
+        if (k > 0) {  // every wave is done with the last tile's stages
+          wait_vm<0>();
+          __syncthreads();
+        }
+        describe(k);
+      }
+      const long item = vid + (long)k * G;
+      if (item >= tiles * g.nsplit) break;
+      const long t = item / g.nsplit;
+      split = (int)(item - t * g.nsplit);
+      const uint32_t d = (uint32_t)__builtin_amdgcn_readlane((int)desc, k & 63);
+      e = (int)(d & 1023u);
+      int lo, hi;
+      rows_of(g.offsets, e, g.M, lo, hi);
+      row0 = lo;
+      rows = hi - lo;
+      // in a group: bands of MG row tiles, column by column, so that tiles
+      // that run together share row and weight slices in L2
+      const int mt = (rows + BM - 1) / BM;
+      const int local = (int)(t - (long)(d >> 10) * jt);
+      const int m0 = (local / (MG * jt)) * MG;
+      const int mg = max(1, min(MG, mt - m0));
+      const int in = local - m0 * jt;
+      j0 = (in / mg) * HN;
+      const int h = ((rows + mt - 1) / mt + 15) & ~15;  // balanced height
+      i0 = (m0 + in % mg) * h;
+      i_end = min(rows, i0 + h);
+    }
+    e = uni(e), i0 = uni(i0), i_end = uni(i_end), j0 = uni(j0), split = uni(split), rows = uni(rows);
+    row0 = uni((int)row0);
+    const int R = DW ? rows : g.R;
+    const int steps = (R + 63) >> 6;
+    const int per = (steps + g.nsplit - 1) / g.nsplit;
+    const int k_lo = min(split * per, steps), k_hi = min(steps, k_lo + per);
+    const int r_end = min(R, k_hi * 64);  // reduction of this item: [64 k_lo, r_end)
+    const int J = sub.J;
+    const uint32_t lda2 = (uint32_t)sub.lda * 2, ldb2 = (uint32_t)sub.ldb * 2;
+
+    // ---- where the tiles come from
+    const char* a_base;
+    uint32_t a_bytes = 0;  // RED: the tile's; OUT: a row's part
+    if constexpr (DW) {
+      a_base = (const char*)sub.a + row0 * (int64_t)lda2 + (int64_t)i0 * 2;
+      a_bytes = (uint32_t)min(BM, ((sub.I + 7) & ~7) - i0) * 2;
+    } else {
+      a_base = (const char*)sub.a + (row0 + i0) * (int64_t)lda2;
+      a_bytes = i_end > i0 ? (uint32_t)(i_end - i0 - 1) * lda2 + (uint32_t)g.R * 2 : 0u;
+    }
+    a_base = uni(a_base);
+    const char* b_base;
+    const char* b_base2 = nullptr;
+    uint32_t b_bytes;
+    if constexpr (FORM == MOE_GMM_FWD) {
+      const int64_t at = ((int64_t)e * g.b_group + (int64_t)j0 * sub.ldb) * 2;
+      b_base = uni((const char*)sub.b + at);
+      if (SW) b_base2 = uni((const char*)g.b2 + at);
+      b_bytes = (uint32_t)(min(HN, J - j0) - 1) * ldb2 + (uint32_t)g.R * 2;
+    } else {
+      const int64_t at = (FORM == MOE_GMM_DX ? (int64_t)e * g.b_group * 2 : row0 * (int64_t)ldb2) +
+                         (int64_t)j0 * 2;
+      b_base = uni((const char*)sub.b + at);
+      if (FORM == MOE_GMM_DX && g.r_switch) b_base2 = uni((const char*)g.b2 + at);
+      b_bytes = (uint32_t)min(BN, J - j0) * 2;
+    }
+    // lane offsets of the first instructions of each kind
+    uint32_t a_off[TA::NP], b_off[TB::NP];
+#pragma unroll
+    for (int q = 0; q < TA::NP; ++q)
+      a_off[q] = (uint32_t)TA::row(q, wave, lane) * lda2 + TA::chunk(q, wave, lane) * 16;
+#pragma unroll
+    for (int q = 0; q < TB::NP; ++q)
+      b_off[q] = (uint32_t)TB::row(q, wave, lane) * ldb2 + TB::chunk(q, wave, lane) * 16;
+    // and what instruction q adds to them
+    auto a_add = [&](int q) { return (int)((uint32_t)(q - q % TA::NP) * (NW * TA::RPI) * lda2); };
+    auto b_add = [&](int q) {
+      // SwiGLU step: gate rows fill the first half of the tile, up rows the second
+      const int h = (SW && q >= B_PW / 2) ? q - B_PW / 2 : q;
+      return (int)((uint32_t)(h - h % TB::NP) * (NW * TB::RPI) * ldb2);
+    };
+
+    f32x4_t acc[MB][NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    auto stage_a = [&](auto sc) -> char* { return decltype(sc)::value == 0 ? s_a0 : s_a1; };
+    auto stage_b = [&](auto sc) -> char* {
+      constexpr int S = decltype(sc)::value;
+      return S == 0 ? s_b0 : S == 1 ? s_b1 : s_b2;
+    };
+    // rows of an OUT tile's step that exist
+    auto left_of = [&](int ks, int end) { return min(64, max(0, end - ks * 64)); };
+    auto load_a = [&](auto sc, int ks, int q) {
+      char* dst = stage_a(sc) + (wave + q * NW) * 1024;
+      if constexpr (DW) {
+        const int left = left_of(ks, r_end);
+        const auto rs = descriptor(a_base + (int64_t)ks * 64 * lda2,
+                                   left > 0 ? (uint32_t)(left - 1) * lda2 + a_bytes : 0u);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)a_off[q % TA::NP],
+                                                 a_add(q), 0, 0);
+      } else {
+        const auto rs = descriptor(a_base, a_bytes);
+        const int left = r_end - ks * 64;
+        uint32_t off = a_off[q % TA::NP];
+        if (left < 64) off = TA::chunk(q, wave, lane) * 8 < left ? off : kOutside;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)off,
+                                                 ks * 128 + a_add(q), 0, 0);
+      }
+    };
+    auto load_b = [&](auto sc, int ks, int q) {
+      char* dst = stage_b(sc) + (wave + q * NW) * 1024;
+      if constexpr (FORM == MOE_GMM_FWD) {
+        const auto rs = descriptor((SW && q >= B_PW / 2) ? b_base2 : b_base, b_bytes);
+        const int left = r_end - ks * 64;
+        uint32_t off = b_off[q % TB::NP];
+        if (left < 64) off = TB::chunk(q, wave, lane) * 8 < left ? off : kOutside;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)off,
+                                                 ks * 128 + b_add(q), 0, 0);
+      } else {
+        int left = left_of(ks, FORM == MOE_GMM_DX ? min(r_end, g.RB) : r_end), r = ks * 64;
+        const char* base = b_base;
+        if (FORM == MOE_GMM_DX && g.r_switch && r >= g.r_switch) {
+          base = b_base2;
+          r -= g.r_switch;
+        }
+        const auto rs = descriptor(base + (int64_t)r * ldb2,
+                                   left > 0 ? (uint32_t)(left - 1) * ldb2 + b_bytes : 0u);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)b_off[q % TB::NP],
+                                                 b_add(q), 0, 0);
+      }
+    };
+
+    // One step on stages (AS, BS) with MBA active row blocks: its own loads
+    // have landed when at most the next step's B loads are outstanding.
+    auto step = [&](auto mbac, auto asc, auto bsc, int ks) {
+      constexpr int MBA = decltype(mbac)::value;
+      constexpr int AS = decltype(asc)::value, BS = decltype(bsc)::value;
+      const char* sa = stage_a(asc);
+      const char* sb = stage_b(bsc);
+      wait_vm<B_PW>();
+      barrier_all();
+      using NA = std::integral_constant<int, (AS + 1) % 2>;
+      using NBS = std::integral_constant<int, (BS + 2) % 3>;
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        bf16x8_t fa[MBA], fb[NB];
+#pragma unroll
+        for (int i = 0; i < MBA; ++i) fa[i] = TA::frag(sa, a_lane, DW ? i : i * WM, kk);
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+          fb[j] = TB::frag(sb, b_lane, SW && j >= NB / 2 ? BN / 32 + j - NB / 2 : j, kk);
+        if (kk == 0) {
+#pragma unroll
+          for (int q = 0; q < A_PW; ++q) load_a(NA{}, ks + 1, q);
+        } else {
+#pragma unroll
+          for (int q = 0; q < B_PW; ++q) load_b(NBS{}, ks + 2, q);
+        }
+#pragma unroll
+        for (int i = 0; i < MBA; ++i)
+#pragma unroll
+          for (int j = 0; j < NB; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      __builtin_amdgcn_s_setprio(0);
+    };
+
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    auto loop = [&](auto mbac) {
+      // the last tile's reads and stores are done before its stages are
+      // filled and before vmcnt counts this tile's loads
+      wait_vm<0>();
+      barrier_all();
+#pragma unroll
+      for (int q = 0; q < A_PW; ++q) load_a(I0{}, k_lo, q);
+#pragma unroll
+      for (int q = 0; q < B_PW; ++q) load_b(I0{}, k_lo, q);
+#pragma unroll
+      for (int q = 0; q < B_PW; ++q) load_b(I1{}, k_lo + 1, q);
+      for (int ks = k_lo; ks < k_hi; ks += 6) {
+        step(mbac, I0{}, I0{}, ks);
+        if (ks + 1 >= k_hi) break;
+        step(mbac, I1{}, I1{}, ks + 1);
+        if (ks + 2 >= k_hi) break;
+        step(mbac, I0{}, I2{}, ks + 2);
+        if (ks + 3 >= k_hi) break;
+        step(mbac, I1{}, I0{}, ks + 3);
+        if (ks + 4 >= k_hi) break;
+        step(mbac, I0{}, I1{}, ks + 4);
+        if (ks + 5 >= k_hi) break;
+        step(mbac, I1{}, I2{}, ks + 5);
+      }
+    };
+    if constexpr (DW || MB == 1) {
+      loop(std::integral_constant<int, MB>{});
+    } else {
+      // row blocks of this wave that hold rows (a wave without any still
+      // loads and waits with the others, on one block that is not stored)
+      const int nrb = (i_end - i0 + 15) / 16;
+      const int mba = min(MB, (nrb - wm + WM - 1) / WM);
+      if (mba >= 4 && MB >= 4) loop(std::integral_constant<int, MB >= 4 ? 4 : MB>{});
+      else if (mba == 3 && MB >= 3) loop(std::integral_constant<int, MB >= 3 ? 3 : MB>{});
+      else if (mba == 2) loop(std::integral_constant<int, 2>{});
+      else loop(std::integral_constant<int, 1>{});
+    }
+
+    // ---- out.  b was the MFMA's row operand: lane (l16, l4) holds columns
+    // 4 l4 .. 4 l4 + 3 of row l16 of a 16 x 16 block.
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      const int ii = i0 + (DW ? wm * MB + i : i * WM + wm) * 16 + l16;
+      if constexpr (SW) {
+        // z, u -> h, dz, du, and this wave's part of <dh, h>
+        const bool live = ii < i_end;
+        const long p = row0 + min(ii, rows - 1);
+        const int at = g.perm[p];
+        const float gt = (unsigned)at < (unsigned)g.M ? g.gate[at] : 0.f;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < NB / 2; ++j) {
+          const int jj = j0 + (wn * (NB / 2) + j) * 16 + l4 * 4;
+          if (!live || jj >= J) continue;  // J is a multiple of 64 here
+          const f32x4_t dh = *reinterpret_cast<const f32x4_t*>(g.dh + p * J + jj);
+          f32x4_t dz, du, hs;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float z = acc[i][j][v], u = acc[i][j + NB / 2][v];
+            const float sg = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504f));
+            const float si = z * sg, h = si * u, d = gt * dh[v];
+            sum += dh[v] * h;
+            dz[v] = d * u * (sg * (1.f + z * (1.f - sg)));
+            du[v] = d * si;
+            hs[v] = gt * h;
+          }
+          char* o = (char*)g.dzu + (p * 2 * J + jj) * 2;
+          *reinterpret_cast<uint2*>(o) = bf16x4(dz);
+          *reinterpret_cast<uint2*>(o + (int64_t)J * 2) = bf16x4(du);
+          *reinterpret_cast<uint2*>((char*)g.hs + (p * J + jj) * 2) = bf16x4(hs);
+        }
+        sum += __shfl_xor(sum, 16, kWave);
+        sum += __shfl_xor(sum, 32, kWave);
+        if (live && l4 == 0)
+          g.dpart[p * (long)(((J + HN - 1) / HN) * WN) + (j0 / HN) * WN + wn] = sum;
+      } else {
+        asm volatile("" ::: "memory");  // one row block's old values at a time
+        if (ii >= i_end) continue;
+        const long orow = DW ? (long)e * g.out_group + (long)ii * sub.ldo : (row0 + ii) * sub.ldo;
+        const long prow = (DW ? (long)e * sub.I + ii : row0 + ii) * J;
+        const int jj0 = j0 + wn * NB * 16 + l4 * 4;
+        if (g.nsplit > 1) {
+          float* p = g.part + split * g.part_stride + prow + jj0;
+#pragma unroll
+          for (int j = 0; j < NB; ++j)
+            if (jj0 + j * 16 < J) *reinterpret_cast<f32x4_t*>(p + j * 16) = acc[i][j];
+          continue;
+        }
+        TO* p = (TO*)sub.out + orow + jj0;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          if (jj0 + j * 16 >= J) continue;
+          f32x4_t v = acc[i][j];
+          if (g.accumulate) {
+            if constexpr (sizeof(TO) == 4) {
+              v += *reinterpret_cast<const f32x4_t*>(p + j * 16);
+            } else {
+              const uint2 old = *reinterpret_cast<const uint2*>(p + j * 16);
+              const f32x4_t w = {__uint_as_float(old.x << 16), __uint_as_float(old.x & 0xffff0000u),
+                                 __uint_as_float(old.y << 16), __uint_as_float(old.y & 0xffff0000u)};
+              v += w;
+            }
+          }
+          if constexpr (sizeof(TO) == 4) *reinterpret_cast<f32x4_t*>(p + j * 16) = v;
+          else *reinterpret_cast<uint2*>(p + j * 16) = bf16x4(v);
+        }
+      }
+    }
+  }
+#endif
+}
+
+bool mfma_ok(int form, int dtype, int N, int K, int64_t lda, int64_t ldc) {
+  if (dtype != MOE_BF16 || K % 8 != 0 || lda % 8 != 0) return false;
+  // a descriptor spans at most 256 rows
+  if (lda >= (1 << 21) || ldc >= (1 << 21)) return false;
+  return form == MOE_GMM_FWD ? N % 4 == 0 && ldc % 4 == 0 : N % 8 == 0 && ldc % 8 == 0;
+}
+
+template <int FORM, int EPI, typename TO, int BM, int BN, int WM, int WN>
+static int launch_tile(const MfmaArgs& g, hipStream_t st) {
+  const int cus = stream_cu_count(st);
+  if (cus <= 0) return MOE_EHIP;
+  constexpr bool DW = FORM == MOE_GMM_DW;
+  constexpr int HN = EPI == EPI_SWIGLU ? BN / 2 : BN;
+  long grid;
+  if (DW) {
+    long t = 0;
+    for (int q = 0; q < g.nsub; ++q)
+      t += (long)((g.s[q].I + BM - 1) / BM) * ((g.s[q].J + BN - 1) / BN);
+    t *= (long)g.ngroups * g.nsplit;
+    grid = (t + 255) / 256 * 256;  // whole rounds of 8 XCDs x 32 tiles
+  } else {
+    const long most = (long)(g.M / BM + (g.M < g.ngroups ? g.M : g.ngroups)) *
+                      ((g.s[0].J + HN - 1) / HN) * g.nsplit;
+    constexpr int LDS = BM * 256 + BN * 384;
+    grid = (long)cus * (160 * 1024 / LDS < 2 ? 1 : 2);
+    if (grid > most) grid = most;
+    if (grid > 8) grid -= grid % 8;
+  }
+  if (grid < 1) return MOE_OK;
+  if (grid > 0x7fffffffl) return MOE_EUNSUPPORTED;
+  hipLaunchKernelGGL((gmm_mfma_kernel<FORM, EPI, TO, BM, BN, WM, WN>), dim3((unsigned)grid),
+                     dim3(64 * WM * WN), 0, st, g);
+  return check_launch();
+}
+
+// Tile choice: by the rows a group has on average (FWD, DX) and whether the
+// larger tiles fill the chip.
+template <int FORM, typename TO>
+static int launch_form(const MfmaArgs& g, hipStream_t st) {
+  const int cus = stream_cu_count(st);
+  if (cus <= 0) return MOE_EHIP;
+  if constexpr (FORM == MOE_GMM_DW) {
+    long t = 0;
+    for (int q = 0; q < g.nsub; ++q)
+      t += (long)((g.s[q].I + 255) / 256) * ((g.s[q].J + 255) / 256);
+    if (t * g.ngroups * g.nsplit >= cus)
+      return launch_tile<FORM, EPI_STORE, TO, 256, 256, 4, 2>(g, st);
+    return launch_tile<FORM, EPI_STORE, TO, 128, 128, 2, 2>(g, st);
+  }
+  else {
+    const long per = g.M / g.ngroups;
+    const long t256 = (g.M / 256 + (g.M < g.ngroups ? g.M : g.ngroups)) * ((g.s[0].J + 255) / 256);
+    if (per >= 128 && t256 * g.nsplit >= cus)
+      return launch_tile<FORM, EPI_STORE, TO, 256, 256, 4, 2>(g, st);
+    if (per >= 48) return launch_tile<FORM, EPI_STORE, TO, 128, 128, 2, 2>(g, st);
+    return launch_tile<FORM, EPI_STORE, TO, 64, 128, 1, 4>(g, st);
+  }
+}
+
+int launch_gmm_mfma(int form, int out_dtype, const MfmaArgs& g, hipStream_t st) {
+  const bool f32 = out_dtype == MOE_F32;
+  if (form == MOE_GMM_FWD)
+    return f32 ? launch_form<MOE_GMM_FWD, float>(g, st) : launch_form<MOE_GMM_FWD, __bf16>(g, st);
+  if (form == MOE_GMM_DX)
+    return f32 ? launch_form<MOE_GMM_DX, float>(g, st) : launch_form<MOE_GMM_DX, __bf16>(g, st);
+  return f32 ? launch_form<MOE_GMM_DW, float>(g, st) : launch_form<MOE_GMM_DW, __bf16>(g, st);
+}
+
+// Rows per expert decide the tile, as for the other products; the partial
+// sums of dgate per row follow from it.
+static int swiglu_tile(int M, int ngroups) {
+  const int per = M / ngroups;
+  return per >= 128 ? 256 : per >= 48 ? 128 : 64;
+}
+
+int swiglu_parts(int M, int ngroups, int f) {
+  const int tile = swiglu_tile(M, ngroups);
+  return tile == 256 ? ((f + 127) / 128) * 2 : ((f + 63) / 64) * (tile == 128 ? 2 : 4);
+}
+
+int launch_swiglu_mfma(const MfmaArgs& g, hipStream_t st) {
+  const int tile = swiglu_tile(g.M, g.ngroups);
+  if (tile == 256) return launch_tile<MOE_GMM_FWD, EPI_SWIGLU, __bf16, 256, 256, 4, 2>(g, st);
+  if (tile == 128) return launch_tile<MOE_GMM_FWD, EPI_SWIGLU, __bf16, 128, 128, 2, 2>(g, st);
+  return launch_tile<MOE_GMM_FWD, EPI_SWIGLU, __bf16, 64, 128, 1, 4>(g, st);
+}
+
+}  // namespace moe

@@ -33,6 +33,46 @@ struct GmmArgs {
 // 16-byte aligned.
 int launch_gmm_general(int form, int dtype, int out_dtype, bool vec, const GmmArgs& g,
                        hipStream_t st);
+// bf16 products on bf16 MFMAs (gmm_mfma.hip).  Up to three products over the
+// same groups in one launch (DW only; else one).
+struct GmmSub {
+  const void* a;
+  const void* b;
+  void* out;
+  int64_t lda, ldb, ldo;
+  int I, J;
+};
+struct MfmaArgs {
+  GmmSub s[3];
+  int nsub;
+  int ngroups;
+  const int32_t* offsets;
+  int M;
+  int R;                 // FWD, DX: length of the reduction
+  int RB;                // DX: rows that a group of b holds (<= R; zeros behind)
+  int r_switch;          // DX: reduction rows from here on come from b2 (0: none)
+  const void* b2;        // DX: see r_switch; SwiGLU step: w_up
+  int64_t b_group, out_group;
+  float* part;
+  int64_t part_stride;
+  int nsplit;
+  int accumulate;
+  // SwiGLU's backward step (FWD): z = a b^T, u = a b2^T
+  const int32_t* perm;
+  const float* gate;
+  const float* dh;       // [rows, J] fp32
+  void* dzu;             // [rows, 2 J]
+  void* hs;              // [rows, J]
+  float* dpart;          // [rows, swiglu_parts()]
+};
+constexpr int kMfmaMaxRows = 1 << 29;  // row tiles are counted in 22 bits
+// Whether a product can run there: 16-byte rows and row starts, and sizes
+// that 32-bit offsets within a tile reach.
+bool mfma_ok(int form, int dtype, int N, int K, int64_t lda, int64_t ldc);
+int launch_gmm_mfma(int form, int out_dtype, const MfmaArgs& g, hipStream_t st);
+int launch_swiglu_mfma(const MfmaArgs& g, hipStream_t st);
+int swiglu_parts(int M, int ngroups, int f);  // partial sums of dgate per row
+
 // Sums `part` into out (rounded, added to when accumulating).
 int launch_gmm_join(int form, int out_dtype, const GmmArgs& g, hipStream_t st);
 

@@ -55,12 +55,37 @@ static size_t gmm_part_bytes(const moe_gmm_shape* s, int nsplit) {
   return up256(out * nsplit * sizeof(float));
 }
 
-// Runs one product, its split reduction joined.
-static int run_gmm(int form, int dtype, int out_dtype, const GmmArgs& g, hipStream_t st) {
-  const int es = elem_size(dtype);
-  const bool vec = g.lda % 4 == 0 && g.ldb % 4 == 0 && g.b_group % 4 == 0 && al16(g.a) && al16(g.b) &&
-                   es > 0;
-  int rc = launch_gmm_general(form, dtype, out_dtype, vec, g, st);
+// Runs one product, its split reduction joined.  rb: rows that a group of b
+// holds (DX), when fewer than the reduction's length.
+static int run_gmm(int form, int dtype, int out_dtype, const GmmArgs& g, hipStream_t st, int rb = 0) {
+  const bool dw = form == MOE_GMM_DW;
+  const int64_t lda = form == MOE_GMM_DX ? g.ldo : dw ? g.ldb : g.lda;
+  const int64_t ldc = form == MOE_GMM_FWD ? g.ldo : g.lda;
+  // DW loads whole chunks of c's rows: a row's gap holds what a chunk has
+  // beyond N when the caller says so (rb)
+  const int N = form == MOE_GMM_FWD ? g.J : dw ? (rb ? rb : g.I) : g.R;
+  const int K = form == MOE_GMM_FWD ? g.R : g.J;
+  int rc;
+  if (g.M < kMfmaMaxRows && mfma_ok(form, dtype, N, K, lda, ldc) && al16(g.a) && al16(g.b) && al16(g.out)) {
+    MfmaArgs m{};
+    m.s[0] = {g.a, g.b, g.out, g.lda, g.ldb, g.ldo, g.I, g.J};
+    m.nsub = 1;
+    m.ngroups = g.ngroups;
+    m.offsets = g.offsets;
+    m.M = g.M;
+    m.R = g.R;
+    m.RB = form == MOE_GMM_DX && rb ? rb : g.R;
+    m.b_group = g.b_group;
+    m.out_group = g.out_group;
+    m.part = g.part;
+    m.part_stride = g.part_stride;
+    m.nsplit = g.nsplit;
+    m.accumulate = g.accumulate;
+    rc = launch_gmm_mfma(form, out_dtype, m, st);
+  } else {
+    const bool vec = g.lda % 4 == 0 && g.ldb % 4 == 0 && g.b_group % 4 == 0 && al16(g.a) && al16(g.b);
+    rc = launch_gmm_general(form, dtype, out_dtype, vec, g, st);
+  }
   if (rc || g.nsplit <= 1) return rc;
   return launch_gmm_join(form, out_dtype, g, st);
 }
@@ -71,7 +96,8 @@ constexpr int kRouteSplits = 16;  // token ranges of the router's weight gradien
 
 struct BwdLayout {
   size_t xp, dyp, zu, dh, dzu, hs, part, dl, offs, dxr, drp, total;
-  int ep, nsplit;
+  int ep, nsplit, parts;
+  bool mfma;  // the bf16 kernels, with SwiGLU's step in the products' epilogue
 };
 
 static BwdLayout bwd_layout(const moe_shape* s) {
@@ -81,6 +107,9 @@ static BwdLayout bwd_layout(const moe_shape* s) {
   BwdLayout w;
   w.ep = (int)((E + 7) & ~(size_t)7);
   w.nsplit = (int)std::max(1l, std::min((long)kRouteSplits, (long)s->T / 256));
+  w.mfma = s->dtype == MOE_BF16 && s->d_model < (1 << 20) && s->d_ff < (1 << 20) &&
+           rows < kMfmaMaxRows;
+  w.parts = w.mfma ? swiglu_parts((int)rows, s->n_ffn, s->d_ff) : 1;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -89,11 +118,11 @@ static BwdLayout bwd_layout(const moe_shape* s) {
   };
   w.xp = take(rows * d * es);
   w.dyp = take(rows * d * es);
-  w.zu = take(rows * 2 * f * 4);
+  w.zu = take(w.mfma ? 0 : rows * 2 * f * 4);
   w.dh = take(rows * f * 4);
   w.dzu = take(rows * 2 * f * es);
   w.hs = take(rows * f * es);
-  w.part = take(rows * 4);
+  w.part = take(rows * w.parts * 4);
   w.dl = take((size_t)s->T * w.ep * es);
   w.offs = take((2 + kRouteSplits + 1) * sizeof(int32_t));
   w.dxr = take((size_t)s->T * d * 4);
@@ -234,24 +263,57 @@ int moe_layer_backward(const moe_shape* s, const moe_backward_io* io, void* ws, 
     g.accumulate = accumulate;
     return run_gmm(form, dt, out_dtype, g, st);
   };
-  // z and u again, and the gradient at H
-  if ((rc = product(MOE_GMM_FWD, MOE_F32, xp, d, io->w_gate, d, zu, 2 * f, 0, f, d, 0))) return rc;
-  if ((rc = product(MOE_GMM_FWD, MOE_F32, xp, d, io->w_up, d, zu + f, 2 * f, 0, f, d, 0))) return rc;
-  if ((rc = product(MOE_GMM_DX, MOE_F32, dyp, d, io->w_down, f, dh, f, 0, f, d, 0))) return rc;
-  if ((rc = launch_swiglu_bwd(dt, zu, dh, io->perm, io->topk_gate, io->offsets, s->n_ffn, Tk, f,
-                              dzu, hs, part, st)))
-    return rc;
-  // gradients of the experts' weights
   const int acc = io->accumulate != 0;
-  if ((rc = product(MOE_GMM_DW, dt, dzu, 2 * f, xp, d, io->dw_gate, d, f, d, 0, acc))) return rc;
-  if ((rc = product(MOE_GMM_DW, dt, dzu + (size_t)f * es, 2 * f, xp, d, io->dw_up, d, f, d, 0, acc)))
-    return rc;
-  if ((rc = product(MOE_GMM_DW, dt, dyp, d, hs, f, io->dw_down, f, d, f, 0, acc))) return rc;
-  // gradients of the rows, over x's rows, which are not needed any more
-  char* dx_perm = xp;
-  if ((rc = product(MOE_GMM_DX, dt, dzu, 2 * f, io->w_gate, d, dx_perm, d, 0, d, f, 0))) return rc;
-  if ((rc = product(MOE_GMM_DX, dt, dzu + (size_t)f * es, 2 * f, io->w_up, d, dx_perm, d, 0, d, f, 1)))
-    return rc;
+  char* dx_perm = xp;  // over x's rows, once they are not needed any more
+  if (w.mfma) {
+    // the gradient at H, then z and u again with SwiGLU's step behind them
+    if ((rc = product(MOE_GMM_DX, MOE_F32, dyp, d, io->w_down, f, dh, f, 0, f, d, 0))) return rc;
+    MfmaArgs m{};
+    m.nsub = 1;
+    m.ngroups = s->n_ffn;
+    m.offsets = io->offsets;
+    m.M = Tk;
+    m.R = m.RB = d;
+    m.b_group = m.out_group = (int64_t)d * f;
+    m.nsplit = 1;
+    m.s[0] = {xp, io->w_gate, nullptr, d, d, 0, 0, f};
+    m.b2 = io->w_up;
+    m.perm = io->perm;
+    m.gate = io->topk_gate;
+    m.dh = dh;
+    m.dzu = dzu;
+    m.hs = hs;
+    m.dpart = part;
+    if ((rc = launch_swiglu_mfma(m, st))) return rc;
+    // gradients of the experts' weights, in one launch
+    m.nsub = 3;
+    m.s[0] = {dzu, xp, io->dw_gate, 2 * f, d, d, f, d};
+    m.s[1] = {dzu + (size_t)f * es, xp, io->dw_up, 2 * f, d, d, f, d};
+    m.s[2] = {dyp, hs, io->dw_down, d, f, f, d, f};
+    m.accumulate = acc;
+    if ((rc = launch_gmm_mfma(MOE_GMM_DW, dt, m, st))) return rc;
+    // gradients of the rows: one reduction over gate's and up's columns
+    m.nsub = 1;
+    m.s[0] = {dzu, io->w_gate, dx_perm, 2 * f, d, d, 0, d};
+    m.b2 = io->w_up;
+    m.R = m.RB = 2 * f;
+    m.r_switch = f;
+    m.accumulate = 0;
+    if ((rc = launch_gmm_mfma(MOE_GMM_DX, dt, m, st))) return rc;
+  } else {
+    if ((rc = product(MOE_GMM_FWD, MOE_F32, xp, d, io->w_gate, d, zu, 2 * f, 0, f, d, 0))) return rc;
+    if ((rc = product(MOE_GMM_FWD, MOE_F32, xp, d, io->w_up, d, zu + f, 2 * f, 0, f, d, 0))) return rc;
+    if ((rc = product(MOE_GMM_DX, MOE_F32, dyp, d, io->w_down, f, dh, f, 0, f, d, 0))) return rc;
+    if ((rc = launch_swiglu_bwd(dt, zu, dh, io->perm, io->topk_gate, io->offsets, s->n_ffn, Tk, f,
+                                dzu, hs, part, st)))
+      return rc;
+    char* du = dzu + (size_t)f * es;
+    if ((rc = product(MOE_GMM_DW, dt, dzu, 2 * f, xp, d, io->dw_gate, d, f, d, 0, acc))) return rc;
+    if ((rc = product(MOE_GMM_DW, dt, du, 2 * f, xp, d, io->dw_up, d, f, d, 0, acc))) return rc;
+    if ((rc = product(MOE_GMM_DW, dt, dyp, d, hs, f, io->dw_down, f, d, f, 0, acc))) return rc;
+    if ((rc = product(MOE_GMM_DX, dt, dzu, 2 * f, io->w_gate, d, dx_perm, d, 0, d, f, 0))) return rc;
+    if ((rc = product(MOE_GMM_DX, dt, du, 2 * f, io->w_up, d, dx_perm, d, 0, d, f, 1))) return rc;
+  }
 
   // gradients at the gates and logits, and the router's products
   TokenArgs a{};
@@ -272,7 +334,7 @@ int moe_layer_backward(const moe_shape* s, const moe_backward_io* io, void* ws, 
   a.E = E;
   a.k = s->top_k;
   a.n_ffn = s->n_ffn;
-  a.parts = 1;
+  a.parts = w.parts;
   a.ep = w.ep;
   a.nsplit = w.nsplit;
   if ((rc = launch_token_bwd(dt, a, st))) return rc;
@@ -290,8 +352,8 @@ int moe_layer_backward(const moe_shape* s, const moe_backward_io* io, void* ws, 
     r.offsets = route_offs;
     r.ngroups = 1;
     r.J = d;
-    r.R = E;
-    if ((rc = run_gmm(MOE_GMM_DX, dt, MOE_F32, r, st))) return rc;
+    r.R = w.mfma ? w.ep : E;  // zeros behind E, where w_router has no rows
+    if ((rc = run_gmm(MOE_GMM_DX, dt, MOE_F32, r, st, E))) return rc;
     // dlogits^T x over ranges of the tokens, joined
     r.b = io->x;
     r.out = drp;
@@ -299,7 +361,7 @@ int moe_layer_backward(const moe_shape* s, const moe_backward_io* io, void* ws, 
     r.offsets = split_offs;
     r.ngroups = w.nsplit;
     r.I = E;
-    if ((rc = run_gmm(MOE_GMM_DW, dt, MOE_F32, r, st))) return rc;
+    if ((rc = run_gmm(MOE_GMM_DW, dt, MOE_F32, r, st, w.ep))) return rc;
     r.part = drp;
     r.part_stride = (int64_t)E * d;
     r.nsplit = w.nsplit;
