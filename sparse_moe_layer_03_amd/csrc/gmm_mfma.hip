@@ -124,6 +124,20 @@ __device__ __forceinline__ uint2 bf16x4(const f32x4_t& v) {
   return make_uint2(lo, hi);
 }
 
+// Two 16 x 16 blocks side by side, packed to bf16: a lane holds columns 4 l4 ..
+// + 3 of both; swapping 16-lane rows between the two registers leaves it with
+// 8 neighbouring columns of one block (of the first for even l4, of the
+// second for odd), so that a row's 64 bytes go out in 16-byte stores (with
+// 8-byte stores in 32-byte pieces the weights' gradients were written at half
+// the rate).  bf16_col() is the first of the lane's columns.
+__device__ __forceinline__ u32x4_t bf16x8(const f32x4_t& a, const f32x4_t& b) {
+  const uint2 x = bf16x4(a), y = bf16x4(b);
+  const auto lo = __builtin_amdgcn_permlane16_swap(x.x, y.x, false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(x.y, y.y, false, false);
+  return u32x4_t{(uint32_t)lo[0], (uint32_t)hi[0], (uint32_t)lo[1], (uint32_t)hi[1]};
+}
+__device__ __forceinline__ int bf16_col(int l4) { return (l4 & 1) * 16 + (l4 >> 1) * 8; }
+
 template <int FORM, int EPI, typename TO, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
 gmm_mfma_kernel(MfmaArgs g) {
@@ -465,12 +479,11 @@ gmm_mfma_kernel(MfmaArgs g) {
         const int at = g.perm[p];
         const float gt = (unsigned)at < (unsigned)g.M ? g.gate[at] : 0.f;
         float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < NB / 2; ++j) {
+        // J is a multiple of 64 here: blocks are whole
+        auto block = [&](int j, f32x4_t& dz, f32x4_t& du, f32x4_t& hs) {
           const int jj = j0 + (wn * (NB / 2) + j) * 16 + l4 * 4;
-          if (!live || jj >= J) continue;  // J is a multiple of 64 here
-          const f32x4_t dh = *reinterpret_cast<const f32x4_t*>(g.dh + p * J + jj);
-          f32x4_t dz, du, hs;
+          f32x4_t dh = {0.f, 0.f, 0.f, 0.f};
+          if (live && jj < J) dh = *reinterpret_cast<const f32x4_t*>(g.dh + p * J + jj);
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             const float z = acc[i][j][v], u = acc[i][j + NB / 2][v];
@@ -481,10 +494,33 @@ gmm_mfma_kernel(MfmaArgs g) {
             du[v] = d * si;
             hs[v] = gt * h;
           }
-          char* o = (char*)g.dzu + (p * 2 * J + jj) * 2;
-          *reinterpret_cast<uint2*>(o) = bf16x4(dz);
-          *reinterpret_cast<uint2*>(o + (int64_t)J * 2) = bf16x4(du);
-          *reinterpret_cast<uint2*>((char*)g.hs + (p * J + jj) * 2) = bf16x4(hs);
+        };
+        if constexpr (NB / 2 >= 2) {
+#pragma unroll
+          for (int j = 0; j < NB / 2; j += 2) {
+            f32x4_t dz[2], du[2], hs[2];
+            block(j, dz[0], du[0], hs[0]);
+            block(j + 1, dz[1], du[1], hs[1]);
+            const u32x4_t oz = bf16x8(dz[0], dz[1]), ou = bf16x8(du[0], du[1]),
+                          oh = bf16x8(hs[0], hs[1]);
+            const int jj = j0 + (wn * (NB / 2) + j) * 16 + bf16_col(l4);
+            if (live && jj < J) {
+              char* o = (char*)g.dzu + (p * 2 * J + jj) * 2;
+              st16(o, oz);
+              st16(o + (int64_t)J * 2, ou);
+              st16((char*)g.hs + (p * J + jj) * 2, oh);
+            }
+          }
+        } else {
+          f32x4_t dz, du, hs;
+          block(0, dz, du, hs);
+          const int jj = j0 + wn * 16 + l4 * 4;
+          if (live && jj < J) {
+            char* o = (char*)g.dzu + (p * 2 * J + jj) * 2;
+            *reinterpret_cast<uint2*>(o) = bf16x4(dz);
+            *reinterpret_cast<uint2*>(o + (int64_t)J * 2) = bf16x4(du);
+            *reinterpret_cast<uint2*>((char*)g.hs + (p * J + jj) * 2) = bf16x4(hs);
+          }
         }
         sum += __shfl_xor(sum, 16, kWave);
         sum += __shfl_xor(sum, 32, kWave);
@@ -492,34 +528,50 @@ gmm_mfma_kernel(MfmaArgs g) {
           g.dpart[p * (long)(((J + HN - 1) / HN) * WN) + (j0 / HN) * WN + wn] = sum;
       } else {
         asm volatile("" ::: "memory");  // one row block's old values at a time
-        if (ii >= i_end) continue;
+        const bool live = ii < i_end;
         const long orow = DW ? (long)e * g.out_group + (long)ii * sub.ldo : (row0 + ii) * sub.ldo;
         const long prow = (DW ? (long)e * sub.I + ii : row0 + ii) * J;
-        const int jj0 = j0 + wn * NB * 16 + l4 * 4;
+        const int jw = j0 + wn * NB * 16;  // the wave's first column
         if (g.nsplit > 1) {
-          float* p = g.part + split * g.part_stride + prow + jj0;
+          float* p = g.part + split * g.part_stride + prow + jw + l4 * 4;
 #pragma unroll
           for (int j = 0; j < NB; ++j)
-            if (jj0 + j * 16 < J) *reinterpret_cast<f32x4_t*>(p + j * 16) = acc[i][j];
+            if (live && jw + j * 16 + l4 * 4 < J) *reinterpret_cast<f32x4_t*>(p + j * 16) = acc[i][j];
           continue;
         }
-        TO* p = (TO*)sub.out + orow + jj0;
+        if constexpr (sizeof(TO) == 4) {
+          float* p = (float*)sub.out + orow + jw + l4 * 4;
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          if (jj0 + j * 16 >= J) continue;
-          f32x4_t v = acc[i][j];
-          if (g.accumulate) {
-            if constexpr (sizeof(TO) == 4) {
-              v += *reinterpret_cast<const f32x4_t*>(p + j * 16);
+          for (int j = 0; j < NB; ++j) {
+            if (!live || jw + j * 16 + l4 * 4 >= J) continue;
+            f32x4_t v = acc[i][j];
+            if (g.accumulate) v += *reinterpret_cast<const f32x4_t*>(p + j * 16);
+            *reinterpret_cast<f32x4_t*>(p + j * 16) = v;
+          }
+        } else {
+          auto plus = [&](const f32x4_t& v, int j) -> f32x4_t {
+            const int jj = jw + j * 16 + l4 * 4;
+            if (!g.accumulate || !live || jj >= J) return v;
+            const uint2 old = *reinterpret_cast<const uint2*>((const __bf16*)sub.out + orow + jj);
+            const f32x4_t w = {__uint_as_float(old.x << 16), __uint_as_float(old.x & 0xffff0000u),
+                               __uint_as_float(old.y << 16), __uint_as_float(old.y & 0xffff0000u)};
+            return v + w;
+          };
+          const bool wide = ((J | (int)sub.ldo) & 7) == 0;  // whole 16-byte pieces
+#pragma unroll
+          for (int j = 0; j < NB; j += 2) {
+            const f32x4_t v0 = plus(acc[i][j], j), v1 = plus(acc[i][j + 1], j + 1);
+            __bf16* p = (__bf16*)sub.out + orow;
+            if (wide) {
+              const u32x4_t o = bf16x8(v0, v1);
+              const int jj = jw + j * 16 + bf16_col(l4);
+              if (live && jj < J) st16(p + jj, o);
             } else {
-              const uint2 old = *reinterpret_cast<const uint2*>(p + j * 16);
-              const f32x4_t w = {__uint_as_float(old.x << 16), __uint_as_float(old.x & 0xffff0000u),
-                                 __uint_as_float(old.y << 16), __uint_as_float(old.y & 0xffff0000u)};
-              v += w;
+              const int jj = jw + j * 16 + l4 * 4;
+              if (live && jj < J) *reinterpret_cast<uint2*>(p + jj) = bf16x4(v0);
+              if (live && jj + 16 < J) *reinterpret_cast<uint2*>(p + jj + 16) = bf16x4(v1);
             }
           }
-          if constexpr (sizeof(TO) == 4) *reinterpret_cast<f32x4_t*>(p + j * 16) = v;
-          else *reinterpret_cast<uint2*>(p + j * 16) = bf16x4(v);
         }
       }
     }
