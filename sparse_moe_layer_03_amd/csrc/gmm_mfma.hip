@@ -27,6 +27,7 @@
 //    one workgroup per tile, so that the hardware evens out hot experts;
 //    chunks of 32 neighbouring tiles go to one XCD and share its L2.
 
+#include <algorithm>
 #include <type_traits>
 
 #include "common.h"
@@ -35,6 +36,7 @@
 namespace moe {
 
 typedef __attribute__((address_space(3))) void lds_void_t;
+typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 
@@ -150,6 +152,8 @@ gmm_mfma_kernel(MfmaArgs g) {
   constexpr int A_PW = TA::PW, B_PW = TB::PW;
   constexpr int HN = SW ? BN / 2 : BN;  // output columns per tile
   constexpr int MG = 4;
+  // store instructions of a tile's epilogue (16 bytes a lane)
+  constexpr int NST = SW ? 0 : MB * NB * (int)sizeof(TO) / 4;
   static_assert(A_PW >= 1 && B_PW >= 1 && (!SW || (NB % 2 == 0 && B_PW % 2 == 0)), "tile");
 
   // one array per stage: the compiler then sees that the stage being read is
@@ -214,192 +218,239 @@ gmm_mfma_kernel(MfmaArgs g) {
     __syncthreads();
   };
 
-  for (int k = 0;; ++k) {
-    int e, i0, i_end, j0, split = 0;
+  // ---- one tile's place, the same in all lanes
+  struct Place {
+    int e, i0, i_end, j0, split, rows;
     long row0;
-    int rows;
+    int k_lo, k_hi, r_end;  // its steps, and the end of its reduction
+    int I, J;
+    int64_t ldo;
+    char* out;
+    const char *a_base, *b_base, *b_base2;
+    uint32_t a_bytes, b_bytes;  // OUT: of a row's part; RED: of the tile
+    uint32_t lda2, ldb2;        // bytes between rows
+  };
+  // lane offsets of the first load instructions of each kind
+  uint32_t a_off[TA::NP], b_off[TB::NP];
+
+  // Tile number k of this workgroup; false behind the last one.
+  auto setup = [&](int k, Place& t) -> bool {
     GmmSub sub = g.s[0];
+    t.split = 0;
     if constexpr (DW) {
-      if (k > 0) break;
-      // chunks of 32 tiles deal over the XCDs (workgroup b runs on XCD b % 8)
-      const int x = bid % 8, y = bid / 8;
-      long t = ((long)(y / 32) * 8 + x) * 32 + y % 32;
-      split = (int)(t % g.nsplit);
-      t /= g.nsplit;
       auto count = [](const GmmSub& s) { return ((s.I + BM - 1) / BM) * ((s.J + BN - 1) / BN); };
-      const int per_group = count(g.s[0]) + (g.nsub > 1 ? count(g.s[1]) : 0) +
-                            (g.nsub > 2 ? count(g.s[2]) : 0);
-      if (t >= (long)per_group * g.ngroups) break;
-      e = (int)(t / per_group);
-      int local = (int)(t - (long)e * per_group);
-      const int n0 = count(g.s[0]);
-      if (local >= n0) {
-        local -= n0;
+      const int c0 = count(g.s[0]), c1 = g.nsub > 1 ? count(g.s[1]) : 0,
+                c2 = g.nsub > 2 ? count(g.s[2]) : 0;
+      const uint32_t per_group = (uint32_t)(c0 + c1 + c2);
+      const uint32_t all = per_group * (uint32_t)g.ngroups * (uint32_t)g.nsplit;
+      // chunks of 32 tiles deal over the XCDs (workgroup b runs on XCD b % 8);
+      // a round of the grid is a multiple of 8
+      const uint32_t b = (uint32_t)bid + (uint32_t)k * (uint32_t)G;
+      const uint32_t x = b & 7, y = b >> 3;
+      uint32_t n = ((y >> 5) * 8 + x) * 32 + (y & 31);
+      // the tail's chunks may lie behind the end while later ones do not
+      if (b >= (all + 255) / 256 * 256) return false;
+      if (n >= all) {
+        t.e = -1;
+        return true;
+      }
+      if (g.nsplit > 1) {
+        t.split = (int)(n % (uint32_t)g.nsplit);
+        n /= (uint32_t)g.nsplit;
+      }
+      t.e = (int)(n / per_group);
+      int local = (int)(n - (uint32_t)t.e * per_group);
+      if (local >= c0) {
+        local -= c0;
         sub = g.s[1];
-        const int n1 = g.nsub > 1 ? count(g.s[1]) : 0;
-        if (local >= n1) {
-          local -= n1;
+        if (local >= c1) {
+          local -= c1;
           sub = g.s[2];
         }
       }
-      const int nj = (sub.J + BN - 1) / BN;
       // bands of 4 rows of tiles, column by column
-      const int ni = (sub.I + BM - 1) / BM;
+      const int nj = (sub.J + BN - 1) / BN, ni = (sub.I + BM - 1) / BM;
       const int band = local / (4 * nj), in = local - band * 4 * nj;
       const int high = min(4, ni - band * 4);
-      i0 = (band * 4 + in % high) * BM;
-      j0 = (in / high) * BN;
-      i_end = min(sub.I, i0 + BM);
+      t.i0 = (band * 4 + in % high) * BM;
+      t.j0 = (in / high) * BN;
+      t.i_end = min(sub.I, t.i0 + BM);
       int lo, hi;
-      rows_of(g.offsets, e, g.M, lo, hi);
-      row0 = lo;
-      rows = hi - lo;
+      rows_of(g.offsets, t.e, g.M, lo, hi);
+      t.row0 = lo;
+      t.rows = hi - lo;
     } else {
-      if ((k & 63) == 0) {
-        if (k > 0) {  // every wave is done with the last tile's stages
-          wait_vm<0>();
-          __syncthreads();
-        }
-        describe(k);
-      }
       const long item = vid + (long)k * G;
-      if (item >= tiles * g.nsplit) break;
-      const long t = item / g.nsplit;
-      split = (int)(item - t * g.nsplit);
+      if (item >= tiles * g.nsplit) return false;
+      long n = item;
+      if (g.nsplit > 1) {
+        n = item / g.nsplit;
+        t.split = (int)(item - n * g.nsplit);
+      }
       const uint32_t d = (uint32_t)__builtin_amdgcn_readlane((int)desc, k & 63);
-      e = (int)(d & 1023u);
+      t.e = (int)(d & 1023u);
       int lo, hi;
-      rows_of(g.offsets, e, g.M, lo, hi);
-      row0 = lo;
-      rows = hi - lo;
+      rows_of(g.offsets, t.e, g.M, lo, hi);
+      t.row0 = lo;
+      t.rows = hi - lo;
       // in a group: bands of MG row tiles, column by column, so that tiles
       // that run together share row and weight slices in L2
-      const int mt = (rows + BM - 1) / BM;
-      const int local = (int)(t - (long)(d >> 10) * jt);
+      const int mt = (t.rows + BM - 1) / BM;
+      const int local = (int)(n - (long)(d >> 10) * jt);
       const int m0 = (local / (MG * jt)) * MG;
       const int mg = max(1, min(MG, mt - m0));
       const int in = local - m0 * jt;
-      j0 = (in / mg) * HN;
-      const int h = ((rows + mt - 1) / mt + 15) & ~15;  // balanced height
-      i0 = (m0 + in % mg) * h;
-      i_end = min(rows, i0 + h);
+      t.j0 = (in / mg) * HN;
+      const int h = ((t.rows + mt - 1) / mt + 15) & ~15;  // balanced height
+      t.i0 = (m0 + in % mg) * h;
+      t.i_end = min(t.rows, t.i0 + h);
     }
-    e = uni(e), i0 = uni(i0), i_end = uni(i_end), j0 = uni(j0), split = uni(split), rows = uni(rows);
-    row0 = uni((int)row0);
-    const int R = DW ? rows : g.R;
+    t.e = uni(t.e), t.i0 = uni(t.i0), t.i_end = uni(t.i_end), t.j0 = uni(t.j0);
+    t.split = uni(t.split), t.rows = uni(t.rows), t.row0 = uni((int)t.row0);
+    const int R = DW ? t.rows : g.R;
     const int steps = (R + 63) >> 6;
-    const int per = (steps + g.nsplit - 1) / g.nsplit;
-    const int k_lo = min(split * per, steps), k_hi = min(steps, k_lo + per);
-    const int r_end = min(R, k_hi * 64);  // reduction of this item: [64 k_lo, r_end)
-    const int J = sub.J;
-    const uint32_t lda2 = (uint32_t)sub.lda * 2, ldb2 = (uint32_t)sub.ldb * 2;
-
-    // ---- where the tiles come from
-    const char* a_base;
-    uint32_t a_bytes = 0;  // RED: the tile's; OUT: a row's part
+    const int per = g.nsplit > 1 ? (steps + g.nsplit - 1) / g.nsplit : steps;
+    t.k_lo = min(t.split * per, steps), t.k_hi = min(steps, t.k_lo + per);
+    t.r_end = min(R, t.k_hi * 64);
+    t.I = sub.I, t.J = sub.J, t.ldo = sub.ldo, t.out = (char*)sub.out;
+    t.lda2 = (uint32_t)sub.lda * 2, t.ldb2 = (uint32_t)sub.ldb * 2;
+    // where the operands' tiles begin and end
     if constexpr (DW) {
-      a_base = (const char*)sub.a + row0 * (int64_t)lda2 + (int64_t)i0 * 2;
-      a_bytes = (uint32_t)min(BM, ((sub.I + 7) & ~7) - i0) * 2;
+      t.a_base = uni((const char*)sub.a + t.row0 * (int64_t)t.lda2 + (int64_t)t.i0 * 2);
+      t.a_bytes = (uint32_t)min(BM, ((sub.I + 7) & ~7) - t.i0) * 2;
     } else {
-      a_base = (const char*)sub.a + (row0 + i0) * (int64_t)lda2;
-      a_bytes = i_end > i0 ? (uint32_t)(i_end - i0 - 1) * lda2 + (uint32_t)g.R * 2 : 0u;
+      t.a_base = uni((const char*)sub.a + (t.row0 + t.i0) * (int64_t)t.lda2);
+      t.a_bytes = t.i_end > t.i0 ? (uint32_t)(t.i_end - t.i0 - 1) * t.lda2 + (uint32_t)g.R * 2 : 0u;
     }
-    a_base = uni(a_base);
-    const char* b_base;
-    const char* b_base2 = nullptr;
-    uint32_t b_bytes;
+    t.b_base2 = nullptr;
     if constexpr (FORM == MOE_GMM_FWD) {
-      const int64_t at = ((int64_t)e * g.b_group + (int64_t)j0 * sub.ldb) * 2;
-      b_base = uni((const char*)sub.b + at);
-      if (SW) b_base2 = uni((const char*)g.b2 + at);
-      b_bytes = (uint32_t)(min(HN, J - j0) - 1) * ldb2 + (uint32_t)g.R * 2;
+      const int64_t at = ((int64_t)t.e * g.b_group + (int64_t)t.j0 * sub.ldb) * 2;
+      t.b_base = uni((const char*)sub.b + at);
+      if (SW) t.b_base2 = uni((const char*)g.b2 + at);
+      t.b_bytes = (uint32_t)(min(HN, t.J - t.j0) - 1) * t.ldb2 + (uint32_t)g.R * 2;
     } else {
-      const int64_t at = (FORM == MOE_GMM_DX ? (int64_t)e * g.b_group * 2 : row0 * (int64_t)ldb2) +
-                         (int64_t)j0 * 2;
-      b_base = uni((const char*)sub.b + at);
-      if (FORM == MOE_GMM_DX && g.r_switch) b_base2 = uni((const char*)g.b2 + at);
-      b_bytes = (uint32_t)min(BN, J - j0) * 2;
+      const int64_t at = (FORM == MOE_GMM_DX ? (int64_t)t.e * g.b_group * 2
+                                             : t.row0 * (int64_t)t.ldb2) + (int64_t)t.j0 * 2;
+      t.b_base = uni((const char*)sub.b + at);
+      if (FORM == MOE_GMM_DX && g.r_switch) t.b_base2 = uni((const char*)g.b2 + at);
+      t.b_bytes = (uint32_t)min(BN, t.J - t.j0) * 2;
     }
-    // lane offsets of the first instructions of each kind
-    uint32_t a_off[TA::NP], b_off[TB::NP];
 #pragma unroll
     for (int q = 0; q < TA::NP; ++q)
-      a_off[q] = (uint32_t)TA::row(q, wave, lane) * lda2 + TA::chunk(q, wave, lane) * 16;
+      a_off[q] = (uint32_t)TA::row(q, wave, lane) * t.lda2 + TA::chunk(q, wave, lane) * 16;
 #pragma unroll
     for (int q = 0; q < TB::NP; ++q)
-      b_off[q] = (uint32_t)TB::row(q, wave, lane) * ldb2 + TB::chunk(q, wave, lane) * 16;
-    // and what instruction q adds to them
-    auto a_add = [&](int q) { return (int)((uint32_t)(q - q % TA::NP) * (NW * TA::RPI) * lda2); };
-    auto b_add = [&](int q) {
-      // SwiGLU step: gate rows fill the first half of the tile, up rows the second
-      const int h = (SW && q >= B_PW / 2) ? q - B_PW / 2 : q;
-      return (int)((uint32_t)(h - h % TB::NP) * (NW * TB::RPI) * ldb2);
-    };
+      b_off[q] = (uint32_t)TB::row(q, wave, lane) * t.ldb2 + TB::chunk(q, wave, lane) * 16;
+    return true;
+  };
 
+  auto stage_a = [&](auto sc) -> char* { return decltype(sc)::value == 0 ? s_a0 : s_a1; };
+  auto stage_b = [&](auto sc) -> char* {
+    constexpr int S = decltype(sc)::value;
+    return S == 0 ? s_b0 : S == 1 ? s_b1 : s_b2;
+  };
+  // Load instruction q of step ks into a stage.  What its wave-uniform part
+  // adds to the lane offset goes through the scalar offset.
+  auto load_a = [&](const Place& t, auto sc, int ks, int q) {
+    char* dst = stage_a(sc) + (wave + q * NW) * 1024;
+    const int add = (int)((uint32_t)(q - q % TA::NP) * (NW * TA::RPI) * t.lda2);
+    if constexpr (DW) {
+      const int left = min(64, t.r_end - ks * 64);  // >= 1
+      const auto rs = descriptor(t.a_base + (int64_t)ks * 64 * t.lda2,
+                                 (uint32_t)(left - 1) * t.lda2 + t.a_bytes);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)a_off[q % TA::NP], add,
+                                               0, 0);
+    } else {
+      const auto rs = descriptor(t.a_base, t.a_bytes);
+      const int left = t.r_end - ks * 64;
+      uint32_t off = a_off[q % TA::NP];
+      if (left < 64) off = TA::chunk(q, wave, lane) * 8 < left ? off : kOutside;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)off, ks * 128 + add, 0,
+                                               0);
+    }
+  };
+  auto load_b = [&](const Place& t, auto sc, int ks, int q) {
+    char* dst = stage_b(sc) + (wave + q * NW) * 1024;
+    // SwiGLU step: gate rows fill the first half of the tile, up rows the second
+    const bool second = SW && q >= B_PW / 2;
+    const int h = second ? q - B_PW / 2 : q;
+    const int add = (int)((uint32_t)(h - h % TB::NP) * (NW * TB::RPI) * t.ldb2);
+    if constexpr (FORM == MOE_GMM_FWD) {
+      const auto rs = descriptor(second ? t.b_base2 : t.b_base, t.b_bytes);
+      const int left = t.r_end - ks * 64;
+      uint32_t off = b_off[h % TB::NP];
+      if (left < 64) off = TB::chunk(q, wave, lane) * 8 < left ? off : kOutside;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)off, ks * 128 + add, 0,
+                                               0);
+    } else {
+      int r = ks * 64;
+      // rows of b that this step has (w_router ends before dlogits' padding)
+      const int left = max(0, min(64, (FORM == MOE_GMM_DX ? min(t.r_end, g.RB) : t.r_end) - r));
+      const char* base = t.b_base;
+      if (FORM == MOE_GMM_DX && g.r_switch && r >= g.r_switch) {
+        base = t.b_base2;
+        r -= g.r_switch;
+      }
+      const auto rs = descriptor(base + (int64_t)r * t.ldb2,
+                                 left > 0 ? (uint32_t)(left - 1) * t.ldb2 + t.b_bytes : 0u);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)b_off[h % TB::NP], add,
+                                               0, 0);
+    }
+  };
+
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  // A tile's first loads: step 0 of both operands, step 1 of b.
+  auto prologue = [&](const Place& t) {
+    if (t.k_lo >= t.k_hi) return;
+#pragma unroll
+    for (int q = 0; q < A_PW; ++q) load_a(t, I0{}, t.k_lo, q);
+#pragma unroll
+    for (int q = 0; q < B_PW; ++q) load_b(t, I0{}, t.k_lo, q);
+    if (t.k_lo + 1 < t.k_hi) {
+#pragma unroll
+      for (int q = 0; q < B_PW; ++q) load_b(t, I1{}, t.k_lo + 1, q);
+    }
+  };
+
+  if constexpr (!DW) describe(0);
+  Place t, next;
+  if (!setup(0, t)) return;
+  if (t.e >= 0) prologue(t);
+  bool stored = false;  // whether the last tile's NST stores may be outstanding
+  for (int k = 0;; ++k) {
+    if (DW && t.e < 0) {  // a place behind the end: others may follow
+      if (!setup(k + 1, t)) break;
+      if (t.e >= 0) prologue(t);
+      stored = false;  // the stores are older than these loads
+      continue;
+    }
     f32x4_t acc[MB][NB];
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    auto stage_a = [&](auto sc) -> char* { return decltype(sc)::value == 0 ? s_a0 : s_a1; };
-    auto stage_b = [&](auto sc) -> char* {
-      constexpr int S = decltype(sc)::value;
-      return S == 0 ? s_b0 : S == 1 ? s_b1 : s_b2;
-    };
-    // rows of an OUT tile's step that exist
-    auto left_of = [&](int ks, int end) { return min(64, max(0, end - ks * 64)); };
-    auto load_a = [&](auto sc, int ks, int q) {
-      char* dst = stage_a(sc) + (wave + q * NW) * 1024;
-      if constexpr (DW) {
-        const int left = left_of(ks, r_end);
-        const auto rs = descriptor(a_base + (int64_t)ks * 64 * lda2,
-                                   left > 0 ? (uint32_t)(left - 1) * lda2 + a_bytes : 0u);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)a_off[q % TA::NP],
-                                                 a_add(q), 0, 0);
-      } else {
-        const auto rs = descriptor(a_base, a_bytes);
-        const int left = r_end - ks * 64;
-        uint32_t off = a_off[q % TA::NP];
-        if (left < 64) off = TA::chunk(q, wave, lane) * 8 < left ? off : kOutside;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)off,
-                                                 ks * 128 + a_add(q), 0, 0);
-      }
-    };
-    auto load_b = [&](auto sc, int ks, int q) {
-      char* dst = stage_b(sc) + (wave + q * NW) * 1024;
-      if constexpr (FORM == MOE_GMM_FWD) {
-        const auto rs = descriptor((SW && q >= B_PW / 2) ? b_base2 : b_base, b_bytes);
-        const int left = r_end - ks * 64;
-        uint32_t off = b_off[q % TB::NP];
-        if (left < 64) off = TB::chunk(q, wave, lane) * 8 < left ? off : kOutside;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)off,
-                                                 ks * 128 + b_add(q), 0, 0);
-      } else {
-        int left = left_of(ks, FORM == MOE_GMM_DX ? min(r_end, g.RB) : r_end), r = ks * 64;
-        const char* base = b_base;
-        if (FORM == MOE_GMM_DX && g.r_switch && r >= g.r_switch) {
-          base = b_base2;
-          r -= g.r_switch;
-        }
-        const auto rs = descriptor(base + (int64_t)r * ldb2,
-                                   left > 0 ? (uint32_t)(left - 1) * ldb2 + b_bytes : 0u);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)b_off[q % TB::NP],
-                                                 b_add(q), 0, 0);
-      }
-    };
-
-    // One step on stages (AS, BS) with MBA active row blocks: its own loads
-    // have landed when at most the next step's B loads are outstanding.
+    // One step on stages (AS, BS) with MBA active row blocks.  Its loads have
+    // landed when at most the next step's b loads are outstanding; at a tile's
+    // first step the last tile's stores may be, too (they were issued later).
     auto step = [&](auto mbac, auto asc, auto bsc, int ks) {
       constexpr int MBA = decltype(mbac)::value;
       constexpr int AS = decltype(asc)::value, BS = decltype(bsc)::value;
-      const char* sa = stage_a(asc);
-      const char* sb = stage_b(bsc);
-      wait_vm<B_PW>();
-      barrier_all();
       using NA = std::integral_constant<int, (AS + 1) % 2>;
       using NBS = std::integral_constant<int, (BS + 2) % 3>;
+      const char* sa = stage_a(asc);
+      const char* sb = stage_b(bsc);
+      const bool more = ks + 1 < t.k_hi;
+      if (AS == 0 && BS == 0 && stored && ks == t.k_lo) {
+        if (more) wait_vm<B_PW + NST>();
+        else wait_vm<NST>();
+      } else {
+        if (more) wait_vm<B_PW>();
+        else wait_vm<0>();
+      }
+      barrier_all();
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
@@ -410,11 +461,13 @@ gmm_mfma_kernel(MfmaArgs g) {
         for (int j = 0; j < NB; ++j)
           fb[j] = TB::frag(sb, b_lane, SW && j >= NB / 2 ? BN / 32 + j - NB / 2 : j, kk);
         if (kk == 0) {
+          if (more) {
 #pragma unroll
-          for (int q = 0; q < A_PW; ++q) load_a(NA{}, ks + 1, q);
-        } else {
+            for (int q = 0; q < A_PW; ++q) load_a(t, NA{}, ks + 1, q);
+          }
+        } else if (ks + 2 < t.k_hi) {
 #pragma unroll
-          for (int q = 0; q < B_PW; ++q) load_b(NBS{}, ks + 2, q);
+          for (int q = 0; q < B_PW; ++q) load_b(t, NBS{}, ks + 2, q);
         }
 #pragma unroll
         for (int i = 0; i < MBA; ++i)
@@ -426,31 +479,18 @@ gmm_mfma_kernel(MfmaArgs g) {
       __builtin_amdgcn_s_setprio(0);
     };
 
-    using I0 = std::integral_constant<int, 0>;
-    using I1 = std::integral_constant<int, 1>;
-    using I2 = std::integral_constant<int, 2>;
     auto loop = [&](auto mbac) {
-      // the last tile's reads and stores are done before its stages are
-      // filled and before vmcnt counts this tile's loads
-      wait_vm<0>();
-      barrier_all();
-#pragma unroll
-      for (int q = 0; q < A_PW; ++q) load_a(I0{}, k_lo, q);
-#pragma unroll
-      for (int q = 0; q < B_PW; ++q) load_b(I0{}, k_lo, q);
-#pragma unroll
-      for (int q = 0; q < B_PW; ++q) load_b(I1{}, k_lo + 1, q);
-      for (int ks = k_lo; ks < k_hi; ks += 6) {
+      for (int ks = t.k_lo; ks < t.k_hi; ks += 6) {
         step(mbac, I0{}, I0{}, ks);
-        if (ks + 1 >= k_hi) break;
+        if (ks + 1 >= t.k_hi) break;
         step(mbac, I1{}, I1{}, ks + 1);
-        if (ks + 2 >= k_hi) break;
+        if (ks + 2 >= t.k_hi) break;
         step(mbac, I0{}, I2{}, ks + 2);
-        if (ks + 3 >= k_hi) break;
+        if (ks + 3 >= t.k_hi) break;
         step(mbac, I1{}, I0{}, ks + 3);
-        if (ks + 4 >= k_hi) break;
+        if (ks + 4 >= t.k_hi) break;
         step(mbac, I0{}, I1{}, ks + 4);
-        if (ks + 5 >= k_hi) break;
+        if (ks + 5 >= t.k_hi) break;
         step(mbac, I1{}, I2{}, ks + 5);
       }
     };
@@ -459,7 +499,7 @@ gmm_mfma_kernel(MfmaArgs g) {
     } else {
       // row blocks of this wave that hold rows (a wave without any still
       // loads and waits with the others, on one block that is not stored)
-      const int nrb = (i_end - i0 + 15) / 16;
+      const int nrb = (t.i_end - t.i0 + 15) / 16;
       const int mba = min(MB, (nrb - wm + WM - 1) / WM);
       if (mba >= 4 && MB >= 4) loop(std::integral_constant<int, MB >= 4 ? 4 : MB>{});
       else if (mba == 3 && MB >= 3) loop(std::integral_constant<int, MB >= 3 ? 3 : MB>{});
@@ -467,21 +507,33 @@ gmm_mfma_kernel(MfmaArgs g) {
       else loop(std::integral_constant<int, 1>{});
     }
 
+    // ---- the next tile's first loads, before this one's stores: every wave
+    // is done with the stages, and no load is outstanding
+    bool have = false;
+    const bool early = DW || ((k + 1) & 63) != 0;  // else its place is not known yet
+    if (early) {
+      have = setup(k + 1, next);
+      barrier_all();
+      if (have && (!DW || next.e >= 0)) prologue(next);
+    }
+
     // ---- out.  b was the MFMA's row operand: lane (l16, l4) holds columns
     // 4 l4 .. 4 l4 + 3 of row l16 of a 16 x 16 block.
+    const int J = t.J;
+    stored = false;
+    if constexpr (SW) {
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      const int ii = i0 + (DW ? wm * MB + i : i * WM + wm) * 16 + l16;
-      if constexpr (SW) {
+      for (int i = 0; i < MB; ++i) {
         // z, u -> h, dz, du, and this wave's part of <dh, h>
-        const bool live = ii < i_end;
-        const long p = row0 + min(ii, rows - 1);
+        const int ii = t.i0 + (i * WM + wm) * 16 + l16;
+        const bool live = ii < t.i_end;
+        const long p = t.row0 + min(ii, t.rows - 1);
         const int at = g.perm[p];
         const float gt = (unsigned)at < (unsigned)g.M ? g.gate[at] : 0.f;
         float sum = 0.f;
         // J is a multiple of 64 here: blocks are whole
         auto block = [&](int j, f32x4_t& dz, f32x4_t& du, f32x4_t& hs) {
-          const int jj = j0 + (wn * (NB / 2) + j) * 16 + l4 * 4;
+          const int jj = t.j0 + (wn * (NB / 2) + j) * 16 + l4 * 4;
           f32x4_t dh = {0.f, 0.f, 0.f, 0.f};
           if (live && jj < J) dh = *reinterpret_cast<const f32x4_t*>(g.dh + p * J + jj);
 #pragma unroll
@@ -503,7 +555,7 @@ gmm_mfma_kernel(MfmaArgs g) {
             block(j + 1, dz[1], du[1], hs[1]);
             const u32x4_t oz = bf16x8(dz[0], dz[1]), ou = bf16x8(du[0], du[1]),
                           oh = bf16x8(hs[0], hs[1]);
-            const int jj = j0 + (wn * (NB / 2) + j) * 16 + bf16_col(l4);
+            const int jj = t.j0 + (wn * (NB / 2) + j) * 16 + bf16_col(l4);
             if (live && jj < J) {
               char* o = (char*)g.dzu + (p * 2 * J + jj) * 2;
               st16(o, oz);
@@ -514,7 +566,7 @@ gmm_mfma_kernel(MfmaArgs g) {
         } else {
           f32x4_t dz, du, hs;
           block(0, dz, du, hs);
-          const int jj = j0 + wn * 16 + l4 * 4;
+          const int jj = t.j0 + wn * 16 + l4 * 4;
           if (live && jj < J) {
             char* o = (char*)g.dzu + (p * 2 * J + jj) * 2;
             *reinterpret_cast<uint2*>(o) = bf16x4(dz);
@@ -525,56 +577,101 @@ gmm_mfma_kernel(MfmaArgs g) {
         sum += __shfl_xor(sum, 16, kWave);
         sum += __shfl_xor(sum, 32, kWave);
         if (live && l4 == 0)
-          g.dpart[p * (long)(((J + HN - 1) / HN) * WN) + (j0 / HN) * WN + wn] = sum;
-      } else {
-        asm volatile("" ::: "memory");  // one row block's old values at a time
-        const bool live = ii < i_end;
-        const long orow = DW ? (long)e * g.out_group + (long)ii * sub.ldo : (row0 + ii) * sub.ldo;
-        const long prow = (DW ? (long)e * sub.I + ii : row0 + ii) * J;
-        const int jw = j0 + wn * NB * 16;  // the wave's first column
-        if (g.nsplit > 1) {
-          float* p = g.part + split * g.part_stride + prow + jw + l4 * 4;
+          g.dpart[p * (long)(((J + HN - 1) / HN) * WN) + (t.j0 / HN) * WN + wn] = sum;
+      }
+    } else {
+      constexpr int IB = DW ? 1 : WM;                    // row blocks between a wave's blocks
+      const int ib0 = DW ? wm * MB : wm;
+      const int jw = t.j0 + wn * NB * 16;                // the wave's first column
+      const int high = max(0, t.i_end - t.i0);           // rows of the tile
+      // Stores go through a descriptor that ends with the tile's last row, so
+      // that their number is the same for every tile; columns behind the last
+      // one are sent outside it.
+      if (g.nsplit > 1) {
+        const long first = DW ? (long)t.e * t.I : t.row0;
+        const auto ro = descriptor((const char*)(g.part + t.split * g.part_stride +
+                                                 (first + t.i0) * J),
+                                   (uint32_t)high * J * 4);
 #pragma unroll
-          for (int j = 0; j < NB; ++j)
-            if (live && jw + j * 16 + l4 * 4 < J) *reinterpret_cast<f32x4_t*>(p + j * 16) = acc[i][j];
-          continue;
-        }
-        if constexpr (sizeof(TO) == 4) {
-          float* p = (float*)sub.out + orow + jw + l4 * 4;
+        for (int i = 0; i < MB; ++i)
 #pragma unroll
           for (int j = 0; j < NB; ++j) {
-            if (!live || jw + j * 16 + l4 * 4 >= J) continue;
-            f32x4_t v = acc[i][j];
-            if (g.accumulate) v += *reinterpret_cast<const f32x4_t*>(p + j * 16);
-            *reinterpret_cast<f32x4_t*>(p + j * 16) = v;
-          }
-        } else {
-          auto plus = [&](const f32x4_t& v, int j) -> f32x4_t {
             const int jj = jw + j * 16 + l4 * 4;
-            if (!g.accumulate || !live || jj >= J) return v;
-            const uint2 old = *reinterpret_cast<const uint2*>((const __bf16*)sub.out + orow + jj);
-            const f32x4_t w = {__uint_as_float(old.x << 16), __uint_as_float(old.x & 0xffff0000u),
-                               __uint_as_float(old.y << 16), __uint_as_float(old.y & 0xffff0000u)};
-            return v + w;
-          };
-          const bool wide = ((J | (int)sub.ldo) & 7) == 0;  // whole 16-byte pieces
+            const uint32_t off = (uint32_t)((ib0 + i * IB) * 16 + l16) * J * 4 + jj * 4;
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[i][j]), ro,
+                                                   jj < J ? off : kOutside, 0, 0);
+          }
+      } else {
+        const long first = DW ? (long)t.e * g.out_group + (long)t.i0 * t.ldo : (t.row0 + t.i0) * t.ldo;
+        const auto ro = descriptor(uni(t.out + first * (long)sizeof(TO)),
+                                   high > 0 ? ((uint32_t)(high - 1) * (uint32_t)t.ldo + J) *
+                                                  (uint32_t)sizeof(TO)
+                                            : 0u);
+        const uint32_t ldo_b = (uint32_t)t.ldo * (uint32_t)sizeof(TO);
+        const bool add = g.accumulate;
 #pragma unroll
-          for (int j = 0; j < NB; j += 2) {
-            const f32x4_t v0 = plus(acc[i][j], j), v1 = plus(acc[i][j + 1], j + 1);
-            __bf16* p = (__bf16*)sub.out + orow;
-            if (wide) {
-              const u32x4_t o = bf16x8(v0, v1);
-              const int jj = jw + j * 16 + bf16_col(l4);
-              if (live && jj < J) st16(p + jj, o);
+        for (int i = 0; i < MB; ++i) {
+          const uint32_t row = (uint32_t)((ib0 + i * IB) * 16 + l16) * ldo_b;
+          auto at = [&](int jj) { return jj < J ? row + (uint32_t)jj * (uint32_t)sizeof(TO) : kOutside; };
+          asm volatile("" ::: "memory");  // one row block's old values at a time
+          if constexpr (sizeof(TO) == 4) {
+            f32x4_t old[NB];
+            if (add) {
+#pragma unroll
+              for (int j = 0; j < NB; ++j)
+                old[j] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                         ro, at(jw + j * 16 + l4 * 4), 0, 0));
+#pragma unroll
+              for (int j = 0; j < NB; ++j) acc[i][j] += old[j];
+            }
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[i][j]), ro,
+                                                     at(jw + j * 16 + l4 * 4), 0, 0);
+          } else {
+            if (add) {
+              uint2 old[NB];
+#pragma unroll
+              for (int j = 0; j < NB; ++j)
+                old[j] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(
+                                                       ro, at(jw + j * 16 + l4 * 4), 0, 0));
+#pragma unroll
+              for (int j = 0; j < NB; ++j) {
+                const f32x4_t w = {__uint_as_float(old[j].x << 16),
+                                   __uint_as_float(old[j].x & 0xffff0000u),
+                                   __uint_as_float(old[j].y << 16),
+                                   __uint_as_float(old[j].y & 0xffff0000u)};
+                acc[i][j] += w;
+              }
+            }
+            if (((J | (int)t.ldo) & 7) == 0) {  // whole 16-byte pieces
+#pragma unroll
+              for (int j = 0; j < NB; j += 2)
+                __builtin_amdgcn_raw_buffer_store_b128(bf16x8(acc[i][j], acc[i][j + 1]), ro,
+                                                       at(jw + j * 16 + bf16_col(l4)), 0, 0);
             } else {
-              const int jj = jw + j * 16 + l4 * 4;
-              if (live && jj < J) *reinterpret_cast<uint2*>(p + jj) = bf16x4(v0);
-              if (live && jj + 16 < J) *reinterpret_cast<uint2*>(p + jj + 16) = bf16x4(v1);
+#pragma unroll
+              for (int j = 0; j < NB; ++j)
+                __builtin_amdgcn_raw_buffer_store_b64(
+                    __builtin_bit_cast(u32x2_t, bf16x4(acc[i][j])), ro, at(jw + j * 16 + l4 * 4), 0, 0);
             }
           }
         }
+        // (the 8-byte stores are more; that only waits longer)
+        stored = early;
       }
     }
+    if (!early) {
+      // the next 64 tiles' places are worked out in the stages
+      wait_vm<0>();
+      __syncthreads();
+      describe(k + 1);
+      have = setup(k + 1, next);
+      if (have) prologue(next);
+      stored = false;
+    }
+    if (!have) break;
+    t = next;
   }
 #endif
 }
@@ -582,7 +679,7 @@ gmm_mfma_kernel(MfmaArgs g) {
 bool mfma_ok(int form, int dtype, int N, int K, int64_t lda, int64_t ldc) {
   if (dtype != MOE_BF16 || K % 8 != 0 || lda % 8 != 0) return false;
   // a descriptor spans at most 256 rows
-  if (lda >= (1 << 21) || ldc >= (1 << 21)) return false;
+  if (lda > (1 << 20) || ldc > (1 << 20)) return false;
   return form == MOE_GMM_FWD ? N % 4 == 0 && ldc % 4 == 0 : N % 8 == 0 && ldc % 8 == 0;
 }
 
@@ -598,7 +695,10 @@ static int launch_tile(const MfmaArgs& g, hipStream_t st) {
     for (int q = 0; q < g.nsub; ++q)
       t += (long)((g.s[q].I + BM - 1) / BM) * ((g.s[q].J + BN - 1) / BN);
     t *= (long)g.ngroups * g.nsplit;
-    grid = (t + 255) / 256 * 256;  // whole rounds of 8 XCDs x 32 tiles
+    if (t >= (1l << 31)) return MOE_EUNSUPPORTED;
+    constexpr int LDS = BM * 256 + BN * 384;
+    grid = (long)cus * (160 * 1024 / LDS < 2 ? 1 : 2) / 8 * 8;
+    grid = std::max(8l, std::min(grid, (t + 255) / 256 * 256));
   } else {
     const long most = (long)(g.M / BM + (g.M < g.ngroups ? g.M : g.ngroups)) *
                       ((g.s[0].J + HN - 1) / HN) * g.nsplit;
