@@ -70,17 +70,28 @@ __device__ __forceinline__ void rows_of(const int32_t* offsets, int e, int M, in
   hi = min(max(offsets[e + 1], lo), M);
 }
 
-// One operand's tile geometry: W rows or columns of the output side.
-template <bool OUT, int W, int NW>
+// The same for a group known to be one for all lanes, through the scalar
+// cache: a vector load would wait behind the last tile's stores.
+__device__ __forceinline__ void rows_of_uniform(const int32_t* offsets, int e, int M, int& lo, int& hi) {
+  typedef const __attribute__((address_space(4))) int32_t* const_ptr_t;
+  const const_ptr_t o = (const_ptr_t)(offsets + e);
+  lo = min(max(o[0], 0), M);
+  hi = min(max(o[1], lo), M);
+}
+
+// One operand's tile geometry: W rows or columns of the output side, KS
+// reduction values (64 or 32) a step.
+template <bool OUT, int W, int NW, int KS>
 struct Tile {
-  static constexpr int RB = OUT ? W * 2 : 128;   // bytes per LDS row
-  static constexpr int RPI = 1024 / RB;          // LDS rows per DMA instruction
-  static constexpr int PW = W / 8 / NW;          // DMA instructions per wave and step
-  static constexpr int BYTES = W * 128;
+  static constexpr int RB = OUT ? W * 2 : KS * 2;  // bytes per LDS row
+  static constexpr int RPI = 1024 / RB;            // LDS rows per DMA instruction
+  static constexpr int BYTES = W * KS * 2;
+  static constexpr int PW = BYTES / 1024 / NW;     // DMA instructions per wave and step
   // Instructions q and q + P of a wave fetch the same chunks of rows that lie
   // (P NW RPI) apart: their lane offsets differ by a wave-uniform amount.
-  static constexpr int P = OUT ? (NW * RPI >= 16 ? 1 : 16 / (NW * RPI)) : (NW >= 8 ? 1 : 8 / NW);
+  static constexpr int P = NW * RPI >= 16 ? 1 : 16 / (NW * RPI);  // the swizzles repeat every 16 rows
   static constexpr int NP = P < PW ? P : PW;
+  static_assert(PW >= 1 && PW * NW * 1024 == BYTES, "whole instructions");
   static_assert(!OUT || W >= 128, "OUT tiles are 128 or 256 wide");
   // LDS row and logical 16-byte chunk that lane `lane` of instruction q of
   // wave `wave` fills
@@ -90,9 +101,19 @@ struct Tile {
   static __device__ __forceinline__ int chunk(int q, int wave, int lane) {
     const int r = row(q, wave, lane), slot = lane % (RB / 16);
     if (OUT) return slot ^ (flip(r) << 1);
-    return slot ^ ((r ^ (r >> 3)) & 7);
+    return slot ^ turn(r);
   }
+  // OUT: half a wave's tr read covers 8 rows (b 8 + 0 .. 3, two values of b)
+  // of 32 bytes, which land on 8 different 32-byte pieces of the 256 that the
+  // banks span.
   static __device__ __forceinline__ int flip(int r) { return (r & 3) | ((r >> 1) & 4); }
+  // RED: a 16-byte read serves 16 lanes a cycle, among them rows 0 .. 3 and
+  // 12 .. 15 at one chunk with rows 4 .. 11 at the next; r ^ r >> 3, which
+  // suits 16 rows of one chunk, had cost every read a second pass.
+  static __device__ __forceinline__ int turn(int r) {
+    if (KS == 32) return ((r >> 2) & 1) | (((r >> 1) ^ (r >> 2)) & 2);
+    return (r >> 1) & 7;
+  }
   // Fragments: block b covers 16 outputs, slice kk 32 reduction values.  The
   // block's wave-dependent part goes into the lane's base address, the rest
   // (with no bit in common) into constants.
@@ -103,8 +124,7 @@ struct Tile {
       return r * RB + ((b ^ flip(r)) << 5) + (l16 & 3) * 8;
     }
     // chunk (4 kk + l4) of row 16 b + l16, under the row's swizzle
-    const int s = (l16 ^ (l16 >> 3)) & 7;
-    return b * 2048 + l16 * 128 + ((l4 ^ s ^ ((2 * b) & 6)) << 4);
+    return (b * 16 + l16) * RB + ((l4 ^ turn(l16)) << 4);
   }
   static __device__ __forceinline__ bf16x8_t frag(const char* s, int base, int b, int kk) {
     if constexpr (OUT) {
@@ -113,7 +133,7 @@ struct Tile {
       const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + 4 * RB));
       return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      return *reinterpret_cast<const bf16x8_t*>(s + b * 2048 + (base ^ (((4 * kk) ^ ((2 * b) & 6)) << 4)));
+      return *reinterpret_cast<const bf16x8_t*>(s + b * 16 * RB + (base ^ (kk << 6)));
     }
   }
 };
@@ -140,21 +160,24 @@ __device__ __forceinline__ u32x4_t bf16x8(const f32x4_t& a, const f32x4_t& b) {
 }
 __device__ __forceinline__ int bf16_col(int l4) { return (l4 & 1) * 16 + (l4 >> 1) * 8; }
 
-template <int FORM, int EPI, typename TO, int BM, int BN, int WM, int WN>
+template <int FORM, int EPI, typename TO, int BM, int BN, int WM, int WN, int KS>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
 gmm_mfma_kernel(MfmaArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NW = WM * WN, NT = 64 * NW;
   constexpr bool DW = FORM == MOE_GMM_DW, SW = EPI == EPI_SWIGLU;
-  using TA = Tile<DW, BM, NW>;
-  using TB = Tile<FORM != MOE_GMM_FWD, BN, NW>;
+  using TA = Tile<DW, BM, NW, KS>;
+  using TB = Tile<FORM != MOE_GMM_FWD, BN, NW, KS>;
   constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
   constexpr int A_PW = TA::PW, B_PW = TB::PW;
   constexpr int HN = SW ? BN / 2 : BN;  // output columns per tile
   constexpr int MG = 4;
   // store instructions of a tile's epilogue (16 bytes a lane)
-  constexpr int NST = SW ? 0 : MB * NB * (int)sizeof(TO) / 4;
+  constexpr int NST_ALL = MB * NB * (int)sizeof(TO) / 4;
+  // (vmcnt counts to 63; 0: every load waits for the stores before it)
+  constexpr int NST = SW || NST_ALL + A_PW + B_PW > 63 ? 0 : NST_ALL;
   static_assert(A_PW >= 1 && B_PW >= 1 && (!SW || (NB % 2 == 0 && B_PW % 2 == 0)), "tile");
+  static_assert(TA::BYTES > kMfmaMaxGroups * 4, "the groups' prefix fits a stage");
 
   // one array per stage: the compiler then sees that the stage being read is
   // not one being filled
@@ -258,7 +281,7 @@ gmm_mfma_kernel(MfmaArgs g) {
         t.split = (int)(n % (uint32_t)g.nsplit);
         n /= (uint32_t)g.nsplit;
       }
-      t.e = (int)(n / per_group);
+      t.e = uni((int)(n / per_group));
       int local = (int)(n - (uint32_t)t.e * per_group);
       if (local >= c0) {
         local -= c0;
@@ -276,7 +299,7 @@ gmm_mfma_kernel(MfmaArgs g) {
       t.j0 = (in / high) * BN;
       t.i_end = min(sub.I, t.i0 + BM);
       int lo, hi;
-      rows_of(g.offsets, t.e, g.M, lo, hi);
+      rows_of_uniform(g.offsets, t.e, g.M, lo, hi);
       t.row0 = lo;
       t.rows = hi - lo;
     } else {
@@ -288,9 +311,9 @@ gmm_mfma_kernel(MfmaArgs g) {
         t.split = (int)(item - n * g.nsplit);
       }
       const uint32_t d = (uint32_t)__builtin_amdgcn_readlane((int)desc, k & 63);
-      t.e = (int)(d & 1023u);
+      t.e = uni((int)(d & 1023u));
       int lo, hi;
-      rows_of(g.offsets, t.e, g.M, lo, hi);
+      rows_of_uniform(g.offsets, t.e, g.M, lo, hi);
       t.row0 = lo;
       t.rows = hi - lo;
       // in a group: bands of MG row tiles, column by column, so that tiles
@@ -308,10 +331,10 @@ gmm_mfma_kernel(MfmaArgs g) {
     t.e = uni(t.e), t.i0 = uni(t.i0), t.i_end = uni(t.i_end), t.j0 = uni(t.j0);
     t.split = uni(t.split), t.rows = uni(t.rows), t.row0 = uni((int)t.row0);
     const int R = DW ? t.rows : g.R;
-    const int steps = (R + 63) >> 6;
+    const int steps = (R + KS - 1) / KS;
     const int per = g.nsplit > 1 ? (steps + g.nsplit - 1) / g.nsplit : steps;
     t.k_lo = min(t.split * per, steps), t.k_hi = min(steps, t.k_lo + per);
-    t.r_end = min(R, t.k_hi * 64);
+    t.r_end = min(R, t.k_hi * KS);
     t.I = sub.I, t.J = sub.J, t.ldo = sub.ldo, t.out = (char*)sub.out;
     t.lda2 = (uint32_t)sub.lda * 2, t.ldb2 = (uint32_t)sub.ldb * 2;
     // where the operands' tiles begin and end
@@ -355,17 +378,17 @@ gmm_mfma_kernel(MfmaArgs g) {
     char* dst = stage_a(sc) + (wave + q * NW) * 1024;
     const int add = (int)((uint32_t)(q - q % TA::NP) * (NW * TA::RPI) * t.lda2);
     if constexpr (DW) {
-      const int left = min(64, t.r_end - ks * 64);  // >= 1
-      const auto rs = descriptor(t.a_base + (int64_t)ks * 64 * t.lda2,
+      const int left = min(KS, t.r_end - ks * KS);  // >= 1
+      const auto rs = descriptor(t.a_base + (int64_t)ks * KS * t.lda2,
                                  (uint32_t)(left - 1) * t.lda2 + t.a_bytes);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)a_off[q % TA::NP], add,
                                                0, 0);
     } else {
       const auto rs = descriptor(t.a_base, t.a_bytes);
-      const int left = t.r_end - ks * 64;
+      const int left = t.r_end - ks * KS;
       uint32_t off = a_off[q % TA::NP];
-      if (left < 64) off = TA::chunk(q, wave, lane) * 8 < left ? off : kOutside;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)off, ks * 128 + add, 0,
+      if (left < KS) off = TA::chunk(q, wave, lane) * 8 < left ? off : kOutside;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)off, ks * KS * 2 + add, 0,
                                                0);
     }
   };
@@ -377,15 +400,15 @@ gmm_mfma_kernel(MfmaArgs g) {
     const int add = (int)((uint32_t)(h - h % TB::NP) * (NW * TB::RPI) * t.ldb2);
     if constexpr (FORM == MOE_GMM_FWD) {
       const auto rs = descriptor(second ? t.b_base2 : t.b_base, t.b_bytes);
-      const int left = t.r_end - ks * 64;
+      const int left = t.r_end - ks * KS;
       uint32_t off = b_off[h % TB::NP];
-      if (left < 64) off = TB::chunk(q, wave, lane) * 8 < left ? off : kOutside;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)off, ks * 128 + add, 0,
+      if (left < KS) off = TB::chunk(q, wave, lane) * 8 < left ? off : kOutside;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)off, ks * KS * 2 + add, 0,
                                                0);
     } else {
-      int r = ks * 64;
+      int r = ks * KS;
       // rows of b that this step has (w_router ends before dlogits' padding)
-      const int left = max(0, min(64, (FORM == MOE_GMM_DX ? min(t.r_end, g.RB) : t.r_end) - r));
+      const int left = max(0, min(KS, (FORM == MOE_GMM_DX ? min(t.r_end, g.RB) : t.r_end) - r));
       const char* base = t.b_base;
       if (FORM == MOE_GMM_DX && g.r_switch && r >= g.r_switch) {
         base = t.b_base2;
@@ -401,7 +424,7 @@ gmm_mfma_kernel(MfmaArgs g) {
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
   using I2 = std::integral_constant<int, 2>;
-  // A tile's first loads: step 0 of both operands, step 1 of b.
+  // A tile's first loads: steps 0 and 1 of both operands.
   auto prologue = [&](const Place& t) {
     if (t.k_lo >= t.k_hi) return;
 #pragma unroll
@@ -411,6 +434,8 @@ gmm_mfma_kernel(MfmaArgs g) {
     if (t.k_lo + 1 < t.k_hi) {
 #pragma unroll
       for (int q = 0; q < B_PW; ++q) load_b(t, I1{}, t.k_lo + 1, q);
+#pragma unroll
+      for (int q = 0; q < A_PW; ++q) load_a(t, I1{}, t.k_lo + 1, q);
     }
   };
 
@@ -433,8 +458,9 @@ gmm_mfma_kernel(MfmaArgs g) {
       for (int j = 0; j < NB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
     // One step on stages (AS, BS) with MBA active row blocks.  Its loads have
-    // landed when at most the next step's b loads are outstanding; at a tile's
-    // first step the last tile's stores may be, too (they were issued later).
+    // landed when at most those issued later are outstanding: the next step's
+    // b loads (at a tile's first step its a loads, too), and at the first two
+    // steps the last tile's stores.
     auto step = [&](auto mbac, auto asc, auto bsc, int ks) {
       constexpr int MBA = decltype(mbac)::value;
       constexpr int AS = decltype(asc)::value, BS = decltype(bsc)::value;
@@ -443,17 +469,21 @@ gmm_mfma_kernel(MfmaArgs g) {
       const char* sa = stage_a(asc);
       const char* sb = stage_b(bsc);
       const bool more = ks + 1 < t.k_hi;
-      if (AS == 0 && BS == 0 && stored && ks == t.k_lo) {
-        if (more) wait_vm<B_PW + NST>();
-        else wait_vm<NST>();
+      const bool first = AS == 0 && BS == 0 && ks == t.k_lo;
+      const bool early_step = first || (AS == 1 && BS == 1 && ks == t.k_lo + 1);
+      if (early_step && stored) {
+        if (!more) wait_vm<NST>();
+        else if (first) wait_vm<B_PW + A_PW + NST>();
+        else wait_vm<B_PW + NST>();
       } else {
-        if (more) wait_vm<B_PW>();
-        else wait_vm<0>();
+        if (!more) wait_vm<0>();
+        else if (first) wait_vm<B_PW + A_PW>();
+        else wait_vm<B_PW>();
       }
       barrier_all();
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
+      for (int kk = 0; kk < KS / 32; ++kk) {
         bf16x8_t fa[MBA], fb[NB];
 #pragma unroll
         for (int i = 0; i < MBA; ++i) fa[i] = TA::frag(sa, a_lane, DW ? i : i * WM, kk);
@@ -461,11 +491,12 @@ gmm_mfma_kernel(MfmaArgs g) {
         for (int j = 0; j < NB; ++j)
           fb[j] = TB::frag(sb, b_lane, SW && j >= NB / 2 ? BN / 32 + j - NB / 2 : j, kk);
         if (kk == 0) {
-          if (more) {
+          if (more && !first) {
 #pragma unroll
             for (int q = 0; q < A_PW; ++q) load_a(t, NA{}, ks + 1, q);
           }
-        } else if (ks + 2 < t.k_hi) {
+        }
+        if (kk == KS / 32 - 1 && ks + 2 < t.k_hi) {
 #pragma unroll
           for (int q = 0; q < B_PW; ++q) load_b(t, NBS{}, ks + 2, q);
         }
@@ -658,7 +689,7 @@ gmm_mfma_kernel(MfmaArgs g) {
           }
         }
         // (the 8-byte stores are more; that only waits longer)
-        stored = early;
+        stored = early && NST > 0;
       }
     }
     if (!early) {
@@ -683,7 +714,7 @@ bool mfma_ok(int form, int dtype, int N, int K, int64_t lda, int64_t ldc) {
   return form == MOE_GMM_FWD ? N % 4 == 0 && ldc % 4 == 0 : N % 8 == 0 && ldc % 8 == 0;
 }
 
-template <int FORM, int EPI, typename TO, int BM, int BN, int WM, int WN>
+template <int FORM, int EPI, typename TO, int BM, int BN, int WM, int WN, int KS>
 static int launch_tile(const MfmaArgs& g, hipStream_t st) {
   const int cus = stream_cu_count(st);
   if (cus <= 0) return MOE_EHIP;
@@ -696,20 +727,20 @@ static int launch_tile(const MfmaArgs& g, hipStream_t st) {
       t += (long)((g.s[q].I + BM - 1) / BM) * ((g.s[q].J + BN - 1) / BN);
     t *= (long)g.ngroups * g.nsplit;
     if (t >= (1l << 31)) return MOE_EUNSUPPORTED;
-    constexpr int LDS = BM * 256 + BN * 384;
+    constexpr int LDS = (BM * 4 + BN * 6) * KS;
     grid = (long)cus * (160 * 1024 / LDS < 2 ? 1 : 2) / 8 * 8;
     grid = std::max(8l, std::min(grid, (t + 255) / 256 * 256));
   } else {
     const long most = (long)(g.M / BM + (g.M < g.ngroups ? g.M : g.ngroups)) *
                       ((g.s[0].J + HN - 1) / HN) * g.nsplit;
-    constexpr int LDS = BM * 256 + BN * 384;
+    constexpr int LDS = (BM * 4 + BN * 6) * KS;
     grid = (long)cus * (160 * 1024 / LDS < 2 ? 1 : 2);
     if (grid > most) grid = most;
     if (grid > 8) grid -= grid % 8;
   }
   if (grid < 1) return MOE_OK;
   if (grid > 0x7fffffffl) return MOE_EUNSUPPORTED;
-  hipLaunchKernelGGL((gmm_mfma_kernel<FORM, EPI, TO, BM, BN, WM, WN>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((gmm_mfma_kernel<FORM, EPI, TO, BM, BN, WM, WN, KS>), dim3((unsigned)grid),
                      dim3(64 * WM * WN), 0, st, g);
   return check_launch();
 }
@@ -725,16 +756,16 @@ static int launch_form(const MfmaArgs& g, hipStream_t st) {
     for (int q = 0; q < g.nsub; ++q)
       t += (long)((g.s[q].I + 255) / 256) * ((g.s[q].J + 255) / 256);
     if (t * g.ngroups * g.nsplit >= cus)
-      return launch_tile<FORM, EPI_STORE, TO, 256, 256, 4, 2>(g, st);
-    return launch_tile<FORM, EPI_STORE, TO, 128, 128, 2, 2>(g, st);
+      return launch_tile<FORM, EPI_STORE, TO, 256, 256, 4, 2, 64>(g, st);
+    return launch_tile<FORM, EPI_STORE, TO, 128, 128, 2, 2, 64>(g, st);
   }
   else {
     const long per = g.M / g.ngroups;
     const long t256 = (g.M / 256 + (g.M < g.ngroups ? g.M : g.ngroups)) * ((g.s[0].J + 255) / 256);
     if (per >= 128 && t256 * g.nsplit >= cus)
-      return launch_tile<FORM, EPI_STORE, TO, 256, 256, 4, 2>(g, st);
-    if (per >= 48) return launch_tile<FORM, EPI_STORE, TO, 128, 128, 2, 2>(g, st);
-    return launch_tile<FORM, EPI_STORE, TO, 64, 128, 1, 4>(g, st);
+      return launch_tile<FORM, EPI_STORE, TO, 256, 256, 4, 2, 64>(g, st);
+    if (per >= 48) return launch_tile<FORM, EPI_STORE, TO, 128, 128, 2, 2, 64>(g, st);
+    return launch_tile<FORM, EPI_STORE, TO, 64, 128, 1, 4, 64>(g, st);
   }
 }
 
@@ -761,9 +792,9 @@ int swiglu_parts(int M, int ngroups, int f) {
 
 int launch_swiglu_mfma(const MfmaArgs& g, hipStream_t st) {
   const int tile = swiglu_tile(g.M, g.ngroups);
-  if (tile == 256) return launch_tile<MOE_GMM_FWD, EPI_SWIGLU, __bf16, 256, 256, 4, 2>(g, st);
-  if (tile == 128) return launch_tile<MOE_GMM_FWD, EPI_SWIGLU, __bf16, 128, 128, 2, 2>(g, st);
-  return launch_tile<MOE_GMM_FWD, EPI_SWIGLU, __bf16, 64, 128, 1, 4>(g, st);
+  if (tile == 256) return launch_tile<MOE_GMM_FWD, EPI_SWIGLU, __bf16, 256, 256, 4, 2, 64>(g, st);
+  if (tile == 128) return launch_tile<MOE_GMM_FWD, EPI_SWIGLU, __bf16, 128, 128, 2, 2, 64>(g, st);
+  return launch_tile<MOE_GMM_FWD, EPI_SWIGLU, __bf16, 64, 128, 1, 4, 64>(g, st);
 }
 
 }  // namespace moe
