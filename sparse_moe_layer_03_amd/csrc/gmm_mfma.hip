@@ -160,7 +160,7 @@ __device__ __forceinline__ u32x4_t bf16x8(const f32x4_t& a, const f32x4_t& b) {
 }
 __device__ __forceinline__ int bf16_col(int l4) { return (l4 & 1) * 16 + (l4 >> 1) * 8; }
 
-template <int FORM, int EPI, typename TO, int BM, int BN, int WM, int WN, int KS>
+template <int FORM, int EPI, typename TO, int BM, int BN, int WM, int WN, int KS, int SA, int SB>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
 gmm_mfma_kernel(MfmaArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -169,23 +169,31 @@ gmm_mfma_kernel(MfmaArgs g) {
   using TA = Tile<DW, BM, NW, KS>;
   using TB = Tile<FORM != MOE_GMM_FWD, BN, NW, KS>;
   constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
-  constexpr int A_PW = TA::PW, B_PW = TB::PW;
+  constexpr int A_PW = TA::PW, B_PW = TB::PW, PW = A_PW + B_PW;
   constexpr int HN = SW ? BN / 2 : BN;  // output columns per tile
   constexpr int MG = 4;
+  constexpr int DA = SA - 1, DB = SB - 1;
   // store instructions of a tile's epilogue (16 bytes a lane)
   constexpr int NST_ALL = MB * NB * (int)sizeof(TO) / 4;
   // (vmcnt counts to 63; 0: every load waits for the stores before it)
-  constexpr int NST = SW || NST_ALL + A_PW + B_PW > 63 ? 0 : NST_ALL;
+  constexpr int NST = SW || NST_ALL + DB * PW > 63 ? 0 : NST_ALL;
   static_assert(A_PW >= 1 && B_PW >= 1 && (!SW || (NB % 2 == 0 && B_PW % 2 == 0)), "tile");
   static_assert(TA::BYTES > kMfmaMaxGroups * 4, "the groups' prefix fits a stage");
 
-  // one array per stage: the compiler then sees that the stage being read is
-  // not one being filled
+  // Rings of SA and SB stages, one array each: the compiler then sees that the
+  // stage being read is not one being filled.  Loads of a are DA steps ahead,
+  // those of b DB.
+  static_assert(DA >= 1 && DB >= DA && SB <= 5 && SA * TA::BYTES + SB * TB::BYTES <= 160 * 1024, "LDS");
   __shared__ __attribute__((aligned(1024))) char s_a0[TA::BYTES];
   __shared__ __attribute__((aligned(1024))) char s_a1[TA::BYTES];
+  __shared__ __attribute__((aligned(1024))) char s_a2[SA > 2 ? TA::BYTES : 16];
+  __shared__ __attribute__((aligned(1024))) char s_a3[SA > 3 ? TA::BYTES : 16];
+  __shared__ __attribute__((aligned(1024))) char s_a4[SA > 4 ? TA::BYTES : 16];
   __shared__ __attribute__((aligned(1024))) char s_b0[TB::BYTES];
   __shared__ __attribute__((aligned(1024))) char s_b1[TB::BYTES];
-  __shared__ __attribute__((aligned(1024))) char s_b2[TB::BYTES];
+  __shared__ __attribute__((aligned(1024))) char s_b2[SB > 2 ? TB::BYTES : 16];
+  __shared__ __attribute__((aligned(1024))) char s_b3[SB > 3 ? TB::BYTES : 16];
+  __shared__ __attribute__((aligned(1024))) char s_b4[SB > 4 ? TB::BYTES : 16];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = uni(tid >> 6);
@@ -253,7 +261,8 @@ gmm_mfma_kernel(MfmaArgs g) {
     uint32_t a_bytes, b_bytes;  // OUT: of a row's part; RED: of the tile
     uint32_t lda2, ldb2;        // bytes between rows
   };
-  // lane offsets of the first load instructions of each kind
+  // lane offsets of the first load instructions of each kind, in the tile
+  // whose loads go out
   uint32_t a_off[TA::NP], b_off[TB::NP];
 
   // Tile number k of this workgroup; false behind the last one.
@@ -358,19 +367,16 @@ gmm_mfma_kernel(MfmaArgs g) {
       if (FORM == MOE_GMM_DX && g.r_switch) t.b_base2 = uni((const char*)g.b2 + at);
       t.b_bytes = (uint32_t)min(BN, t.J - t.j0) * 2;
     }
-#pragma unroll
-    for (int q = 0; q < TA::NP; ++q)
-      a_off[q] = (uint32_t)TA::row(q, wave, lane) * t.lda2 + TA::chunk(q, wave, lane) * 16;
-#pragma unroll
-    for (int q = 0; q < TB::NP; ++q)
-      b_off[q] = (uint32_t)TB::row(q, wave, lane) * t.ldb2 + TB::chunk(q, wave, lane) * 16;
     return true;
   };
 
-  auto stage_a = [&](auto sc) -> char* { return decltype(sc)::value == 0 ? s_a0 : s_a1; };
+  auto stage_a = [&](auto sc) -> char* {
+    constexpr int N = decltype(sc)::value % SA;
+    return N == 0 ? s_a0 : N == 1 ? s_a1 : N == 2 ? s_a2 : N == 3 ? s_a3 : s_a4;
+  };
   auto stage_b = [&](auto sc) -> char* {
-    constexpr int S = decltype(sc)::value;
-    return S == 0 ? s_b0 : S == 1 ? s_b1 : s_b2;
+    constexpr int N = decltype(sc)::value % SB;
+    return N == 0 ? s_b0 : N == 1 ? s_b1 : N == 2 ? s_b2 : N == 3 ? s_b3 : s_b4;
   };
   // Load instruction q of step ks into a stage.  What its wave-uniform part
   // adds to the lane offset goes through the scalar offset.
@@ -421,32 +427,57 @@ gmm_mfma_kernel(MfmaArgs g) {
     }
   };
 
-  using I0 = std::integral_constant<int, 0>;
-  using I1 = std::integral_constant<int, 1>;
-  using I2 = std::integral_constant<int, 2>;
-  // A tile's first loads: steps 0 and 1 of both operands.
+  constexpr int UNROLL = SA == SB ? SA : SA * SB;
+  // A tile's first DA and DB steps, in the order in which the loop would
+  // have asked for them.
   auto prologue = [&](const Place& t) {
-    if (t.k_lo >= t.k_hi) return;
 #pragma unroll
-    for (int q = 0; q < A_PW; ++q) load_a(t, I0{}, t.k_lo, q);
+    for (int q = 0; q < TA::NP; ++q)
+      a_off[q] = (uint32_t)TA::row(q, wave, lane) * t.lda2 + TA::chunk(q, wave, lane) * 16;
 #pragma unroll
-    for (int q = 0; q < B_PW; ++q) load_b(t, I0{}, t.k_lo, q);
-    if (t.k_lo + 1 < t.k_hi) {
+    for (int q = 0; q < TB::NP; ++q)
+      b_off[q] = (uint32_t)TB::row(q, wave, lane) * t.ldb2 + TB::chunk(q, wave, lane) * 16;
+    auto one = [&](auto vc) {  // what step V of -DB .. -1 would load
+      constexpr int V = decltype(vc)::value - DB;
+      if constexpr (V + DA >= 0) {
+        if (t.k_lo + V + DA < t.k_hi) {
 #pragma unroll
-      for (int q = 0; q < B_PW; ++q) load_b(t, I1{}, t.k_lo + 1, q);
+          for (int q = 0; q < A_PW; ++q)
+            load_a(t, std::integral_constant<int, V + DA>{}, t.k_lo + V + DA, q);
+        }
+      }
+      if (t.k_lo + V + DB < t.k_hi) {
 #pragma unroll
-      for (int q = 0; q < A_PW; ++q) load_a(t, I1{}, t.k_lo + 1, q);
-    }
+        for (int q = 0; q < B_PW; ++q)
+          load_b(t, std::integral_constant<int, V + DB>{}, t.k_lo + V + DB, q);
+      }
+    };
+    one(std::integral_constant<int, 0>{});
+    if constexpr (DB > 1) one(std::integral_constant<int, 1>{});
+    if constexpr (DB > 2) one(std::integral_constant<int, 2>{});
+    if constexpr (DB > 3) one(std::integral_constant<int, 3>{});
+  };
+  // Loads issued after the last one that a step with `behind` steps behind it
+  // needs: a's of the next DA - 1 steps, and b's from (DB - DA) steps ahead on
+  // (with equal leads, b's own is needed).
+  auto later = [](int behind) constexpr {
+    const int na = behind < DA - 1 ? behind : DA - 1;
+    const int lo = DB == DA ? 1 : DB - DA, hi = behind < DB - 1 ? behind : DB - 1;
+    return na * A_PW + (hi >= lo ? hi - lo + 1 : 0) * B_PW;
   };
 
   if constexpr (!DW) describe(0);
   Place t, next;
   if (!setup(0, t)) return;
-  if (t.e >= 0) prologue(t);
+  if (!DW || t.e >= 0) prologue(t);
   bool stored = false;  // whether the last tile's NST stores may be outstanding
   for (int k = 0;; ++k) {
+    // the next tile's place, while this one's first loads are under way
+    const bool early = DW || ((k + 1) & 63) != 0;  // else it is not known yet
+    bool have = early && setup(k + 1, next);
     if (DW && t.e < 0) {  // a place behind the end: others may follow
-      if (!setup(k + 1, t)) break;
+      if (!have) break;
+      t = next;
       if (t.e >= 0) prologue(t);
       stored = false;  // the stores are older than these loads
       continue;
@@ -457,29 +488,24 @@ gmm_mfma_kernel(MfmaArgs g) {
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    // One step on stages (AS, BS) with MBA active row blocks.  Its loads have
-    // landed when at most those issued later are outstanding: the next step's
-    // b loads (at a tile's first step its a loads, too), and at the first two
-    // steps the last tile's stores.
-    auto step = [&](auto mbac, auto asc, auto bsc, int ks) {
-      constexpr int MBA = decltype(mbac)::value;
-      constexpr int AS = decltype(asc)::value, BS = decltype(bsc)::value;
-      using NA = std::integral_constant<int, (AS + 1) % 2>;
-      using NBS = std::integral_constant<int, (BS + 2) % 3>;
-      const char* sa = stage_a(asc);
-      const char* sb = stage_b(bsc);
-      const bool more = ks + 1 < t.k_hi;
-      const bool first = AS == 0 && BS == 0 && ks == t.k_lo;
-      const bool early_step = first || (AS == 1 && BS == 1 && ks == t.k_lo + 1);
-      if (early_step && stored) {
-        if (!more) wait_vm<NST>();
-        else if (first) wait_vm<B_PW + A_PW + NST>();
-        else wait_vm<B_PW + NST>();
-      } else {
-        if (!more) wait_vm<0>();
-        else if (first) wait_vm<B_PW + A_PW>();
-        else wait_vm<B_PW>();
-      }
+    // Step ks, at place N of the unrolled loop, with MBA active row blocks.  Its
+    // loads have landed when at most the later ones are outstanding and, at a
+    // tile's first DA steps (whose loads were issued before them), the last
+    // tile's stores.
+    auto step = [&](auto mbac, auto nc, int ks) {
+      constexpr int MBA = decltype(mbac)::value, N = decltype(nc)::value;
+      const char* sa = stage_a(nc);
+      const char* sb = stage_b(nc);
+      const int behind = t.k_hi - 1 - ks;
+      auto wait = [&](auto extra) {
+        constexpr int X = decltype(extra)::value;
+        if (DB == 1 || behind >= DB - 1) wait_vm<later(DB - 1) + X>();
+        else if (DB > 3 && behind == 2) wait_vm<later(DB > 3 ? 2 : 0) + X>();
+        else if (DB > 2 && behind == 1) wait_vm<later(DB > 2 ? 1 : 0) + X>();
+        else wait_vm<later(0) + X>();
+      };
+      if (stored && ks < t.k_lo + DA) wait(std::integral_constant<int, NST>{});
+      else wait(std::integral_constant<int, 0>{});
       barrier_all();
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -490,15 +516,14 @@ gmm_mfma_kernel(MfmaArgs g) {
 #pragma unroll
         for (int j = 0; j < NB; ++j)
           fb[j] = TB::frag(sb, b_lane, SW && j >= NB / 2 ? BN / 32 + j - NB / 2 : j, kk);
-        if (kk == 0) {
-          if (more && !first) {
+        // into the stages that every wave has left at this step's barrier
+        if (kk == 0 && behind >= DA) {
 #pragma unroll
-            for (int q = 0; q < A_PW; ++q) load_a(t, NA{}, ks + 1, q);
-          }
+          for (int q = 0; q < A_PW; ++q) load_a(t, std::integral_constant<int, N + DA>{}, ks + DA, q);
         }
-        if (kk == KS / 32 - 1 && ks + 2 < t.k_hi) {
+        if (kk == KS / 32 - 1 && behind >= DB) {
 #pragma unroll
-          for (int q = 0; q < B_PW; ++q) load_b(t, NBS{}, ks + 2, q);
+          for (int q = 0; q < B_PW; ++q) load_b(t, std::integral_constant<int, N + DB>{}, ks + DB, q);
         }
 #pragma unroll
         for (int i = 0; i < MBA; ++i)
@@ -511,18 +536,26 @@ gmm_mfma_kernel(MfmaArgs g) {
     };
 
     auto loop = [&](auto mbac) {
-      for (int ks = t.k_lo; ks < t.k_hi; ks += 6) {
-        step(mbac, I0{}, I0{}, ks);
+      for (int ks = t.k_lo; ks < t.k_hi; ks += UNROLL) {
+        step(mbac, std::integral_constant<int, 0>{}, ks);
         if (ks + 1 >= t.k_hi) break;
-        step(mbac, I1{}, I1{}, ks + 1);
-        if (ks + 2 >= t.k_hi) break;
-        step(mbac, I0{}, I2{}, ks + 2);
-        if (ks + 3 >= t.k_hi) break;
-        step(mbac, I1{}, I0{}, ks + 3);
-        if (ks + 4 >= t.k_hi) break;
-        step(mbac, I0{}, I1{}, ks + 4);
-        if (ks + 5 >= t.k_hi) break;
-        step(mbac, I1{}, I2{}, ks + 5);
+        step(mbac, std::integral_constant<int, 1>{}, ks + 1);
+        if constexpr (UNROLL > 2) {
+          if (ks + 2 >= t.k_hi) break;
+          step(mbac, std::integral_constant<int, 2>{}, ks + 2);
+        }
+        if constexpr (UNROLL > 3) {
+          if (ks + 3 >= t.k_hi) break;
+          step(mbac, std::integral_constant<int, 3>{}, ks + 3);
+        }
+        if constexpr (UNROLL > 4) {
+          if (ks + 4 >= t.k_hi) break;
+          step(mbac, std::integral_constant<int, 4>{}, ks + 4);
+        }
+        if constexpr (UNROLL > 5) {
+          if (ks + 5 >= t.k_hi) break;
+          step(mbac, std::integral_constant<int, 5>{}, ks + 5);
+        }
       }
     };
     if constexpr (DW || MB == 1) {
@@ -540,10 +573,7 @@ gmm_mfma_kernel(MfmaArgs g) {
 
     // ---- the next tile's first loads, before this one's stores: every wave
     // is done with the stages, and no load is outstanding
-    bool have = false;
-    const bool early = DW || ((k + 1) & 63) != 0;  // else its place is not known yet
     if (early) {
-      have = setup(k + 1, next);
       barrier_all();
       if (have && (!DW || next.e >= 0)) prologue(next);
     }
@@ -714,7 +744,7 @@ bool mfma_ok(int form, int dtype, int N, int K, int64_t lda, int64_t ldc) {
   return form == MOE_GMM_FWD ? N % 4 == 0 && ldc % 4 == 0 : N % 8 == 0 && ldc % 8 == 0;
 }
 
-template <int FORM, int EPI, typename TO, int BM, int BN, int WM, int WN, int KS>
+template <int FORM, int EPI, typename TO, int BM, int BN, int WM, int WN, int KS, int SA, int SB>
 static int launch_tile(const MfmaArgs& g, hipStream_t st) {
   const int cus = stream_cu_count(st);
   if (cus <= 0) return MOE_EHIP;
@@ -727,20 +757,20 @@ static int launch_tile(const MfmaArgs& g, hipStream_t st) {
       t += (long)((g.s[q].I + BM - 1) / BM) * ((g.s[q].J + BN - 1) / BN);
     t *= (long)g.ngroups * g.nsplit;
     if (t >= (1l << 31)) return MOE_EUNSUPPORTED;
-    constexpr int LDS = (BM * 4 + BN * 6) * KS;
+    constexpr int LDS = (BM * SA + BN * SB) * KS * 2;
     grid = (long)cus * (160 * 1024 / LDS < 2 ? 1 : 2) / 8 * 8;
     grid = std::max(8l, std::min(grid, (t + 255) / 256 * 256));
   } else {
     const long most = (long)(g.M / BM + (g.M < g.ngroups ? g.M : g.ngroups)) *
                       ((g.s[0].J + HN - 1) / HN) * g.nsplit;
-    constexpr int LDS = (BM * 4 + BN * 6) * KS;
+    constexpr int LDS = (BM * SA + BN * SB) * KS * 2;
     grid = (long)cus * (160 * 1024 / LDS < 2 ? 1 : 2);
     if (grid > most) grid = most;
     if (grid > 8) grid -= grid % 8;
   }
   if (grid < 1) return MOE_OK;
   if (grid > 0x7fffffffl) return MOE_EUNSUPPORTED;
-  hipLaunchKernelGGL((gmm_mfma_kernel<FORM, EPI, TO, BM, BN, WM, WN, KS>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((gmm_mfma_kernel<FORM, EPI, TO, BM, BN, WM, WN, KS, SA, SB>), dim3((unsigned)grid),
                      dim3(64 * WM * WN), 0, st, g);
   return check_launch();
 }
@@ -756,16 +786,16 @@ static int launch_form(const MfmaArgs& g, hipStream_t st) {
     for (int q = 0; q < g.nsub; ++q)
       t += (long)((g.s[q].I + 255) / 256) * ((g.s[q].J + 255) / 256);
     if (t * g.ngroups * g.nsplit >= cus)
-      return launch_tile<FORM, EPI_STORE, TO, 256, 256, 4, 2, 64>(g, st);
-    return launch_tile<FORM, EPI_STORE, TO, 128, 128, 2, 2, 64>(g, st);
+      return launch_tile<FORM, EPI_STORE, TO, 256, 256, 4, 2, 32, 4, 4>(g, st);
+    return launch_tile<FORM, EPI_STORE, TO, 128, 128, 2, 2, 32, 4, 4>(g, st);
   }
   else {
     const long per = g.M / g.ngroups;
     const long t256 = (g.M / 256 + (g.M < g.ngroups ? g.M : g.ngroups)) * ((g.s[0].J + 255) / 256);
     if (per >= 128 && t256 * g.nsplit >= cus)
-      return launch_tile<FORM, EPI_STORE, TO, 256, 256, 4, 2, 64>(g, st);
-    if (per >= 48) return launch_tile<FORM, EPI_STORE, TO, 128, 128, 2, 2, 64>(g, st);
-    return launch_tile<FORM, EPI_STORE, TO, 64, 128, 1, 4, 64>(g, st);
+      return launch_tile<FORM, EPI_STORE, TO, 256, 256, 4, 2, 64, 2, 3>(g, st);
+    if (per >= 48) return launch_tile<FORM, EPI_STORE, TO, 128, 128, 2, 2, 64, 2, 3>(g, st);
+    return launch_tile<FORM, EPI_STORE, TO, 64, 128, 1, 4, 64, 3, 3>(g, st);
   }
 }
 
@@ -792,9 +822,9 @@ int swiglu_parts(int M, int ngroups, int f) {
 
 int launch_swiglu_mfma(const MfmaArgs& g, hipStream_t st) {
   const int tile = swiglu_tile(g.M, g.ngroups);
-  if (tile == 256) return launch_tile<MOE_GMM_FWD, EPI_SWIGLU, __bf16, 256, 256, 4, 2, 64>(g, st);
-  if (tile == 128) return launch_tile<MOE_GMM_FWD, EPI_SWIGLU, __bf16, 128, 128, 2, 2, 64>(g, st);
-  return launch_tile<MOE_GMM_FWD, EPI_SWIGLU, __bf16, 64, 128, 1, 4, 64>(g, st);
+  if (tile == 256) return launch_tile<MOE_GMM_FWD, EPI_SWIGLU, __bf16, 256, 256, 4, 2, 64, 2, 3>(g, st);
+  if (tile == 128) return launch_tile<MOE_GMM_FWD, EPI_SWIGLU, __bf16, 128, 128, 2, 2, 64, 2, 3>(g, st);
+  return launch_tile<MOE_GMM_FWD, EPI_SWIGLU, __bf16, 64, 128, 1, 4, 64, 3, 3>(g, st);
 }
 
 }  // namespace moe
