@@ -7,7 +7,7 @@
 //     DX   A = lhs[row, r]   B = W_e[r, j]     (j contiguous in B)
 //     DW   A = lhs[row, i]   B = rhs[row, j]   (r is the row)
 //
-// Both operands are brought into LDS as fp32, reduction-major (16 values of
+// Both operands are brought into LDS as fp32, reduction-major (32 values of
 // r, each with the tile's i or j side by side), whatever their layout and
 // type in memory; 16x16x4 fp32 MFMAs take one value per lane from there.  A
 // product of two bf16 values is exact in fp32, so one kernel serves both
@@ -25,7 +25,7 @@
 namespace moe {
 
 constexpr int kGmmMaxGroups = 1024;
-constexpr int kGenBK = 16;
+constexpr int kGenBK = 32;
 
 template <typename T>
 __device__ __forceinline__ float elem(const T* p) {
@@ -69,7 +69,7 @@ __device__ __forceinline__ void group_rows(const int32_t* offsets, int e, int M,
 template <typename T, typename TO, int FORM, int BM, bool VEC>
 __global__ void __launch_bounds__(256)
 gmm_general_kernel(GmmArgs g) {
-  constexpr int BK = kGenBK, LDT = BM + 16, WT = BM / 2, NB = WT / 16, CH = BM / 64;
+  constexpr int BK = kGenBK, LDT = BM + 16, WT = BM / 2, NB = WT / 16, CH = BM * BK / 1024;
   constexpr bool A_RED = FORM != MOE_GMM_DW, B_RED = FORM == MOE_GMM_FWD;
   __shared__ __attribute__((aligned(16))) float s_a[2][BK * LDT];
   __shared__ __attribute__((aligned(16))) float s_b[2][BK * LDT];
@@ -79,8 +79,13 @@ gmm_general_kernel(GmmArgs g) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave >> 1, wn = wave & 1;
   const int r16 = lane & 15, q4 = lane >> 4;
-  const int jt = (g.J + BM - 1) / BM;
-  const int it_dw = (g.I + BM - 1) / BM;
+  auto tiles_of = [](int n) { return (n + BM - 1) / BM; };
+  // tiles of the products: per row tile (FWD, DX), per group (DW)
+  int n_sub[3];
+#pragma unroll
+  for (int q = 0; q < 3; ++q)
+    n_sub[q] = q < g.nsub ? tiles_of(g.s[q].J) * (FORM == MOE_GMM_DW ? tiles_of(g.s[q].I) : 1) : 0;
+  const int per = n_sub[0] + n_sub[1] + n_sub[2];
 
   // FWD, DX: prefix over the groups of their row tiles
   if (FORM != MOE_GMM_DW) {
@@ -103,27 +108,37 @@ gmm_general_kernel(GmmArgs g) {
       if (tid * PER + k < g.ngroups) s_pref[tid * PER + k + 1] = base + loc[k];
     __syncthreads();
   }
-  const long tiles = FORM == MOE_GMM_DW ? (long)g.ngroups * it_dw * jt : (long)s_pref[g.ngroups] * jt;
+  const long tiles = (long)(FORM == MOE_GMM_DW ? g.ngroups : s_pref[g.ngroups]) * per;
   const long items = tiles * g.nsplit;
 
   for (long item = blockIdx.x; item < items; item += gridDim.x) {
     const long t = item / g.nsplit;
     const int split = (int)(item - t * g.nsplit);
-    const int tj = (int)(t % jt);
+    const int m = (int)(t / per);
+    int local = (int)(t - (long)m * per);
+    GmmSub sub = g.s[0];
+    if (local >= n_sub[0]) {
+      local -= n_sub[0];
+      sub = g.s[1];
+      if (local >= n_sub[1]) {
+        local -= n_sub[1];
+        sub = g.s[2];
+      }
+    }
+    const int jt = tiles_of(sub.J);
+    const int tj = local % jt;
     int e, i0, rows, I, R;
     long row0;
     if (FORM == MOE_GMM_DW) {
-      const long u = t / jt;
-      e = (int)(u / it_dw);
-      i0 = (int)(u % it_dw) * BM;
+      e = m;
+      i0 = (local / jt) * BM;
       int lo, hi;
       group_rows(g.offsets, e, g.M, lo, hi);
       row0 = lo;
       rows = hi - lo;
-      I = g.I;
+      I = sub.I;
       R = rows;
     } else {
-      const int m = (int)(t / jt);
       int lo_e = 0, hi_e = g.ngroups - 1;  // last group with s_pref <= m
       while (lo_e < hi_e) {
         const int mid = (lo_e + hi_e + 1) >> 1;
@@ -141,12 +156,15 @@ gmm_general_kernel(GmmArgs g) {
     const int j0 = tj * BM;
     // this split's range of the reduction, in whole steps
     const int steps = (R + BK - 1) / BK;
-    const int per = (steps + g.nsplit - 1) / g.nsplit;
-    const int r_lo = min(split * per, steps) * BK, r_hi = min(R, min((split + 1) * per, steps) * BK);
+    const int len = (steps + g.nsplit - 1) / g.nsplit;
+    const int r_lo = min(split * len, steps) * BK, r_hi = min(R, min((split + 1) * len, steps) * BK);
 
-    const T* a = (const T*)g.a + (A_RED ? (row0 + i0) * g.lda : row0 * g.lda + i0);
-    const T* b = B_RED ? (const T*)g.b + e * g.b_group + (long)j0 * g.ldb
-                       : (const T*)g.b + (FORM == MOE_GMM_DX ? e * g.b_group : row0 * g.ldb) + j0;
+    const T* a = (const T*)sub.a + (A_RED ? (row0 + i0) * sub.lda : row0 * sub.lda + i0);
+    const long b_at = B_RED ? e * g.b_group + (long)j0 * sub.ldb
+                            : (FORM == MOE_GMM_DX ? e * g.b_group : row0 * sub.ldb) + j0;
+    const T* b = (const T*)sub.b + b_at;
+    const T* b2 = FORM == MOE_GMM_DX && g.r_switch ? (const T*)g.b2 + b_at : b;
+    const int rb_hi = FORM == MOE_GMM_DX ? min(r_hi, g.RB) : r_hi;
 
     f32x4_t acc[NB][NB];
 #pragma unroll
@@ -155,16 +173,16 @@ gmm_general_kernel(GmmArgs g) {
       for (int j = 0; j < NB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
     // chunk c of this thread: four elements that lie side by side in memory
-    auto fetch = [&](bool red, const T* base, long ld, int wide, int r0, f32x4_t* v) {
+    auto fetch = [&](bool red, const T* base, long ld, int wide, int r0, int r_end, f32x4_t* v) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int x = tid + c * 256;
         if (red) {  // row x % BM, r = 4 (x / BM) ..
           const int w = x % BM, r = r0 + (x / BM) * 4;
-          v[c] = w < wide ? load4<T, VEC>(base + w * ld + r, r_hi - r) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+          v[c] = w < wide ? load4<T, VEC>(base + w * ld + r, r_end - r) : f32x4_t{0.f, 0.f, 0.f, 0.f};
         } else {    // r = x / (BM / 4), columns 4 (x % (BM / 4)) ..
           const int w = (x % (BM / 4)) * 4, r = r0 + x / (BM / 4);
-          v[c] = r < r_hi ? load4<T, VEC>(base + r * ld + w, wide - w) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+          v[c] = r < r_end ? load4<T, VEC>(base + r * ld + w, wide - w) : f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
       }
     };
@@ -183,21 +201,22 @@ gmm_general_kernel(GmmArgs g) {
     };
 
     f32x4_t va[CH], vb[CH];
-    const int wide_a = I - i0, wide_b = g.J - j0;
+    const int wide_a = I - i0, wide_b = sub.J - j0;
+    auto fetch_ab = [&](int r) {
+      fetch(A_RED, a, sub.lda, wide_a, r, r_hi, va);
+      if (FORM == MOE_GMM_DX && g.r_switch && r >= g.r_switch)
+        fetch(B_RED, b2 - (long)g.r_switch * sub.ldb, sub.ldb, wide_b, r, rb_hi, vb);
+      else
+        fetch(B_RED, b, sub.ldb, wide_b, r, rb_hi, vb);
+    };
     __syncthreads();  // the previous tile's last reads of LDS
-    if (r_lo < r_hi) {
-      fetch(A_RED, a, g.lda, wide_a, r_lo, va);
-      fetch(B_RED, b, g.ldb, wide_b, r_lo, vb);
-    }
+    if (r_lo < r_hi) fetch_ab(r_lo);
     int st = 0;
     for (int r = r_lo; r < r_hi; r += BK, st ^= 1) {
       store(A_RED, s_a[st], va);
       store(B_RED, s_b[st], vb);
       __syncthreads();
-      if (r + BK < r_hi) {
-        fetch(A_RED, a, g.lda, wide_a, r + BK, va);
-        fetch(B_RED, b, g.ldb, wide_b, r + BK, vb);
-      }
+      if (r + BK < r_hi) fetch_ab(r + BK);
 #pragma unroll
       for (int k = 0; k < BK; k += 4) {
         float fa[NB], fb[NB];
@@ -218,24 +237,24 @@ gmm_general_kernel(GmmArgs g) {
     for (int i = 0; i < NB; ++i) {
       const int ii = i0 + wm * WT + i * 16 + r16;
       if (ii >= I) continue;
-      const long orow = FORM == MOE_GMM_DW ? (long)e * g.out_group + (long)ii * g.ldo
-                                           : (row0 + ii) * g.ldo;
+      const long orow = FORM == MOE_GMM_DW ? (long)e * g.out_group + (long)ii * sub.ldo
+                                           : (row0 + ii) * sub.ldo;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const int jj = j0 + wn * WT + j * 16 + q4 * 4;
-        if (jj >= g.J) continue;
+        if (jj >= sub.J) continue;
         if (g.nsplit > 1) {
           // partial outputs are compact: [split][row or group * I + i][J]
-          const long prow = FORM == MOE_GMM_DW ? (long)e * g.I + ii : row0 + ii;
-          float* p = g.part + split * g.part_stride + prow * g.J + jj;
+          const long prow = FORM == MOE_GMM_DW ? (long)e * sub.I + ii : row0 + ii;
+          float* p = g.part + split * g.part_stride + prow * sub.J + jj;
 #pragma unroll
           for (int v = 0; v < 4; ++v)
-            if (jj + v < g.J) p[v] = acc[i][j][v];
+            if (jj + v < sub.J) p[v] = acc[i][j][v];
         } else {
-          TO* p = (TO*)g.out + orow + jj;
+          TO* p = (TO*)sub.out + orow + jj;
 #pragma unroll
           for (int v = 0; v < 4; ++v)
-            if (jj + v < g.J) put(p + v, acc[i][j][v], g.accumulate);
+            if (jj + v < sub.J) put(p + v, acc[i][j][v], g.accumulate);
         }
       }
     }
@@ -245,17 +264,18 @@ gmm_general_kernel(GmmArgs g) {
 // out = sum over splits (in split order) of the partial outputs.
 template <typename TO, int FORM>
 __global__ void __launch_bounds__(256) gmm_join_kernel(GmmArgs g) {
-  const long rows = FORM == MOE_GMM_DW ? (long)g.ngroups * g.I
+  const GmmSub& s = g.s[0];
+  const long rows = FORM == MOE_GMM_DW ? (long)g.ngroups * s.I
                                        : min(max(g.offsets[g.ngroups], 0), g.M);
   const long first = FORM == MOE_GMM_DW ? 0 : min(max(g.offsets[0], 0), g.M);
-  const long n = rows * g.J;
-  for (long x = first * g.J + blockIdx.x * 256L + threadIdx.x; x < n; x += gridDim.x * 256L) {
-    const long row = x / g.J;
-    const int j = (int)(x - row * g.J);
+  const long n = rows * s.J;
+  for (long x = first * s.J + blockIdx.x * 256L + threadIdx.x; x < n; x += gridDim.x * 256L) {
+    const long row = x / s.J;
+    const int j = (int)(x - row * s.J);
     float v = 0.f;
-    for (int s = 0; s < g.nsplit; ++s) v += g.part[s * g.part_stride + x];
-    const long o = FORM == MOE_GMM_DW ? (row / g.I) * g.out_group + (row % g.I) * g.ldo : row * g.ldo;
-    put((TO*)g.out + o + j, v, g.accumulate);
+    for (int q = 0; q < g.nsplit; ++q) v += g.part[q * g.part_stride + x];
+    const long o = FORM == MOE_GMM_DW ? (row / s.I) * g.out_group + (row % s.I) * s.ldo : row * s.ldo;
+    put((TO*)s.out + o + j, v, g.accumulate);
   }
 }
 
@@ -264,10 +284,12 @@ static int launch_general(bool vec, const GmmArgs& g, hipStream_t st) {
   const int cus = stream_cu_count(st);
   if (cus <= 0) return MOE_EHIP;
   auto bound = [&](long bm) {
-    const long jt = (g.J + bm - 1) / bm;
-    const long it = FORM == MOE_GMM_DW ? (long)g.ngroups * ((g.I + bm - 1) / bm)
-                                       : (long)g.M / bm + (g.M < g.ngroups ? g.M : g.ngroups);
-    return it * jt * g.nsplit;
+    long n = 0;
+    for (int q = 0; q < g.nsub; ++q)
+      n += ((g.s[q].J + bm - 1) / bm) * (FORM == MOE_GMM_DW ? (g.s[q].I + bm - 1) / bm : 1);
+    const long m = FORM == MOE_GMM_DW ? (long)g.ngroups
+                                      : (long)g.M / bm + (g.M < g.ngroups ? g.M : g.ngroups);
+    return n * m * g.nsplit;
   };
   // 128 x 128 tiles when they fill the chip twice over, else 64 x 64
   const bool big = bound(128) >= 2L * cus;
@@ -303,7 +325,7 @@ int launch_gmm_general(int form, int dtype, int out_dtype, bool vec, const GmmAr
 }
 
 int launch_gmm_join(int form, int out_dtype, const GmmArgs& g, hipStream_t st) {
-  const long n = (form == MOE_GMM_DW ? (long)g.ngroups * g.I : (long)g.M) * g.J;
+  const long n = (form == MOE_GMM_DW ? (long)g.ngroups * g.s[0].I : (long)g.M) * g.s[0].J;
   if (n < 1) return MOE_OK;
   const long blocks = (n + 255) / 256;
   const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096));

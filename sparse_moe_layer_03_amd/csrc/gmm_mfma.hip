@@ -162,7 +162,7 @@ __device__ __forceinline__ int bf16_col(int l4) { return (l4 & 1) * 16 + (l4 >> 
 
 template <int FORM, int EPI, typename TO, int BM, int BN, int WM, int WN, int KS, int SA, int SB>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
-gmm_mfma_kernel(MfmaArgs g) {
+gmm_mfma_kernel(GmmArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NW = WM * WN, NT = 64 * NW;
   constexpr bool DW = FORM == MOE_GMM_DW, SW = EPI == EPI_SWIGLU;
@@ -583,14 +583,17 @@ gmm_mfma_kernel(MfmaArgs g) {
     const int J = t.J;
     stored = false;
     if constexpr (SW) {
+      float gates[MB];
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+        gates[i] = g.gate[t.row0 + min(t.i0 + (i * WM + wm) * 16 + l16, t.rows - 1)];
 #pragma unroll
       for (int i = 0; i < MB; ++i) {
         // z, u -> h, dz, du, and this wave's part of <dh, h>
         const int ii = t.i0 + (i * WM + wm) * 16 + l16;
         const bool live = ii < t.i_end;
         const long p = t.row0 + min(ii, t.rows - 1);
-        const int at = g.perm[p];
-        const float gt = (unsigned)at < (unsigned)g.M ? g.gate[at] : 0.f;
+        const float gt = gates[i];
         float sum = 0.f;
         // J is a multiple of 64 here: blocks are whole
         auto block = [&](int j, f32x4_t& dz, f32x4_t& du, f32x4_t& hs) {
@@ -745,7 +748,7 @@ bool mfma_ok(int form, int dtype, int N, int K, int64_t lda, int64_t ldc) {
 }
 
 template <int FORM, int EPI, typename TO, int BM, int BN, int WM, int WN, int KS, int SA, int SB>
-static int launch_tile(const MfmaArgs& g, hipStream_t st) {
+static int launch_tile(const GmmArgs& g, hipStream_t st) {
   const int cus = stream_cu_count(st);
   if (cus <= 0) return MOE_EHIP;
   constexpr bool DW = FORM == MOE_GMM_DW;
@@ -778,7 +781,7 @@ static int launch_tile(const MfmaArgs& g, hipStream_t st) {
 // Tile choice: by the rows a group has on average (FWD, DX) and whether the
 // larger tiles fill the chip.
 template <int FORM, typename TO>
-static int launch_form(const MfmaArgs& g, hipStream_t st) {
+static int launch_form(const GmmArgs& g, hipStream_t st) {
   const int cus = stream_cu_count(st);
   if (cus <= 0) return MOE_EHIP;
   if constexpr (FORM == MOE_GMM_DW) {
@@ -799,7 +802,7 @@ static int launch_form(const MfmaArgs& g, hipStream_t st) {
   }
 }
 
-int launch_gmm_mfma(int form, int out_dtype, const MfmaArgs& g, hipStream_t st) {
+int launch_gmm_mfma(int form, int out_dtype, const GmmArgs& g, hipStream_t st) {
   const bool f32 = out_dtype == MOE_F32;
   if (form == MOE_GMM_FWD)
     return f32 ? launch_form<MOE_GMM_FWD, float>(g, st) : launch_form<MOE_GMM_FWD, __bf16>(g, st);
@@ -820,7 +823,7 @@ int swiglu_parts(int M, int ngroups, int f) {
   return tile == 256 ? ((f + 127) / 128) * 2 : ((f + 63) / 64) * (tile == 128 ? 2 : 4);
 }
 
-int launch_swiglu_mfma(const MfmaArgs& g, hipStream_t st) {
+int launch_swiglu_mfma(const GmmArgs& g, hipStream_t st) {
   const int tile = swiglu_tile(g.M, g.ngroups);
   if (tile == 256) return launch_tile<MOE_GMM_FWD, EPI_SWIGLU, __bf16, 256, 256, 4, 2, 64, 2, 3>(g, st);
   if (tile == 128) return launch_tile<MOE_GMM_FWD, EPI_SWIGLU, __bf16, 128, 128, 2, 2, 64, 2, 3>(g, st);

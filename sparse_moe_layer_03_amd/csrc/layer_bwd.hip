@@ -27,14 +27,13 @@ __device__ __forceinline__ float block_max(float v, float* s) {
 template <typename T>
 __global__ void __launch_bounds__(256)
 swiglu_bwd_kernel(const float* __restrict__ zu, const float* __restrict__ dh0,
-                  const int32_t* __restrict__ perm, const float* __restrict__ gate,
-                  const int32_t* __restrict__ offsets, int n_ffn, int f, T* __restrict__ dzu,
-                  T* __restrict__ hs, float* __restrict__ part) {
+                  const float* __restrict__ gate_rows, const int32_t* __restrict__ offsets,
+                  int n_ffn, int f, T* __restrict__ dzu, T* __restrict__ hs,
+                  float* __restrict__ part) {
   __shared__ float s[4];
   const int p = blockIdx.x;  // gridDim.x = T * top_k
   if (p >= offsets[n_ffn]) return;
-  if (!MOE_GUARD((unsigned)perm[p] < gridDim.x, MOE_CHECK_GEMM_ROW)) return;
-  const float gt = gate[perm[p]];
+  const float gt = gate_rows[p];
   const float* zr = zu + (size_t)p * 2 * f;
   const float* dr = dh0 + (size_t)p * f;
   T* o = dzu + (size_t)p * 2 * f;
@@ -58,15 +57,63 @@ swiglu_bwd_kernel(const float* __restrict__ zu, const float* __restrict__ dh0,
   if (threadIdx.x == 0) part[p] = sum;
 }
 
-int launch_swiglu_bwd(int dtype, const float* zu, const float* dh, const int32_t* perm,
-                      const float* gate, const int32_t* offsets, int n_ffn, int Tk, int f,
-                      void* dzu, void* hs, float* dgate_part, hipStream_t st) {
+int launch_swiglu_bwd(int dtype, const float* zu, const float* dh, const float* gate_rows,
+                      const int32_t* offsets, int n_ffn, int Tk, int f, void* dzu, void* hs,
+                      float* dgate_part, hipStream_t st) {
   if (dtype == MOE_BF16)
-    hipLaunchKernelGGL(swiglu_bwd_kernel<__bf16>, dim3(Tk), dim3(256), 0, st, zu, dh, perm, gate,
+    hipLaunchKernelGGL(swiglu_bwd_kernel<__bf16>, dim3(Tk), dim3(256), 0, st, zu, dh, gate_rows,
                        offsets, n_ffn, f, (__bf16*)dzu, (__bf16*)hs, dgate_part);
   else
-    hipLaunchKernelGGL(swiglu_bwd_kernel<float>, dim3(Tk), dim3(256), 0, st, zu, dh, perm, gate,
+    hipLaunchKernelGGL(swiglu_bwd_kernel<float>, dim3(Tk), dim3(256), 0, st, zu, dh, gate_rows,
                        offsets, n_ffn, f, (float*)dzu, (float*)hs, dgate_part);
+  return check_launch();
+}
+
+// One wave per row, both arrays; four 16-byte pieces of each in flight a lane.
+template <typename T>
+__global__ void __launch_bounds__(256)
+gather2_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ gate,
+               const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets, int n_ffn,
+               int Tk, int k, int d, T* __restrict__ xp, T* __restrict__ dyp,
+               float* __restrict__ gate_rows) {
+  constexpr int CE = 16 / sizeof(T), U = 4;
+  const int lane = lane_id();
+  const int rows = min(offsets[n_ffn], Tk);
+  for (int p = blockIdx.x * 4 + (threadIdx.x >> 6); p < rows; p += gridDim.x * 4) {
+    const int at = __builtin_amdgcn_readfirstlane(perm[p]);
+    if (!MOE_GUARD((unsigned)at < (unsigned)Tk, MOE_CHECK_GEMM_ROW)) continue;
+    const size_t src = (size_t)(at / k) * d, dst = (size_t)p * d;
+    if (lane == 0) gate_rows[p] = gate[at];
+    const int chunks = d / CE;
+    for (int c0 = lane; c0 < chunks; c0 += 64 * U) {
+      u32x4_t vx[U], vy[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * 64;
+        if (c < chunks) vx[u] = ld16(x + src + c * CE), vy[u] = ld16(dy + src + c * CE);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * 64;
+        if (c < chunks) st16(xp + dst + c * CE, vx[u]), st16(dyp + dst + c * CE, vy[u]);
+      }
+    }
+  }
+}
+
+int launch_gather2(int dtype, const void* x, const void* dy, const float* gate, const int32_t* perm,
+                   const int32_t* offsets, int n_ffn, int Tk, int k, int d, void* xp, void* dyp,
+                   float* gate_rows, hipStream_t st) {
+  const int blocks = (int)(((long)Tk + 3) / 4);
+  const dim3 grid(blocks < 8192 ? blocks : 8192);
+  if (dtype == MOE_BF16)
+    hipLaunchKernelGGL(gather2_kernel<__bf16>, grid, dim3(256), 0, st, (const __bf16*)x,
+                       (const __bf16*)dy, gate, perm, offsets, n_ffn, Tk, k, d, (__bf16*)xp,
+                       (__bf16*)dyp, gate_rows);
+  else
+    hipLaunchKernelGGL(gather2_kernel<float>, grid, dim3(256), 0, st, (const float*)x,
+                       (const float*)dy, gate, perm, offsets, n_ffn, Tk, k, d, (float*)xp,
+                       (float*)dyp, gate_rows);
   return check_launch();
 }
 

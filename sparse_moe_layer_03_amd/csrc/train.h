@@ -9,68 +9,54 @@
 
 namespace moe {
 
-// One grouped product in the kernels' terms: out[i, j] = sum_r A(i, r) B(j, r)
+// Grouped products in the kernels' terms: out[i, j] = sum_r A(i, r) B(j, r)
 // for every group.  FWD and DX: i runs over the group's rows, r over R.  DW:
-// r runs over the group's rows, i over I.  j runs over J.
-struct GmmArgs {
-  const void* a;
-  const void* b;
-  void* out;
-  const int32_t* offsets;  // [ngroups + 1]
-  float* part;             // split reductions: fp32 partial outputs, split-major
-  int64_t lda, ldb, ldo;   // elements between rows of the arrays
-  int64_t b_group;         // elements between groups of b (FWD, DX)
-  int64_t out_group;       // elements between groups of out (DW)
-  int64_t part_stride;     // elements between splits in `part`
-  int ngroups;
-  int M;                   // rows that the row arrays hold
-  int I, J, R;             // extents (I: DW; R: FWD and DX)
-  int accumulate;
-  int nsplit;
-};
-
-// Any sizes, strides and element types.  vec: every row of a, b and out is
-// 16-byte aligned.
-int launch_gmm_general(int form, int dtype, int out_dtype, bool vec, const GmmArgs& g,
-                       hipStream_t st);
-// bf16 products on bf16 MFMAs (gmm_mfma.hip).  Up to three products over the
-// same groups in one launch (DW only; else one).
+// r runs over the group's rows, i over I.  j runs over J.  Up to three
+// products over the same groups share a launch (FWD: with the same a; DX:
+// one only).
 struct GmmSub {
   const void* a;
   const void* b;
   void* out;
-  int64_t lda, ldb, ldo;
+  int64_t lda, ldb, ldo;   // elements between rows of the arrays
   int I, J;
 };
-struct MfmaArgs {
+struct GmmArgs {
   GmmSub s[3];
   int nsub;
   int ngroups;
-  const int32_t* offsets;
-  int M;
-  int R;                 // FWD, DX: length of the reduction
-  int RB;                // DX: rows that a group of b holds (<= R; zeros behind)
-  int r_switch;          // DX: reduction rows from here on come from b2 (0: none)
-  const void* b2;        // DX: see r_switch; SwiGLU step: w_up
-  int64_t b_group, out_group;
-  float* part;
-  int64_t part_stride;
-  int nsplit;
+  const int32_t* offsets;  // [ngroups + 1]
+  int M;                   // rows that the row arrays hold
+  int R;                   // FWD, DX: length of the reduction
+  int RB;                  // DX: rows that a group of b holds (<= R; zeros behind)
+  int r_switch;            // DX: reduction rows from here on (a multiple of 64)
+                           // come from b2 (0: none)
+  const void* b2;          // DX: see r_switch; SwiGLU step: w_up
+  int64_t b_group;         // elements between groups of b (FWD, DX)
+  int64_t out_group;       // elements between groups of out (DW)
+  float* part;             // split reductions: fp32 partial outputs, split-major
+  int64_t part_stride;     // elements between splits in `part`
+  int nsplit;              // ranges of the reduction (> 1: one product only)
   int accumulate;
   // SwiGLU's backward step (FWD): z = a b^T, u = a b2^T
-  const int32_t* perm;
-  const float* gate;
-  const float* dh;       // [rows, J] fp32
-  void* dzu;             // [rows, 2 J]
-  void* hs;              // [rows, J]
-  float* dpart;          // [rows, swiglu_parts()]
+  const float* gate;       // per row
+  const float* dh;         // [rows, J] fp32
+  void* dzu;               // [rows, 2 J]
+  void* hs;                // [rows, J]
+  float* dpart;            // [rows, swiglu_parts()]
 };
+
+// Any sizes, strides and element types.  vec: rows of a and b start at
+// multiples of four elements.
+int launch_gmm_general(int form, int dtype, int out_dtype, bool vec, const GmmArgs& g,
+                       hipStream_t st);
+// bf16 products on bf16 MFMAs (gmm_mfma.hip; FWD: one product).
 constexpr int kMfmaMaxRows = 1 << 29;  // row tiles are counted in 22 bits
 // Whether a product can run there: 16-byte rows and row starts, and sizes
 // that 32-bit offsets within a tile reach.
 bool mfma_ok(int form, int dtype, int N, int K, int64_t lda, int64_t ldc);
-int launch_gmm_mfma(int form, int out_dtype, const MfmaArgs& g, hipStream_t st);
-int launch_swiglu_mfma(const MfmaArgs& g, hipStream_t st);
+int launch_gmm_mfma(int form, int out_dtype, const GmmArgs& g, hipStream_t st);
+int launch_swiglu_mfma(const GmmArgs& g, hipStream_t st);
 int swiglu_parts(int M, int ngroups, int f);  // partial sums of dgate per row
 
 // Sums `part` into out (rounded, added to when accumulating).
@@ -88,12 +74,18 @@ uint64_t adamw_max_elements();
 
 unsigned check_word_layer_bwd(bool clear);  // as the accessors of internal.h
 
+// The FFN rows of x and dy grouped by expert, and their gates: for p <
+// offsets[n_ffn], row perm[p] / k of each, gate_rows[p] = gate[perm[p]].
+int launch_gather2(int dtype, const void* x, const void* dy, const float* gate, const int32_t* perm,
+                   const int32_t* offsets, int n_ffn, int Tk, int k, int d, void* xp, void* dyp,
+                   float* gate_rows, hipStream_t st);
+
 // Per FFN row p: h, dz, du from z, u and dh (fp32 [rows, f], z and u in
 // `zu` [rows, 2 f]), the row's gate applied; dzu [rows, 2 f] and hs
 // [rows, f] in dtype, dgate_part[p] = <dh, h>.
-int launch_swiglu_bwd(int dtype, const float* zu, const float* dh, const int32_t* perm,
-                      const float* gate, const int32_t* offsets, int n_ffn, int Tk, int f,
-                      void* dzu, void* hs, float* dgate_part, hipStream_t st);
+int launch_swiglu_bwd(int dtype, const float* zu, const float* dh, const float* gate_rows,
+                      const int32_t* offsets, int n_ffn, int Tk, int f, void* dzu, void* hs,
+                      float* dgate_part, hipStream_t st);
 
 // Per token: dgate (parts: partial sums per FFN row), then, with logits, dlogits (fp32 if not
 // null, and in dtype with rows of ep elements, zeros behind E) and the row

@@ -55,47 +55,32 @@ static size_t gmm_part_bytes(const moe_gmm_shape* s, int nsplit) {
   return up256(out * nsplit * sizeof(float));
 }
 
-// Runs one product, its split reduction joined.  rb: rows that a group of b
-// holds (DX), when fewer than the reduction's length.
-static int run_gmm(int form, int dtype, int out_dtype, const GmmArgs& g, hipStream_t st, int rb = 0) {
-  const bool dw = form == MOE_GMM_DW;
-  const int64_t lda = form == MOE_GMM_DX ? g.ldo : dw ? g.ldb : g.lda;
-  const int64_t ldc = form == MOE_GMM_FWD ? g.ldo : g.lda;
-  // DW loads whole chunks of c's rows: a row's gap holds what a chunk has
-  // beyond N when the caller says so (rb)
-  const int N = form == MOE_GMM_FWD ? g.J : dw ? (rb ? rb : g.I) : g.R;
-  const int K = form == MOE_GMM_FWD ? g.R : g.J;
-  int rc;
-  if (g.M < kMfmaMaxRows && mfma_ok(form, dtype, N, K, lda, ldc) && al16(g.a) && al16(g.b) && al16(g.out)) {
-    MfmaArgs m{};
-    m.s[0] = {g.a, g.b, g.out, g.lda, g.ldb, g.ldo, g.I, g.J};
-    m.nsub = 1;
-    m.ngroups = g.ngroups;
-    m.offsets = g.offsets;
-    m.M = g.M;
-    m.R = g.R;
-    m.RB = form == MOE_GMM_DX && rb ? rb : g.R;
-    m.b_group = g.b_group;
-    m.out_group = g.out_group;
-    m.part = g.part;
-    m.part_stride = g.part_stride;
-    m.nsplit = g.nsplit;
-    m.accumulate = g.accumulate;
-    rc = launch_gmm_mfma(form, out_dtype, m, st);
-  } else {
-    const bool vec = g.lda % 4 == 0 && g.ldb % 4 == 0 && g.b_group % 4 == 0 && al16(g.a) && al16(g.b);
-    rc = launch_gmm_general(form, dtype, out_dtype, vec, g, st);
+// Runs products, a split reduction joined.  DW loads whole 8-element chunks of
+// c's rows; `padded`: their gaps hold zeros (else N has to be whole chunks).
+static int run_gmm(int form, int dtype, int out_dtype, const GmmArgs& g, hipStream_t st,
+                   bool padded = false) {
+  const bool fwd = form == MOE_GMM_FWD, dx = form == MOE_GMM_DX;
+  bool mfma = g.M < kMfmaMaxRows && !(fwd && g.nsub > 1), vec = g.b_group % 4 == 0;
+  for (int q = 0; q < g.nsub; ++q) {
+    const GmmSub& s = g.s[q];
+    const int64_t lda = dx ? s.ldo : fwd ? s.lda : s.ldb, ldc = fwd ? s.ldo : s.lda;
+    const int N = fwd ? s.J : dx ? g.R : padded ? (s.I + 7) & ~7 : s.I, K = fwd ? g.R : s.J;
+    const bool al = al16(s.a) && al16(s.b);
+    mfma = mfma && al && al16(s.out) && mfma_ok(form, dtype, N, K, lda, ldc);
+    vec = vec && al && s.lda % 4 == 0 && s.ldb % 4 == 0;
   }
+  const int rc = mfma ? launch_gmm_mfma(form, out_dtype, g, st)
+                      : launch_gmm_general(form, dtype, out_dtype, vec, g, st);
   if (rc || g.nsplit <= 1) return rc;
   return launch_gmm_join(form, out_dtype, g, st);
 }
 
 // ---- the layer's backward pass: workspace
 
-constexpr int kRouteSplits = 16;  // token ranges of the router's weight gradient
+constexpr int kRouteSplits = 16;  // most token ranges of the router's weight gradient
 
 struct BwdLayout {
-  size_t xp, dyp, zu, dh, dzu, hs, part, dl, offs, dxr, drp, total;
+  size_t xp, dyp, gates, zu, dh, dzu, hs, part, dl, offs, dxr, drp, total;
   int ep, nsplit, parts;
   bool mfma;  // the bf16 kernels, with SwiGLU's step in the products' epilogue
 };
@@ -106,8 +91,12 @@ static BwdLayout bwd_layout(const moe_shape* s) {
   const size_t d = s->d_model, f = s->d_ff;
   BwdLayout w;
   w.ep = (int)((E + 7) & ~(size_t)7);
-  w.nsplit = (int)std::max(1l, std::min((long)kRouteSplits, (long)s->T / 256));
-  w.mfma = s->dtype == MOE_BF16 && s->d_model < (1 << 20) && s->d_ff < (1 << 20) &&
+  // the router's weight gradient has few tiles and a reduction over all
+  // tokens: as many ranges of at least 256 of them as give every CU a tile
+  const int cus = device_cu_count();
+  w.nsplit = (int)std::max(1l, std::min({(long)kRouteSplits, (long)s->T / 256,
+                                         (cus > 0 ? cus : 256) / (cdiv(E, 256) * cdiv(d, 256))}));
+  w.mfma = s->dtype == MOE_BF16 && s->d_model < (1 << 20) && s->d_ff < (1 << 19) &&
            rows < kMfmaMaxRows;
   w.parts = w.mfma ? swiglu_parts((int)rows, s->n_ffn, s->d_ff) : 1;
   size_t off = 0;
@@ -118,6 +107,7 @@ static BwdLayout bwd_layout(const moe_shape* s) {
   };
   w.xp = take(rows * d * es);
   w.dyp = take(rows * d * es);
+  w.gates = take(rows * 4);
   w.zu = take(w.mfma ? 0 : rows * 2 * f * 4);
   w.dh = take(rows * f * 4);
   w.dzu = take(rows * 2 * f * es);
@@ -126,7 +116,7 @@ static BwdLayout bwd_layout(const moe_shape* s) {
   w.dl = take((size_t)s->T * w.ep * es);
   w.offs = take((2 + kRouteSplits + 1) * sizeof(int32_t));
   w.dxr = take((size_t)s->T * d * 4);
-  w.drp = take(E * d * 4 * w.nsplit);
+  w.drp = take(w.nsplit > 1 ? E * d * 4 * w.nsplit : 0);
   w.total = off;
   return w;
 }
@@ -176,41 +166,42 @@ int moe_grouped_matmul(const moe_gmm_shape* s, const int32_t* offsets, const voi
   const int cus = device_cu_count();
   if (cus <= 0) return MOE_EHIP;
   GmmArgs g{};
-  g.a = lhs;
-  g.b = rhs;
-  g.out = out;
+  g.nsub = 1;
   g.offsets = offsets;
   g.ngroups = s->n_groups;
   g.M = s->M;
-  g.I = s->N;
+  g.b_group = g.out_group = (int64_t)s->N * s->K;
   g.accumulate = s->accumulate != 0;
   g.nsplit = gmm_splits_of(s, cus);
   if (g.nsplit > 1 && !ws) return MOE_EINVAL;
   g.part = (float*)ws;
+  GmmSub& p = g.s[0];
+  p.a = lhs;
+  p.b = rhs;
+  p.out = out;
+  p.I = s->N;
   if (s->form == MOE_GMM_FWD) {
-    g.lda = s->lda;
-    g.ldb = s->K;
-    g.ldo = s->ldc;
-    g.b_group = (int64_t)s->N * s->K;
-    g.J = s->N;
+    p.lda = s->lda;
+    p.ldb = s->K;
+    p.ldo = s->ldc;
+    p.J = s->N;
     g.R = s->K;
     g.part_stride = (int64_t)s->M * s->N;
   } else if (s->form == MOE_GMM_DX) {
-    g.lda = s->ldc;
-    g.ldb = s->K;
-    g.ldo = s->lda;
-    g.b_group = (int64_t)s->N * s->K;
-    g.J = s->K;
+    p.lda = s->ldc;
+    p.ldb = s->K;
+    p.ldo = s->lda;
+    p.J = s->K;
     g.R = s->N;
     g.part_stride = (int64_t)s->M * s->K;
   } else {
-    g.lda = s->ldc;
-    g.ldb = s->lda;
-    g.ldo = s->K;
-    g.out_group = (int64_t)s->N * s->K;
-    g.J = s->K;
+    p.lda = s->ldc;
+    p.ldb = s->lda;
+    p.ldo = s->K;
+    p.J = s->K;
     g.part_stride = (int64_t)s->n_groups * s->N * s->K;
   }
+  g.RB = g.R;
   if (none && !dw) return MOE_OK;
   return run_gmm(s->form, s->dtype, s->out_dtype, g, (hipStream_t)stream);
 }
@@ -236,10 +227,10 @@ int moe_layer_backward(const moe_shape* s, const moe_backward_io* io, void* ws, 
   char* dl = base + w.dl;
   int32_t *route_offs = (int32_t*)(base + w.offs), *split_offs = route_offs + 2;
 
-  // the FFN rows of x and dy, grouped by expert
-  if ((rc = launch_gather(dt, io->x, io->perm, io->offsets, s->n_ffn, Tk, s->top_k, d, xp, st)))
-    return rc;
-  if ((rc = launch_gather(dt, io->dy, io->perm, io->offsets, s->n_ffn, Tk, s->top_k, d, dyp, st)))
+  float* gates = (float*)(base + w.gates);
+  const int acc = io->accumulate != 0;
+  if ((rc = launch_gather2(dt, io->x, io->dy, io->topk_gate, io->perm, io->offsets, s->n_ffn, Tk,
+                           s->top_k, d, xp, dyp, gates, st)))
     return rc;
 
   GmmArgs g{};
@@ -247,73 +238,47 @@ int moe_layer_backward(const moe_shape* s, const moe_backward_io* io, void* ws, 
   g.ngroups = s->n_ffn;
   g.M = Tk;
   g.nsplit = 1;
-  auto product = [&](int form, int out_dtype, const void* a, int64_t lda, const void* b, int64_t ldb,
-                     void* out, int64_t ldo, int I, int J, int R, int accumulate) {
-    g.a = a;
-    g.lda = lda;
-    g.b = b;
-    g.ldb = ldb;
-    g.out = out;
-    g.ldo = ldo;
-    g.b_group = (int64_t)d * f;
-    g.out_group = (int64_t)d * f;
-    g.I = I;
-    g.J = J;
-    g.R = R;
-    g.accumulate = accumulate;
-    return run_gmm(form, dt, out_dtype, g, st);
-  };
-  const int acc = io->accumulate != 0;
-  char* dx_perm = xp;  // over x's rows, once they are not needed any more
+  g.b_group = g.out_group = (int64_t)d * f;
+  // the gradient at H, before the gate
+  g.nsub = 1;
+  g.s[0] = {dyp, io->w_down, dh, d, f, f, 0, f};
+  g.R = g.RB = d;
+  if ((rc = run_gmm(MOE_GMM_DX, dt, MOE_F32, g, st))) return rc;
+  // z and u again, and SwiGLU's step
   if (w.mfma) {
-    // the gradient at H, then z and u again with SwiGLU's step behind them
-    if ((rc = product(MOE_GMM_DX, MOE_F32, dyp, d, io->w_down, f, dh, f, 0, f, d, 0))) return rc;
-    MfmaArgs m{};
-    m.nsub = 1;
-    m.ngroups = s->n_ffn;
-    m.offsets = io->offsets;
-    m.M = Tk;
-    m.R = m.RB = d;
-    m.b_group = m.out_group = (int64_t)d * f;
-    m.nsplit = 1;
-    m.s[0] = {xp, io->w_gate, nullptr, d, d, 0, 0, f};
-    m.b2 = io->w_up;
-    m.perm = io->perm;
-    m.gate = io->topk_gate;
-    m.dh = dh;
-    m.dzu = dzu;
-    m.hs = hs;
-    m.dpart = part;
-    if ((rc = launch_swiglu_mfma(m, st))) return rc;
-    // gradients of the experts' weights, in one launch
-    m.nsub = 3;
-    m.s[0] = {dzu, xp, io->dw_gate, 2 * f, d, d, f, d};
-    m.s[1] = {dzu + (size_t)f * es, xp, io->dw_up, 2 * f, d, d, f, d};
-    m.s[2] = {dyp, hs, io->dw_down, d, f, f, d, f};
-    m.accumulate = acc;
-    if ((rc = launch_gmm_mfma(MOE_GMM_DW, dt, m, st))) return rc;
-    // gradients of the rows: one reduction over gate's and up's columns
-    m.nsub = 1;
-    m.s[0] = {dzu, io->w_gate, dx_perm, 2 * f, d, d, 0, d};
-    m.b2 = io->w_up;
-    m.R = m.RB = 2 * f;
-    m.r_switch = f;
-    m.accumulate = 0;
-    if ((rc = launch_gmm_mfma(MOE_GMM_DX, dt, m, st))) return rc;
+    g.s[0] = {xp, io->w_gate, nullptr, d, d, 0, 0, f};
+    g.b2 = io->w_up;
+    g.gate = gates;
+    g.dh = dh;
+    g.dzu = dzu;
+    g.hs = hs;
+    g.dpart = part;
+    if ((rc = launch_swiglu_mfma(g, st))) return rc;
   } else {
-    if ((rc = product(MOE_GMM_FWD, MOE_F32, xp, d, io->w_gate, d, zu, 2 * f, 0, f, d, 0))) return rc;
-    if ((rc = product(MOE_GMM_FWD, MOE_F32, xp, d, io->w_up, d, zu + f, 2 * f, 0, f, d, 0))) return rc;
-    if ((rc = product(MOE_GMM_DX, MOE_F32, dyp, d, io->w_down, f, dh, f, 0, f, d, 0))) return rc;
-    if ((rc = launch_swiglu_bwd(dt, zu, dh, io->perm, io->topk_gate, io->offsets, s->n_ffn, Tk, f,
-                                dzu, hs, part, st)))
+    g.nsub = 2;
+    g.s[0] = {xp, io->w_gate, zu, d, d, 2 * f, 0, f};
+    g.s[1] = {xp, io->w_up, zu + f, d, d, 2 * f, 0, f};
+    if ((rc = run_gmm(MOE_GMM_FWD, dt, MOE_F32, g, st))) return rc;
+    if ((rc = launch_swiglu_bwd(dt, zu, dh, gates, io->offsets, s->n_ffn, Tk, f, dzu, hs, part, st)))
       return rc;
-    char* du = dzu + (size_t)f * es;
-    if ((rc = product(MOE_GMM_DW, dt, dzu, 2 * f, xp, d, io->dw_gate, d, f, d, 0, acc))) return rc;
-    if ((rc = product(MOE_GMM_DW, dt, du, 2 * f, xp, d, io->dw_up, d, f, d, 0, acc))) return rc;
-    if ((rc = product(MOE_GMM_DW, dt, dyp, d, hs, f, io->dw_down, f, d, f, 0, acc))) return rc;
-    if ((rc = product(MOE_GMM_DX, dt, dzu, 2 * f, io->w_gate, d, dx_perm, d, 0, d, f, 0))) return rc;
-    if ((rc = product(MOE_GMM_DX, dt, du, 2 * f, io->w_up, d, dx_perm, d, 0, d, f, 1))) return rc;
   }
+  // gradients of the experts' weights
+  g.nsub = 3;
+  g.s[0] = {dzu, xp, io->dw_gate, 2 * f, d, d, f, d};
+  g.s[1] = {dzu + (size_t)f * es, xp, io->dw_up, 2 * f, d, d, f, d};
+  g.s[2] = {dyp, hs, io->dw_down, d, f, f, d, f};
+  g.accumulate = acc;
+  if ((rc = run_gmm(MOE_GMM_DW, dt, dt, g, st))) return rc;
+  // gradients of the rows, one reduction over gate's and up's columns, over
+  // x's rows, which are not needed any more
+  char* dx_perm = xp;
+  g.nsub = 1;
+  g.s[0] = {dzu, io->w_gate, dx_perm, 2 * f, d, d, 0, d};
+  g.b2 = io->w_up;
+  g.R = g.RB = 2 * f;
+  g.r_switch = f;
+  g.accumulate = 0;
+  if ((rc = run_gmm(MOE_GMM_DX, dt, dt, g, st))) return rc;
 
   // gradients at the gates and logits, and the router's products
   TokenArgs a{};
@@ -340,35 +305,36 @@ int moe_layer_backward(const moe_shape* s, const moe_backward_io* io, void* ws, 
   if ((rc = launch_token_bwd(dt, a, st))) return rc;
   if (io->logits) {
     GmmArgs r{};
-    r.a = dl;
-    r.lda = w.ep;
+    r.nsub = 1;
     r.M = s->T;
     r.nsplit = 1;
-    // dlogits W_router, fp32
-    r.b = io->w_router;
-    r.ldb = d;
-    r.out = dxr;
-    r.ldo = d;
+    // dlogits W_router, fp32 (dlogits' rows have zeros behind E, where
+    // w_router has none)
+    r.s[0] = {dl, io->w_router, dxr, w.ep, d, d, 0, d};
     r.offsets = route_offs;
     r.ngroups = 1;
-    r.J = d;
-    r.R = w.mfma ? w.ep : E;  // zeros behind E, where w_router has no rows
-    if ((rc = run_gmm(MOE_GMM_DX, dt, MOE_F32, r, st, E))) return rc;
-    // dlogits^T x over ranges of the tokens, joined
-    r.b = io->x;
-    r.out = drp;
+    r.R = w.ep;
+    r.RB = E;
+    if ((rc = run_gmm(MOE_GMM_DX, dt, MOE_F32, r, st))) return rc;
+    // dlogits^T x, over ranges of the tokens that are joined
+    r.s[0] = {dl, io->x, w.nsplit > 1 ? (void*)drp : io->dw_router, w.ep, d, d, E, d};
     r.out_group = (int64_t)E * d;
     r.offsets = split_offs;
     r.ngroups = w.nsplit;
-    r.I = E;
-    if ((rc = run_gmm(MOE_GMM_DW, dt, MOE_F32, r, st, w.ep))) return rc;
-    r.part = drp;
-    r.part_stride = (int64_t)E * d;
-    r.nsplit = w.nsplit;
-    r.ngroups = 1;
-    r.out = io->dw_router;
-    r.accumulate = acc;
-    if ((rc = launch_gmm_join(MOE_GMM_DW, dt, r, st))) return rc;
+    if (w.nsplit > 1) {
+      if ((rc = run_gmm(MOE_GMM_DW, dt, MOE_F32, r, st, true))) return rc;
+      r.part = drp;
+      r.part_stride = (int64_t)E * d;
+      r.nsplit = w.nsplit;
+      r.ngroups = 1;
+      r.s[0].out = io->dw_router;
+      r.accumulate = acc;
+      rc = launch_gmm_join(MOE_GMM_DW, dt, r, st);
+    } else {
+      r.accumulate = acc;
+      rc = run_gmm(MOE_GMM_DW, dt, dt, r, st, true);
+    }
+    if (rc) return rc;
   }
   return launch_dx(dt, dx_perm, io->dy, io->logits ? dxr : nullptr, io->topk_idx, io->topk_gate,
                    io->inv_perm, s->T, d, s->top_k, s->n_ffn, io->dx, st);

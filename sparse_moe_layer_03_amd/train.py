@@ -104,25 +104,30 @@ def _need(name, t, dtype, numel, device=None):
 
 def _rows(name, t, dtype, rows, width, ld, device):
     """t holds `rows` rows of `width` elements, `ld` elements apart."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.device != device:
         raise ValueError(f"{name}: a tensor on {device} is needed")
     if t.dtype != dtype:
         raise ValueError(f"{name}: {t.dtype}, needed {dtype}")
-    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != width or \
-            (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) != ld):
-        raise ValueError(f"{name}: shape {tuple(t.shape)} strides {tuple(t.stride())}, needed "
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] < rows or shape[1] != width or \
+            (width > 1 and stride[1] != 1) or (shape[0] > 1 and stride[0] != ld):
+        raise ValueError(f"{name}: shape {tuple(shape)} strides {stride}, needed "
                          f"[{rows}, {width}] with strides ({ld}, 1)")
 
 
 def _workspace(ws, need, device):
-    if need and (ws is None or not ws.is_cuda or ws.device != device or not ws.is_contiguous()
+    if need and (ws is None or ws.device != device or not ws.is_contiguous()
                  or ws.numel() * ws.element_size() < need):
         raise ValueError(f"ws: {need} bytes on {device} are needed")
 
 
-def _on(device, stream):
-    """The stream's handle: the device's current stream by default."""
-    return B._stream(torch.cuda.current_stream(device) if stream is None else stream)
+def _on(device, call, stream):
+    """call(stream's handle) with `device` as the current one; the stream is
+    the device's current one by default."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return call(B._stream(stream))
+    return call(B._stream(stream))
 
 
 # ---- grouped products
@@ -145,22 +150,30 @@ def moe_grouped_matmul_workspace_bytes(shape: MoeGmmShape) -> int:
 def moe_grouped_matmul(shape: MoeGmmShape, offsets, lhs, rhs, out, ws=None, stream=None):
     """fwd: out[p] = lhs[p] W_e^T; dx: out[p] = lhs[p] W_e; dw: out[e] = sum
     over the rows p of e of lhs[p]^T rhs[p] (W = rhs, or out)."""
-    s, dev = shape, offsets.device
+    s = shape
     _need("offsets", offsets, torch.int32, s.n_groups + 1)
-    if s.dtype in _DTYPE and s.out_dtype in _DTYPE and s.form in (0, 1, 2):
-        dt, od, nk = _DTYPE[s.dtype], _DTYPE[s.out_dtype], s.n_groups * s.N * s.K
-        a = dict(rows=s.M, width=s.K, ld=s.lda, device=dev)
-        c = dict(rows=s.M, width=s.N, ld=s.ldc, device=dev)
-        if s.form == MOE_GMM_FWD:
-            _rows("lhs", lhs, dt, **a), _need("rhs", rhs, dt, nk, dev), _rows("out", out, od, **c)
-        elif s.form == MOE_GMM_DX:
-            _rows("lhs", lhs, dt, **c), _need("rhs", rhs, dt, nk, dev), _rows("out", out, od, **a)
+    dev, form, M, N, K = offsets.device, s.form, s.M, s.N, s.K
+    if s.dtype in _DTYPE and s.out_dtype in _DTYPE and form in (0, 1, 2):
+        dt, od, nk = _DTYPE[s.dtype], _DTYPE[s.out_dtype], s.n_groups * N * K
+        if form == MOE_GMM_FWD:
+            _rows("lhs", lhs, dt, M, K, s.lda, dev)
+            _need("rhs", rhs, dt, nk, dev)
+            _rows("out", out, od, M, N, s.ldc, dev)
+        elif form == MOE_GMM_DX:
+            _rows("lhs", lhs, dt, M, N, s.ldc, dev)
+            _need("rhs", rhs, dt, nk, dev)
+            _rows("out", out, od, M, K, s.lda, dev)
         else:
-            _rows("lhs", lhs, dt, **c), _rows("rhs", rhs, dt, **a), _need("out", out, od, nk, dev)
-    with torch.cuda.device(dev):
+            _rows("lhs", lhs, dt, M, N, s.ldc, dev)
+            _rows("rhs", rhs, dt, M, K, s.lda, dev)
+            _need("out", out, od, nk, dev)
+
+    def call(st):
         _workspace(ws, moe_grouped_matmul_workspace_bytes(s), dev)
-        B._check("moe_grouped_matmul", lib().moe_grouped_matmul(
-            ctypes.byref(s), B._p(offsets), B._p(lhs), B._p(rhs), B._p(out), B._p(ws), _on(dev, stream)))
+        return lib().moe_grouped_matmul(ctypes.byref(s), B._p(offsets), B._p(lhs), B._p(rhs),
+                                        B._p(out), B._p(ws), st)
+
+    B._check("moe_grouped_matmul", _on(dev, call, stream))
 
 
 # ---- the layer's backward pass
@@ -204,10 +217,12 @@ def moe_layer_backward_workspace_bytes(shape: B.MoeShape) -> int:
 def moe_layer_backward(shape: B.MoeShape, io: BackwardIO, ws, stream=None):
     io.check(shape)
     dev = io.tensors["x"].device
-    with torch.cuda.device(dev):
+
+    def call(st):
         _workspace(ws, moe_layer_backward_workspace_bytes(shape), dev)
-        B._check("moe_layer_backward", lib().moe_layer_backward(
-            ctypes.byref(shape), ctypes.byref(io.c), B._p(ws), _on(dev, stream)))
+        return lib().moe_layer_backward(ctypes.byref(shape), ctypes.byref(io.c), B._p(ws), st)
+
+    B._check("moe_layer_backward", _on(dev, call, stream))
 
 
 # ---- AdamW
@@ -266,10 +281,9 @@ def moe_adamw(params: MoeAdamwParams, tensors: AdamwTensors, state, grad_scale=N
     for name, t in (("grad_scale", grad_scale), ("lr_scale", lr_scale)):
         if t is not None:
             _need(name, t, torch.float32, 1, dev)
-    with torch.cuda.device(dev):
-        B._check("moe_adamw", lib().moe_adamw(
-            ctypes.byref(params), tensors.c, len(tensors.tensors), B._p(state), B._p(grad_scale),
-            B._p(lr_scale), _on(dev, stream)))
+    B._check("moe_adamw", _on(dev, lambda st: lib().moe_adamw(
+        ctypes.byref(params), tensors.c, len(tensors.tensors), B._p(state), B._p(grad_scale),
+        B._p(lr_scale), st), stream))
 
 
 # ---- a training step of the layer
