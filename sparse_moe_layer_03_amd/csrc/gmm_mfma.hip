@@ -41,6 +41,7 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 
 constexpr int kMfmaMaxGroups = 1024;
+constexpr int kCpolNT = 2;  // cache policy of a load: non-temporal
 constexpr uint32_t kOutside = 0x7ffffff0u;  // a buffer offset behind every descriptor's end
 enum { EPI_STORE = 0, EPI_SWIGLU = 1 };
 
@@ -178,7 +179,7 @@ gmm_mfma_kernel(GmmArgs g) {
   // (vmcnt counts to 63; 0: every load waits for the stores before it)
   constexpr int NST = SW || NST_ALL + DB * PW > 63 ? 0 : NST_ALL;
   static_assert(A_PW >= 1 && B_PW >= 1 && (!SW || (NB % 2 == 0 && B_PW % 2 == 0)), "tile");
-  static_assert(TA::BYTES > kMfmaMaxGroups * 4, "the groups' prefix fits a stage");
+  static_assert(TB::BYTES > kMfmaMaxGroups * 4, "the groups' prefix fits a stage");
 
   // Rings of SA and SB stages, one array each: the compiler then sees that the
   // stage being read is not one being filled.  Loads of a are DA steps ahead,
@@ -214,8 +215,8 @@ gmm_mfma_kernel(GmmArgs g) {
   uint32_t desc = 0;
   long tiles = 0;
   auto describe = [&](int k0) {
-    int* s_pref = reinterpret_cast<int*>(s_a0);
-    int* s_scan = reinterpret_cast<int*>(s_a1);
+    int* s_pref = reinterpret_cast<int*>(s_b0);
+    int* s_scan = reinterpret_cast<int*>(s_b1);
     constexpr int PER = (kMfmaMaxGroups + NT - 1) / NT;
     int loc[PER], run = 0;
 #pragma unroll
@@ -260,6 +261,7 @@ gmm_mfma_kernel(GmmArgs g) {
     const char *a_base, *b_base, *b_base2;
     uint32_t a_bytes, b_bytes;  // OUT: of a row's part; RED: of the tile
     uint32_t lda2, ldb2;        // bytes between rows
+    bool once;                  // no other tile reads this tile's part of b
   };
   // lane offsets of the first load instructions of each kind, in the tile
   // whose loads go out
@@ -335,6 +337,7 @@ gmm_mfma_kernel(GmmArgs g) {
       t.j0 = (in / mg) * HN;
       const int h = ((t.rows + mt - 1) / mt + 15) & ~15;  // balanced height
       t.i0 = (m0 + in % mg) * h;
+      t.once = mt == 1;
       t.i_end = min(t.rows, t.i0 + h);
     }
     t.e = uni(t.e), t.i0 = uni(t.i0), t.i_end = uni(t.i_end), t.j0 = uni(t.j0);
@@ -398,7 +401,8 @@ gmm_mfma_kernel(GmmArgs g) {
                                                0);
     }
   };
-  auto load_b = [&](const Place& t, auto sc, int ks, int q) {
+  auto load_b1 = [&](const Place& t, auto sc, int ks, int q, auto cache) {
+    constexpr int AUX = decltype(cache)::value;
     char* dst = stage_b(sc) + (wave + q * NW) * 1024;
     // SwiGLU step: gate rows fill the first half of the tile, up rows the second
     const bool second = SW && q >= B_PW / 2;
@@ -410,7 +414,7 @@ gmm_mfma_kernel(GmmArgs g) {
       uint32_t off = b_off[h % TB::NP];
       if (left < KS) off = TB::chunk(q, wave, lane) * 8 < left ? off : kOutside;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)off, ks * KS * 2 + add, 0,
-                                               0);
+                                               AUX);
     } else {
       int r = ks * KS;
       // rows of b that this step has (w_router ends before dlogits' padding)
@@ -423,7 +427,20 @@ gmm_mfma_kernel(GmmArgs g) {
       const auto rs = descriptor(base + (int64_t)r * t.ldb2,
                                  left > 0 ? (uint32_t)(left - 1) * t.ldb2 + t.b_bytes : 0u);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)b_off[h % TB::NP], add,
-                                               0, 0);
+                                               0, AUX);
+    }
+  };
+
+  // The step's b loads.  Weights that one tile reads are loaded non-temporally:
+  // they need not stay in the caches (few rows per expert: 600 -> 549 us over
+  // 256 experts' 3.2 GB).
+  auto load_b = [&](const Place& t, auto sc, int ks) {
+    if (!DW && t.once) {
+#pragma unroll
+      for (int q = 0; q < B_PW; ++q) load_b1(t, sc, ks, q, std::integral_constant<int, kCpolNT>{});
+    } else {
+#pragma unroll
+      for (int q = 0; q < B_PW; ++q) load_b1(t, sc, ks, q, std::integral_constant<int, 0>{});
     }
   };
 
@@ -446,11 +463,8 @@ gmm_mfma_kernel(GmmArgs g) {
             load_a(t, std::integral_constant<int, V + DA>{}, t.k_lo + V + DA, q);
         }
       }
-      if (t.k_lo + V + DB < t.k_hi) {
-#pragma unroll
-        for (int q = 0; q < B_PW; ++q)
-          load_b(t, std::integral_constant<int, V + DB>{}, t.k_lo + V + DB, q);
-      }
+      if (t.k_lo + V + DB < t.k_hi)
+        load_b(t, std::integral_constant<int, V + DB>{}, t.k_lo + V + DB);
     };
     one(std::integral_constant<int, 0>{});
     if constexpr (DB > 1) one(std::integral_constant<int, 1>{});
@@ -521,10 +535,8 @@ gmm_mfma_kernel(GmmArgs g) {
 #pragma unroll
           for (int q = 0; q < A_PW; ++q) load_a(t, std::integral_constant<int, N + DA>{}, ks + DA, q);
         }
-        if (kk == KS / 32 - 1 && behind >= DB) {
-#pragma unroll
-          for (int q = 0; q < B_PW; ++q) load_b(t, std::integral_constant<int, N + DB>{}, ks + DB, q);
-        }
+        if (kk == KS / 32 - 1 && behind >= DB)
+          load_b(t, std::integral_constant<int, N + DB>{}, ks + DB);
 #pragma unroll
         for (int i = 0; i < MBA; ++i)
 #pragma unroll
@@ -778,27 +790,41 @@ static int launch_tile(const GmmArgs& g, hipStream_t st) {
   return check_launch();
 }
 
-// Tile choice: by the rows a group has on average (FWD, DX) and whether the
-// larger tiles fill the chip.
+// Tile choice.  FWD and DX go by the rows a group has on average (measured
+// over 256 groups of W [1536, 4096], us):
+//   rows        8    47    64   100   127   128   256
+//   FWD  64x128 566  613   609  774          64-row tiles below 64 rows
+//       128x128       659   669  730   748   754    then 128
+//       256x256                              762   850   then 256
+//   DX   64x256 483  548   564  890          256 columns: an OUT tile's rows
+//       128x256       544   557  611   645          are 512 bytes of W
+//       256x256                              676   850
+// DW has 256 x 256 tiles, in steps of 32 (256 groups of 39 ragged rows: 847
+// us, steps of 64: 1034; 128 x 128 tiles 1210).  Where the largest tiles leave
+// CUs idle, 128 x 128.
 template <int FORM, typename TO>
 static int launch_form(const GmmArgs& g, hipStream_t st) {
   const int cus = stream_cu_count(st);
   if (cus <= 0) return MOE_EHIP;
+  const long per = g.M / g.ngroups;
+  long t256 = 0;  // 256 x 256 tiles, at most
+  for (int q = 0; q < g.nsub; ++q)
+    t256 += (long)((g.s[q].J + 255) / 256) * (FORM == MOE_GMM_DW ? (g.s[q].I + 255) / 256 : 1);
+  t256 *= g.nsplit * (FORM == MOE_GMM_DW ? (long)g.ngroups
+                                         : g.M / 256 + (g.M < g.ngroups ? g.M : g.ngroups));
   if constexpr (FORM == MOE_GMM_DW) {
-    long t = 0;
-    for (int q = 0; q < g.nsub; ++q)
-      t += (long)((g.s[q].I + 255) / 256) * ((g.s[q].J + 255) / 256);
-    if (t * g.ngroups * g.nsplit >= cus)
-      return launch_tile<FORM, EPI_STORE, TO, 256, 256, 4, 2, 32, 4, 4>(g, st);
+    if (t256 >= cus) return launch_tile<FORM, EPI_STORE, TO, 256, 256, 4, 2, 32, 4, 4>(g, st);
     return launch_tile<FORM, EPI_STORE, TO, 128, 128, 2, 2, 32, 4, 4>(g, st);
-  }
-  else {
-    const long per = g.M / g.ngroups;
-    const long t256 = (g.M / 256 + (g.M < g.ngroups ? g.M : g.ngroups)) * ((g.s[0].J + 255) / 256);
-    if (per >= 128 && t256 * g.nsplit >= cus)
+  } else {
+    if (per >= 128 && t256 >= cus)
       return launch_tile<FORM, EPI_STORE, TO, 256, 256, 4, 2, 64, 2, 3>(g, st);
-    if (per >= 48) return launch_tile<FORM, EPI_STORE, TO, 128, 128, 2, 2, 64, 2, 3>(g, st);
-    return launch_tile<FORM, EPI_STORE, TO, 64, 128, 1, 4, 64, 3, 3>(g, st);
+    if constexpr (FORM == MOE_GMM_DX) {
+      if (per < 48) return launch_tile<FORM, EPI_STORE, TO, 64, 256, 1, 4, 64, 3, 3>(g, st);
+      if (t256 >= cus) return launch_tile<FORM, EPI_STORE, TO, 128, 256, 2, 4, 64, 3, 3>(g, st);
+    } else if (per < 64) {
+      return launch_tile<FORM, EPI_STORE, TO, 64, 128, 1, 4, 64, 3, 3>(g, st);
+    }
+    return launch_tile<FORM, EPI_STORE, TO, 128, 128, 2, 2, 64, 2, 3>(g, st);
   }
 }
 
