@@ -120,8 +120,8 @@ size_t moe_layer_backward_workspace_bytes(const moe_shape* shape);
  * The selection itself and the bias that steers it have no gradient.  With
  * logits NULL the router is left out: w_router, dlogits and dw_router must
  * be NULL then, and dx holds the experts' part alone.  In bf16, dz, du,
- * gate h and dlogits are rounded to bf16 where they enter a product, the
- * experts' row gradients where they are summed per token; every sum is fp32.
+ * gate h and dlogits are rounded to bf16 where they enter a product; all
+ * else is fp32 until the results are rounded.
  * Shape limits as in moe.h; outputs must not overlap inputs. */
 int moe_layer_backward(const moe_shape* shape, const moe_backward_io* io, void* ws, void* stream);
 

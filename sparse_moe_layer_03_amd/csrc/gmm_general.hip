@@ -7,8 +7,8 @@
 //     DX   A = lhs[row, r]   B = W_e[r, j]     (j contiguous in B)
 //     DW   A = lhs[row, i]   B = rhs[row, j]   (r is the row)
 //
-// Both operands are brought into LDS as fp32, reduction-major (32 values of
-// r, each with the tile's i or j side by side), whatever their layout and
+// Both operands are brought into LDS as fp32, reduction-major (32 or 64
+// values of r, each with the tile's i or j side by side), whatever their layout and
 // type in memory; 16x16x4 fp32 MFMAs take one value per lane from there.  A
 // product of two bf16 values is exact in fp32, so one kernel serves both
 // types.  Rows of LDS are padded by 16 floats: the four r of a fragment read
@@ -25,7 +25,6 @@
 namespace moe {
 
 constexpr int kGmmMaxGroups = 1024;
-constexpr int kGenBK = 32;
 
 template <typename T>
 __device__ __forceinline__ float elem(const T* p) {
@@ -69,7 +68,7 @@ __device__ __forceinline__ void group_rows(const int32_t* offsets, int e, int M,
 template <typename T, typename TO, int FORM, int BM, bool VEC>
 __global__ void __launch_bounds__(256)
 gmm_general_kernel(GmmArgs g) {
-  constexpr int BK = kGenBK, LDT = BM + 16, WT = BM / 2, NB = WT / 16, CH = BM * BK / 1024;
+  constexpr int BK = BM == 32 ? 64 : 32, LDT = BM + 16, WT = BM / 2, NB = WT / 16, CH = BM * BK / 1024;
   constexpr bool A_RED = FORM != MOE_GMM_DW, B_RED = FORM == MOE_GMM_FWD;
   __shared__ __attribute__((aligned(16))) float s_a[2][BK * LDT];
   __shared__ __attribute__((aligned(16))) float s_b[2][BK * LDT];
@@ -291,20 +290,25 @@ static int launch_general(bool vec, const GmmArgs& g, hipStream_t st) {
                                       : (long)g.M / bm + (g.M < g.ngroups ? g.M : g.ngroups);
     return n * m * g.nsplit;
   };
-  // 128 x 128 tiles when they fill the chip twice over, else 64 x 64
-  const bool big = bound(128) >= 2L * cus;
-  const long items = bound(big ? 128 : 64);
+  // 128 x 128 tiles when they fill the chip twice over, 64 x 64 when they give
+  // half the CUs one; else 32 x 32 in longer steps: a small product is bound
+  // by the latency of its steps (64 tokens, reduction 512: 24.6 -> 12.4 us)
+  const int bm = bound(128) >= 2L * cus ? 128 : 2 * bound(64) >= cus ? 64 : 32;
+  const long items = bound(bm);
   if (items < 1) return MOE_OK;
-  const long most = (long)cus * (big ? 3 : 6);
+  const long most = (long)cus * (bm == 128 ? 2 : 3);
   const dim3 grid((unsigned)(items < most ? items : most));
-#define MOE_GMM_GEN(BM, V) \
-  hipLaunchKernelGGL((gmm_general_kernel<T, TO, FORM, BM, V>), grid, dim3(256), 0, st, g)
-  if (big) {
-    if (vec) MOE_GMM_GEN(128, true);
-    else MOE_GMM_GEN(128, false);
+#define MOE_GMM_GEN(BM)                                                                          \
+  if (vec)                                                                                       \
+    hipLaunchKernelGGL((gmm_general_kernel<T, TO, FORM, BM, true>), grid, dim3(256), 0, st, g);  \
+  else                                                                                           \
+    hipLaunchKernelGGL((gmm_general_kernel<T, TO, FORM, BM, false>), grid, dim3(256), 0, st, g)
+  if (bm == 128) {
+    MOE_GMM_GEN(128);
+  } else if (bm == 64) {
+    MOE_GMM_GEN(64);
   } else {
-    if (vec) MOE_GMM_GEN(64, true);
-    else MOE_GMM_GEN(64, false);
+    MOE_GMM_GEN(32);
   }
 #undef MOE_GMM_GEN
   return check_launch();

@@ -211,14 +211,14 @@ int launch_token_bwd(int dtype, const TokenArgs& a, hipStream_t st) {
 MOE_CHECK_ACCESSOR(check_word_layer_bwd)
 
 // One workgroup per token: its FFN rows, the identity gates' share of dy and
-// the router's share, summed in that order.
-template <typename T>
+// the router's share, summed in that order.  All of a piece's loads are issued
+// before the first is added.
+template <typename T, int MAXK>
 __global__ void __launch_bounds__(256)
-dx_kernel(const T* __restrict__ dx_perm, const T* __restrict__ dy, const float* __restrict__ dxr,
+dx_kernel(const float* __restrict__ dx_rows, const T* __restrict__ dy, const float* __restrict__ dxr,
           const int32_t* __restrict__ idx, const float* __restrict__ gate,
           const int32_t* __restrict__ inv_perm, int d, int k, int n_ffn, T* __restrict__ dx) {
-  constexpr int CE = 16 / sizeof(T);
-  __shared__ int s_row[16];
+  __shared__ int s_row[MAXK];
   __shared__ float s_gz;
   __shared__ int s_n;
   const int t = blockIdx.x, tid = threadIdx.x;
@@ -248,41 +248,53 @@ dx_kernel(const T* __restrict__ dx_perm, const T* __restrict__ dy, const float* 
   const int n = s_n;
   const float gz = s_gz;
   const bool ident = n < k;
-  for (int c = tid * CE; c < d; c += 256 * CE) {
-    float acc[CE], v[CE];
+  const size_t at = (size_t)t * d;
+  for (int c = tid * 4; c < d; c += 1024) {
+    f32x4_t rows[MAXK], r = {0.f, 0.f, 0.f, 0.f}, y = r;
 #pragma unroll
-    for (int i = 0; i < CE; ++i) acc[i] = 0.f;
-    for (int q = 0; q < n; ++q) {
-      unpack16(ld16(dx_perm + (size_t)s_row[q] * d + c), v, (T*)nullptr);
-#pragma unroll
-      for (int i = 0; i < CE; ++i) acc[i] += v[i];
-    }
+    for (int q = 0; q < MAXK; ++q)
+      if (q < n) rows[q] = *reinterpret_cast<const f32x4_t*>(dx_rows + (size_t)s_row[q] * d + c);
+    if (dxr) r = *reinterpret_cast<const f32x4_t*>(dxr + at + c);
     if (ident) {
-      unpack16(ld16(dy + (size_t)t * d + c), v, (T*)nullptr);
-#pragma unroll
-      for (int i = 0; i < CE; ++i) acc[i] += gz * v[i];
-    }
-    if (dxr) {
-#pragma unroll
-      for (int i = 0; i < CE; i += 4) {
-        const f32x4_t r = *reinterpret_cast<const f32x4_t*>(dxr + (size_t)t * d + c + i);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i + q] += r[q];
+      if constexpr (sizeof(T) == 4) {
+        y = *reinterpret_cast<const f32x4_t*>(dy + at + c);
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(dy + at + c);
+        y = f32x4_t{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                    __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
       }
     }
-    st16(dx + (size_t)t * d + c, pack16(acc, (T*)nullptr));
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < MAXK; ++q)
+      if (q < n) acc += rows[q];
+    if (ident) acc += gz * y;
+    acc += r;
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<f32x4_t*>(dx + at + c) = acc;
+    } else {
+      __bf16 o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = (__bf16)acc[i];
+      *reinterpret_cast<uint2*>(dx + at + c) = __builtin_bit_cast(uint2, o);
+    }
   }
 }
 
-int launch_dx(int dtype, const void* dx_perm, const void* dy, const float* dxr, const int32_t* idx,
+int launch_dx(int dtype, const float* dx_rows, const void* dy, const float* dxr, const int32_t* idx,
               const float* gate, const int32_t* inv_perm, int T, int d, int k, int n_ffn, void* dx,
               hipStream_t st) {
-  if (dtype == MOE_BF16)
-    hipLaunchKernelGGL(dx_kernel<__bf16>, dim3(T), dim3(256), 0, st, (const __bf16*)dx_perm,
-                       (const __bf16*)dy, dxr, idx, gate, inv_perm, d, k, n_ffn, (__bf16*)dx);
-  else
-    hipLaunchKernelGGL(dx_kernel<float>, dim3(T), dim3(256), 0, st, (const float*)dx_perm,
-                       (const float*)dy, dxr, idx, gate, inv_perm, d, k, n_ffn, (float*)dx);
+#define MOE_DX(TY, MK)                                                                       \
+  hipLaunchKernelGGL((dx_kernel<TY, MK>), dim3(T), dim3(256), 0, st, dx_rows, (const TY*)dy, \
+                     dxr, idx, gate, inv_perm, d, k, n_ffn, (TY*)dx)
+  if (dtype == MOE_BF16) {
+    if (k <= 8) MOE_DX(__bf16, 8);
+    else MOE_DX(__bf16, 16);
+  } else {
+    if (k <= 8) MOE_DX(float, 8);
+    else MOE_DX(float, 16);
+  }
+#undef MOE_DX
   return check_launch();
 }
 

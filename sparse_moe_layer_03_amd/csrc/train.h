@@ -108,9 +108,9 @@ struct TokenArgs {
 };
 int launch_token_bwd(int dtype, const TokenArgs& a, hipStream_t st);
 
-// dx[t] = sum over FFN slots of dx_perm rows + (identity gates) dy[t] + dxr[t]
-// (dxr fp32, may be null).
-int launch_dx(int dtype, const void* dx_perm, const void* dy, const float* dxr, const int32_t* idx,
+// dx[t] = sum over FFN slots of dx_rows + (identity gates) dy[t] + dxr[t]
+// (both fp32; dxr may be null), rounded once.
+int launch_dx(int dtype, const float* dx_rows, const void* dy, const float* dxr, const int32_t* idx,
               const float* gate, const int32_t* inv_perm, int T, int d, int k, int n_ffn, void* dx,
               hipStream_t st);
 

@@ -105,8 +105,8 @@ static BwdLayout bwd_layout(const moe_shape* s) {
     off = up256(off + bytes);
     return at;
   };
-  w.xp = take(rows * d * es);
-  w.dyp = take(rows * d * es);
+  w.xp = take(rows * d * es);   // with dyp behind it, later the rows' gradients:
+  w.dyp = take(rows * d * es);  // fp32 [rows, d]
   w.gates = take(rows * 4);
   w.zu = take(w.mfma ? 0 : rows * 2 * f * 4);
   w.dh = take(rows * f * 4);
@@ -269,16 +269,17 @@ int moe_layer_backward(const moe_shape* s, const moe_backward_io* io, void* ws, 
   g.s[2] = {dyp, hs, io->dw_down, d, f, f, d, f};
   g.accumulate = acc;
   if ((rc = run_gmm(MOE_GMM_DW, dt, dt, g, st))) return rc;
-  // gradients of the rows, one reduction over gate's and up's columns, over
-  // x's rows, which are not needed any more
-  char* dx_perm = xp;
+  // gradients of the rows, one reduction over gate's and up's columns, in fp32
+  // (a bf16 rounding of each row would be a third of dx's error) over x's and
+  // dy's rows, which are not needed any more
+  float* dx_rows = (float*)xp;
   g.nsub = 1;
-  g.s[0] = {dzu, io->w_gate, dx_perm, 2 * f, d, d, 0, d};
+  g.s[0] = {dzu, io->w_gate, dx_rows, 2 * f, d, d, 0, d};
   g.b2 = io->w_up;
   g.R = g.RB = 2 * f;
   g.r_switch = f;
   g.accumulate = 0;
-  if ((rc = run_gmm(MOE_GMM_DX, dt, dt, g, st))) return rc;
+  if ((rc = run_gmm(MOE_GMM_DX, dt, MOE_F32, g, st))) return rc;
 
   // gradients at the gates and logits, and the router's products
   TokenArgs a{};
@@ -336,7 +337,7 @@ int moe_layer_backward(const moe_shape* s, const moe_backward_io* io, void* ws, 
     }
     if (rc) return rc;
   }
-  return launch_dx(dt, dx_perm, io->dy, io->logits ? dxr : nullptr, io->topk_idx, io->topk_gate,
+  return launch_dx(dt, dx_rows, io->dy, io->logits ? dxr : nullptr, io->topk_idx, io->topk_gate,
                    io->inv_perm, s->T, d, s->top_k, s->n_ffn, io->dx, st);
 }
 
