@@ -12,9 +12,10 @@
  *     captured into a HIP graph.  A workspace serves one call at a time: two
  *     calls, or two graphs, that may overlap need one each.
  *   - Return value: MOE_OK (0) or a negative moe_status.  Arguments are
- *     checked on the host before anything is enqueued.  Offsets in device
- *     memory cannot be: the kernels clamp every row range to [0, M], so wrong
- *     ones give wrong values and never an access out of range.
+ *     checked on the host before anything is enqueued.  Offsets and routing
+ *     arrays in device memory cannot be: the kernels keep every row that they
+ *     name inside the arrays, so wrong ones give wrong values and never an
+ *     access out of range.
  *   - Sums are formed in a fixed order, without atomics: the same call gives
  *     the same bits.
  */
@@ -38,7 +39,7 @@ typedef enum {
 /* Sizes of one grouped product.
  *   a [M, K] with lda elements from row to row, c [M, N] with ldc,
  *   W [n_groups, N, K] contiguous.
- * Limits: 1 <= n_groups <= 1024; 0 <= M < 2^31; 1 <= N, K <= 2^20;
+ * Limits: 1 <= n_groups <= 1024; 0 <= M < 2^27; 1 <= N, K <= 2^20;
  * K <= lda < 2^24; N <= ldc < 2^24.  Any sizes and strides within them; rows
  * and strides that are multiples of 16 bytes take the fast kernels. */
 typedef struct {
@@ -122,7 +123,7 @@ size_t moe_layer_backward_workspace_bytes(const moe_shape* shape);
  * be NULL then, and dx holds the experts' part alone.  In bf16, dz, du,
  * gate h and dlogits are rounded to bf16 where they enter a product; all
  * else is fp32 until the results are rounded.
- * Shape limits as in moe.h; outputs must not overlap inputs. */
+ * Shape limits as in moe.h, and T * top_k < 2^27; outputs must not overlap inputs or each other. */
 int moe_layer_backward(const moe_shape* shape, const moe_backward_io* io, void* ws, void* stream);
 
 /* Hyper-parameters of an AdamW step (host struct, copied into the launch). */
@@ -177,7 +178,10 @@ typedef struct {
  * neighbouring codes so that its mean (the mean of its square, for v) is
  * exact: rounding to nearest would hold on to an average that moves by less
  * than half a code each step.  A v > 0 never becomes 0.  The random numbers
- * depend on (seed, step, tensor's place in the list, i) only. */
+ * depend on (seed, step, tensor's place in the list, i) only.  A gradient
+ * that is not finite reaches its own element (8 bits: its block); to leave a
+ * step out, pass a grad_scale that is not finite.  No array may be in the
+ * list twice. */
 int moe_adamw(const moe_adamw_params* params, const moe_adamw_tensor* tensors, int32_t n_tensors,
               moe_adamw_state* state, const float* grad_scale, const float* lr_scale,
               void* stream);

@@ -89,6 +89,7 @@ gmm_general_kernel(GmmArgs g) {
   // FWD, DX: prefix over the groups of their row tiles
   if (FORM != MOE_GMM_DW) {
     constexpr int PER = kGmmMaxGroups / 256;
+    const int most = g.M / BM + g.ngroups;  // row tiles that ascending offsets can give
     int loc[PER], run = 0;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
@@ -96,7 +97,7 @@ gmm_general_kernel(GmmArgs g) {
       if (e < g.ngroups) {
         int lo, hi;
         group_rows(g.offsets, e, g.M, lo, hi);
-        run += (hi - lo + BM - 1) / BM;
+        run = min(run + (hi - lo + BM - 1) / BM, most + 1);
       }
       loc[k] = run;
     }
@@ -107,7 +108,9 @@ gmm_general_kernel(GmmArgs g) {
       if (tid * PER + k < g.ngroups) s_pref[tid * PER + k + 1] = base + loc[k];
     __syncthreads();
   }
-  const long tiles = (long)(FORM == MOE_GMM_DW ? g.ngroups : s_pref[g.ngroups]) * per;
+  const int row_tiles = FORM == MOE_GMM_DW ? g.ngroups : s_pref[g.ngroups];
+  if (FORM != MOE_GMM_DW && row_tiles > g.M / BM + g.ngroups) return;  // offsets not ascending
+  const long tiles = (long)row_tiles * per;
   const long items = tiles * g.nsplit;
 
   for (long item = blockIdx.x; item < items; item += gridDim.x) {

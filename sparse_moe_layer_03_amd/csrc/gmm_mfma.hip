@@ -218,6 +218,9 @@ gmm_mfma_kernel(GmmArgs g) {
     int* s_pref = reinterpret_cast<int*>(s_b0);
     int* s_scan = reinterpret_cast<int*>(s_b1);
     constexpr int PER = (kMfmaMaxGroups + NT - 1) / NT;
+    // ascending offsets give at most this many row tiles; more are cut off
+    // here and computed nowhere
+    const int most = g.M / BM + g.ngroups;
     int loc[PER], run = 0;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
@@ -225,7 +228,7 @@ gmm_mfma_kernel(GmmArgs g) {
       if (e < g.ngroups) {
         int lo, hi;
         rows_of(g.offsets, e, g.M, lo, hi);
-        run += (hi - lo + BM - 1) / BM;
+        run = min(run + (hi - lo + BM - 1) / BM, most + 1);
       }
       loc[k] = run;
     }
@@ -235,7 +238,8 @@ gmm_mfma_kernel(GmmArgs g) {
     for (int k = 0; k < PER; ++k)
       if (tid * PER + k < g.ngroups) s_pref[tid * PER + k + 1] = base + loc[k];
     __syncthreads();
-    tiles = (long)uni(s_pref[g.ngroups]) * jt;
+    const int row_tiles = uni(s_pref[g.ngroups]);
+    tiles = row_tiles <= most ? (long)row_tiles * jt : 0;
     const long t = (vid + (long)(k0 + lane) * G) / g.nsplit;
     desc = 0;
     if (t < tiles) {

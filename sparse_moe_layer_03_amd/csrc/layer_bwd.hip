@@ -81,7 +81,8 @@ gather2_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* _
   const int rows = min(offsets[n_ffn], Tk);
   for (int p = blockIdx.x * 4 + (threadIdx.x >> 6); p < rows; p += gridDim.x * 4) {
     const int at = __builtin_amdgcn_readfirstlane(perm[p]);
-    if (!MOE_GUARD((unsigned)at < (unsigned)Tk, MOE_CHECK_GEMM_ROW)) continue;
+    MOE_CHECK((unsigned)at < (unsigned)Tk, MOE_CHECK_GEMM_ROW);
+    if ((unsigned)at >= (unsigned)Tk) continue;
     const size_t src = (size_t)(at / k) * d, dst = (size_t)p * d;
     if (lane == 0) gate_rows[p] = gate[at];
     const int chunks = d / CE;
@@ -138,7 +139,9 @@ __global__ void __launch_bounds__(256) token_bwd_kernel(TokenArgs a) {
     const int row = a.inv_perm[t * a.k + tid];
     s_e[tid] = e;
     float dg = 0.f;
-    if (e < a.n_ffn && MOE_GUARD((unsigned)row < (unsigned)(a.T * a.k), MOE_CHECK_COMBINE_ROW))
+    const bool inside = (unsigned)row < (unsigned)(a.T * a.k);
+    MOE_CHECK(e >= a.n_ffn || inside, MOE_CHECK_COMBINE_ROW);
+    if (e < a.n_ffn && inside)
       for (int q = 0; q < a.parts; ++q) dg += a.part[(size_t)row * a.parts + q];
     s_dg[tid] = dg;
     identity = e >= a.n_ffn;
@@ -229,9 +232,9 @@ dx_kernel(const float* __restrict__ dx_rows, const T* __restrict__ dy, const flo
       e = idx[t * k + tid];
       g = gate[t * k + tid];
       row = inv_perm[t * k + tid];
-      // gridDim.x = T
-      if (e < n_ffn && !MOE_GUARD((unsigned)row < gridDim.x * (unsigned)k, MOE_CHECK_COMBINE_ROW))
-        row = 0;
+      const bool inside = (unsigned)row < gridDim.x * (unsigned)k;  // gridDim.x = T
+      MOE_CHECK(e >= n_ffn || inside, MOE_CHECK_COMBINE_ROW);
+      if (!inside) row = 0;
     }
     const bool ffn = tid < k && e < n_ffn;
     const uint64_t fb = __ballot(ffn);

@@ -9,6 +9,10 @@
 
 namespace moe {
 
+// Rows of a product: row tiles are counted in 22 bits, and the scan over the
+// groups' tiles stays inside an int whatever the offsets hold.
+constexpr int kGmmMaxRows = 1 << 27;
+
 // Grouped products in the kernels' terms: out[i, j] = sum_r A(i, r) B(j, r)
 // for every group.  FWD and DX: i runs over the group's rows, r over R.  DW:
 // r runs over the group's rows, i over I.  j runs over J.  Up to three
@@ -51,7 +55,6 @@ struct GmmArgs {
 int launch_gmm_general(int form, int dtype, int out_dtype, bool vec, const GmmArgs& g,
                        hipStream_t st);
 // bf16 products on bf16 MFMAs (gmm_mfma.hip; FWD: one product).
-constexpr int kMfmaMaxRows = 1 << 29;  // row tiles are counted in 22 bits
 // Whether a product can run there: 16-byte rows and row starts, and sizes
 // that 32-bit offsets within a tile reach.
 bool mfma_ok(int form, int dtype, int N, int K, int64_t lda, int64_t ldc);

@@ -25,7 +25,7 @@ static int check_gmm(const moe_gmm_shape* s) {
     return MOE_EINVAL;
   if (s->dtype != MOE_F32 && s->dtype != MOE_BF16) return MOE_EUNSUPPORTED;
   if (s->out_dtype != s->dtype && s->out_dtype != MOE_F32) return MOE_EUNSUPPORTED;
-  if (s->n_groups > 1024 || s->N > (1 << 20) || s->K > (1 << 20) || s->lda >= (1 << 24) ||
+  if (s->n_groups > 1024 || s->M >= kGmmMaxRows || s->N > (1 << 20) || s->K > (1 << 20) || s->lda >= (1 << 24) ||
       s->ldc >= (1 << 24))
     return MOE_EUNSUPPORTED;
   return MOE_OK;
@@ -60,7 +60,7 @@ static size_t gmm_part_bytes(const moe_gmm_shape* s, int nsplit) {
 static int run_gmm(int form, int dtype, int out_dtype, const GmmArgs& g, hipStream_t st,
                    bool padded = false) {
   const bool fwd = form == MOE_GMM_FWD, dx = form == MOE_GMM_DX;
-  bool mfma = g.M < kMfmaMaxRows && !(fwd && g.nsub > 1), vec = g.b_group % 4 == 0;
+  bool mfma = !(fwd && g.nsub > 1), vec = g.b_group % 4 == 0;
   for (int q = 0; q < g.nsub; ++q) {
     const GmmSub& s = g.s[q];
     const int64_t lda = dx ? s.ldo : fwd ? s.lda : s.ldb, ldc = fwd ? s.ldo : s.lda;
@@ -96,8 +96,7 @@ static BwdLayout bwd_layout(const moe_shape* s) {
   const int cus = device_cu_count();
   w.nsplit = (int)std::max(1l, std::min({(long)kRouteSplits, (long)s->T / 256,
                                          (cus > 0 ? cus : 256) / (cdiv(E, 256) * cdiv(d, 256))}));
-  w.mfma = s->dtype == MOE_BF16 && s->d_model < (1 << 20) && s->d_ff < (1 << 19) &&
-           rows < kMfmaMaxRows;
+  w.mfma = s->dtype == MOE_BF16 && s->d_model <= (1 << 20) && s->d_ff <= (1 << 19);
   w.parts = w.mfma ? swiglu_parts((int)rows, s->n_ffn, s->d_ff) : 1;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -121,8 +120,14 @@ static BwdLayout bwd_layout(const moe_shape* s) {
   return w;
 }
 
-static int check_backward(const moe_shape* s, const moe_backward_io* io) {
+static int check_backward_shape(const moe_shape* s) {
   const int rc = check_shape(s);
+  if (rc) return rc;
+  return (long)s->T * s->top_k < kGmmMaxRows ? MOE_OK : MOE_EUNSUPPORTED;
+}
+
+static int check_backward(const moe_shape* s, const moe_backward_io* io) {
+  const int rc = check_backward_shape(s);
   if (rc) return rc;
   if (!io) return MOE_EINVAL;
   if (!io->x || !io->topk_idx || !io->topk_gate || !io->offsets || !io->perm || !io->inv_perm ||
@@ -207,7 +212,7 @@ int moe_grouped_matmul(const moe_gmm_shape* s, const int32_t* offsets, const voi
 }
 
 size_t moe_layer_backward_workspace_bytes(const moe_shape* s) {
-  if (check_shape(s) != MOE_OK) return 0;
+  if (check_backward_shape(s) != MOE_OK) return 0;
   return bwd_layout(s).total;
 }
 

@@ -112,6 +112,33 @@ def test_many_rows_and_tiles(form):
     check(form, "bf16", [700, 0, 1300, 256, 511, 1], 520, 776)
 
 
+def ragged(groups, mean, seed=3):
+    """Row counts around a mean, every seventh group empty."""
+    g = torch.Generator().manual_seed(seed)
+    c = torch.randint(0, 2 * mean, (groups,), generator=g)
+    c[::7] = 0
+    return c.tolist()
+
+
+@pytest.mark.parametrize("out,accumulate", [("bf16", False), ("f32", True), ("bf16", True)])
+@pytest.mark.parametrize("form,groups,mean,N,K", [
+    # the tile shapes' ranges: rows per group, and enough tiles for all CUs
+    ("fwd", 40, 30, 1112, 264), ("fwd", 40, 90, 1112, 264), ("fwd", 60, 200, 2056, 328),
+    ("dx", 40, 25, 264, 1112), ("dx", 48, 80, 264, 2056), ("dx", 60, 200, 328, 2056),
+    ("dw", 40, 50, 776, 1032), ("dw", 24, 150, 1032, 1288), ("dw", 9, 700, 264, 520),
+])
+def test_tile_shapes(form, groups, mean, N, K, out, accumulate):
+    check(form, "bf16", ragged(groups, mean), N, K, out=out, accumulate=accumulate, spare=9)
+
+
+@pytest.mark.parametrize("form,rows,N,K", [
+    # more than 64 tiles for a workgroup: the tile list is made anew
+    ("fwd", 1, 5120, 8), ("dx", 1, 8, 5120), ("dx", 50, 8, 4352), ("fwd", 128, 4352, 8),
+])
+def test_many_tiles_per_workgroup(form, rows, N, K):
+    check(form, "bf16", [rows] * 1024, N, K)
+
+
 @pytest.mark.parametrize("form", FORMS)
 def test_most_groups(form):
     counts = [(i * 7) % 5 for i in range(1024)]

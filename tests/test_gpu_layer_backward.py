@@ -274,6 +274,22 @@ def test_training_steps_together(dtype, bits):
             assert ((got - p).abs() <= EPS * (p.abs() + up.abs() + got.abs())).all(), (step, w)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_wrong_routing_arrays_stay_inside(dtype):
+    # wrong values are the caller's; nothing may be read or written outside
+    c = Case(dtype, 64, 128, 6, 2, 128, 3)
+    for name, bad in (("inv_perm", 1 << 30), ("inv_perm", -7), ("perm", 1 << 30), ("perm", -1), ("offsets", 1 << 30),
+                      ("offsets", -9), ("topk_idx", 99), ("topk_idx", -3)):
+        t = getattr(c.buf, name)
+        kept = t.clone()
+        t[::3] = bad
+        c.backward()
+        t.copy_(kept)
+    tb, ref = c.backward(), c.reference()
+    for name, want in ref.items():
+        assert far(getattr(tb, name), want) <= TOL[dtype], name
+
+
 def test_refusals():
     c = Case("bf16", 20, 64, 3, 1, 64, 2)
     small = torch.empty(64, dtype=torch.uint8, device="cuda")

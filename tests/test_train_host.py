@@ -64,6 +64,7 @@ def call_gmm(s, offsets=A, lhs=A, rhs=A, out=A, ws=A):
     (dict(dtype=2), EUNSUPPORTED), (dict(out_dtype=5), EUNSUPPORTED),
     (dict(dtype=B.MOE_F32, out_dtype=B.MOE_BF16), EUNSUPPORTED), (dict(n_groups=1025), EUNSUPPORTED),
     (dict(K=(1 << 20) + 1, lda=(1 << 20) + 1), EUNSUPPORTED), (dict(lda=1 << 24), EUNSUPPORTED),
+    (dict(M=1 << 27), EUNSUPPORTED),
 ])
 def test_grouped_matmul_refuses_bad_shapes(change, code):
     s = gmm(**change)
@@ -108,6 +109,7 @@ def test_layer_backward_refuses_bad_arguments():
     assert backward(s, logits=0, w_router=0, dlogits=0) == EINVAL
     assert backward(shape(d_ff=100)) == EUNSUPPORTED
     assert backward(shape(T=0)) == EINVAL
+    assert backward(shape(T=1 << 26)) == EUNSUPPORTED                         # T * top_k = 2^27
     assert T.lib().moe_layer_backward(ctypes.byref(s), None, P(A), None) == EINVAL
     assert T.moe_layer_backward_workspace_bytes(shape(T=0)) == 0
     assert T.moe_layer_backward_workspace_bytes(s) > 0
