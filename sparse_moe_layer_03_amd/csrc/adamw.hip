@@ -8,7 +8,9 @@
 // The list of up to 48 tensors travels in the kernel arguments, so a step
 // needs no table in device memory and can be captured as it stands.  Chunks
 // of 2048 elements over all tensors are dealt to the workgroups in turn; a
-// thread handles 8 neighbouring elements with 16-byte accesses.
+// thread handles 8 neighbouring elements with 16-byte accesses.  Measured over
+// 402M parameters: 32-bit moments 2.26 ms, 4.99 TB/s (a plain copy runs at
+// 4.9), 8-bit ones 1.36 ms, 4.75 TB/s; non-temporal accesses up to 10% slower.
 //
 // 8-bit moments: 256 elements (32 lanes) share a scale, their largest
 // magnitude / 448, found by a butterfly over half a wave.  Codes are e4m3
@@ -18,7 +20,8 @@
 // second moment is held as its root, which halves the exponents' range; the
 // mean of the square is kept, for a rounding that kept the root's mean would
 // raise v by the rounding's variance at every step.  Random bits: two rounds
-// of multiply and xor-shift ("lowbias32", C. Wellons) of the element's place.
+// of xor-shift and multiply of the element's place, with constants that
+// C. Wellons published for such a mixing of 32 bits.
 // What a code follows from (the moments, their largest, the comparison) is
 // computed operation by operation, each rounded by itself: contracted sums
 // would move one code in a million, and a code is an eighth of its value.
@@ -340,7 +343,10 @@ int launch_adamw(const moe_adamw_params* hp, const moe_adamw_tensor* tensors, in
       chunks += ((uint64_t)s.n + kAdamChunk - 1) / kAdamChunk;
       d.chunk_end = (uint32_t)chunks;  // the caller keeps the sum below 2^32
     }
-    const uint64_t most = 8ull * cus;
+    // four rounds of the 7 or 8 workgroups that a CU holds: 402M parameters with
+    // 8-bit moments 1361 us (one round of 8: 1468, a workgroup per chunk: 2341),
+    // with 32-bit ones 2261 (2271, 2450)
+    const uint64_t most = 28ull * cus;
     const uint64_t grid = chunks < 1 ? 1 : chunks < most ? chunks : most;
     if (hp->state_bits == 8)
       hipLaunchKernelGGL(adamw_kernel<true>, dim3((unsigned)grid), dim3(kAdamThreads), 0, st, a);
