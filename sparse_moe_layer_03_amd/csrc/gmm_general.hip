@@ -167,12 +167,17 @@ gmm_general_kernel(GmmArgs g) {
     const T* b = (const T*)sub.b + b_at;
     const T* b2 = FORM == MOE_GMM_DX && g.r_switch ? (const T*)g.b2 + b_at : b;
     const int rb_hi = FORM == MOE_GMM_DX ? min(r_hi, g.RB) : r_hi;
+    const int rb2_hi = min(r_hi, g.r_switch + g.RB);
 
-    f32x4_t acc[NB][NB];
+    // Sums of 128 products in acc, their sum in tot: a long fp32 reduction
+    // rounds like sqrt(128) + sqrt(n / 128) instead of sqrt(n) additions.
+    constexpr int FLUSH = 128 / BK;
+    f32x4_t acc[NB][NB], tot[NB][NB];
+    int since = 0;
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int j = 0; j < NB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < NB; ++j) acc[i][j] = tot[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
     // chunk c of this thread: four elements that lie side by side in memory
     auto fetch = [&](bool red, const T* base, long ld, int wide, int r0, int r_end, f32x4_t* v) {
@@ -207,7 +212,7 @@ gmm_general_kernel(GmmArgs g) {
     auto fetch_ab = [&](int r) {
       fetch(A_RED, a, sub.lda, wide_a, r, r_hi, va);
       if (FORM == MOE_GMM_DX && g.r_switch && r >= g.r_switch)
-        fetch(B_RED, b2 - (long)g.r_switch * sub.ldb, sub.ldb, wide_b, r, rb_hi, vb);
+        fetch(B_RED, b2 - (long)g.r_switch * sub.ldb, sub.ldb, wide_b, r, rb2_hi, vb);
       else
         fetch(B_RED, b, sub.ldb, wide_b, r, rb_hi, vb);
     };
@@ -232,6 +237,16 @@ gmm_general_kernel(GmmArgs g) {
           for (int j = 0; j < NB; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fb[j], fa[i], acc[i][j], 0, 0, 0);
       }
+      if (++since == FLUSH || r + BK >= r_hi) {
+        since = 0;
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int j = 0; j < NB; ++j) {
+            tot[i][j] += acc[i][j];
+            acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+          }
+      }
     }
 
     // b was the MFMA's row operand: a lane holds columns 4 q4 .. + 3 of row r16
@@ -251,12 +266,12 @@ gmm_general_kernel(GmmArgs g) {
           float* p = g.part + split * g.part_stride + prow * sub.J + jj;
 #pragma unroll
           for (int v = 0; v < 4; ++v)
-            if (jj + v < sub.J) p[v] = acc[i][j][v];
+            if (jj + v < sub.J) p[v] = tot[i][j][v];
         } else {
           TO* p = (TO*)sub.out + orow + jj;
 #pragma unroll
           for (int v = 0; v < 4; ++v)
-            if (jj + v < sub.J) put(p + v, acc[i][j][v], g.accumulate);
+            if (jj + v < sub.J) put(p + v, tot[i][j][v], g.accumulate);
         }
       }
     }

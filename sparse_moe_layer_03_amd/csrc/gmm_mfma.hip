@@ -366,7 +366,7 @@ gmm_mfma_kernel(GmmArgs g) {
     // where the operands' tiles begin and end
     if constexpr (DW) {
       t.a_base = uni((const char*)sub.a + t.row0 * (int64_t)t.lda2 + (int64_t)t.i0 * 2);
-      t.a_bytes = (uint32_t)min(BM, ((sub.I + 7) & ~7) - t.i0) * 2;
+      t.a_bytes = (uint32_t)min(BM, sub.I - t.i0) * 2;
     } else {
       t.a_base = uni((const char*)sub.a + (t.row0 + t.i0) * (int64_t)t.lda2);
       t.a_bytes = t.i_end > t.i0 ? (uint32_t)(t.i_end - t.i0 - 1) * t.lda2 + (uint32_t)g.R * 2 : 0u;
@@ -430,14 +430,17 @@ gmm_mfma_kernel(GmmArgs g) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)off, ks * KS * 2 + add, 0,
                                                AUX);
     } else {
-      int r = ks * KS;
-      // rows of b that this step has (w_router ends before dlogits' padding)
-      const int left = max(0, min(KS, (FORM == MOE_GMM_DX ? min(t.r_end, g.RB) : t.r_end) - r));
+      int r = ks * KS, end = t.r_end;
       const char* base = t.b_base;
-      if (FORM == MOE_GMM_DX && g.r_switch && r >= g.r_switch) {
-        base = t.b_base2;
-        r -= g.r_switch;
+      if (FORM == MOE_GMM_DX) {
+        if (g.r_switch && r >= g.r_switch) {
+          base = t.b_base2;
+          r -= g.r_switch;
+          end -= g.r_switch;
+        }
+        end = min(end, g.RB);
       }
+      const int left = max(0, min(KS, end - r));  // rows of b that this step has
       const auto rs = descriptor(base + (int64_t)r * t.ldb2,
                                  left > 0 ? (uint32_t)(left - 1) * t.ldb2 + t.b_bytes : 0u);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)b_off[h % TB::NP], add,

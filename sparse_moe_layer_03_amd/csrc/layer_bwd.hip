@@ -198,7 +198,16 @@ __global__ void __launch_bounds__(256) token_bwd_kernel(TokenArgs a) {
   for (int q = 0; q < MAXE / 256; ++q) {
     const int e = tid + q * 256;
     const float v = e < a.E ? p[q] * (s_dp[e] - dot) : 0.f;
-    if (e < a.ep) ((T*)a.dl)[(size_t)t * a.ep + e] = ElemOps<T>::from_f(v);
+    if (e < a.ep) {
+      if constexpr (sizeof(T) == 4) {
+        ((float*)a.dl)[(size_t)t * a.ep + e] = v;
+      } else {
+        __bf16* row = (__bf16*)a.dl + (size_t)t * 2 * a.ep;
+        const __bf16 hi = (__bf16)v;
+        row[e] = hi;
+        row[a.ep + e] = (__bf16)(v - (float)hi);
+      }
+    }
     if (a.dlogits && e < a.E) a.dlogits[(size_t)t * a.E + e] = v;
   }
 }

@@ -32,9 +32,10 @@ struct GmmArgs {
   const int32_t* offsets;  // [ngroups + 1]
   int M;                   // rows that the row arrays hold
   int R;                   // FWD, DX: length of the reduction
-  int RB;                  // DX: rows that a group of b holds (<= R; zeros behind)
+  int RB;                  // DX: rows that a group of b, and of b2, holds; behind
+                           // them the reduction reads zeros
   int r_switch;            // DX: reduction rows from here on (a multiple of 64)
-                           // come from b2 (0: none)
+                           // come from b2, from its first one (0: none)
   const void* b2;          // DX: see r_switch; SwiGLU step: w_up
   int64_t b_group;         // elements between groups of b (FWD, DX)
   int64_t out_group;       // elements between groups of out (DW)
@@ -90,10 +91,11 @@ int launch_swiglu_bwd(int dtype, const float* zu, const float* dh, const float* 
                       const int32_t* offsets, int n_ffn, int Tk, int f, void* dzu, void* hs,
                       float* dgate_part, hipStream_t st);
 
-// Per token: dgate (parts: partial sums per FFN row), then, with logits, dlogits (fp32 if not
-// null, and in dtype with rows of ep elements, zeros behind E) and the row
-// bounds of the router's products: route_offs[0..1] = 0, T and
-// split_offs[s] = s * T / nsplit.
+// Per token: dgate (parts: partial sums per FFN row), then, with logits,
+// dlogits (fp32 if not null), its operand `dl` of the router's products, and
+// their row bounds: route_offs[0..1] = 0, T and split_offs[s] = s * T / nsplit.
+// dl in fp32: rows of ep elements, zeros behind E.  In bf16 rows of 2 ep: the
+// rounded values and, ep behind, what the rounding left of them.
 struct TokenArgs {
   const void* x;
   const void* dy;

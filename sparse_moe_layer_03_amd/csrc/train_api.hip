@@ -55,16 +55,14 @@ static size_t gmm_part_bytes(const moe_gmm_shape* s, int nsplit) {
   return up256(out * nsplit * sizeof(float));
 }
 
-// Runs products, a split reduction joined.  DW loads whole 8-element chunks of
-// c's rows; `padded`: their gaps hold zeros (else N has to be whole chunks).
-static int run_gmm(int form, int dtype, int out_dtype, const GmmArgs& g, hipStream_t st,
-                   bool padded = false) {
+// Runs products, a split reduction joined.
+static int run_gmm(int form, int dtype, int out_dtype, const GmmArgs& g, hipStream_t st) {
   const bool fwd = form == MOE_GMM_FWD, dx = form == MOE_GMM_DX;
   bool mfma = !(fwd && g.nsub > 1), vec = g.b_group % 4 == 0;
   for (int q = 0; q < g.nsub; ++q) {
     const GmmSub& s = g.s[q];
     const int64_t lda = dx ? s.ldo : fwd ? s.lda : s.ldb, ldc = fwd ? s.ldo : s.lda;
-    const int N = fwd ? s.J : dx ? g.R : padded ? (s.I + 7) & ~7 : s.I, K = fwd ? g.R : s.J;
+    const int N = fwd ? s.J : dx ? g.R : s.I, K = fwd ? g.R : s.J;
     const bool al = al16(s.a) && al16(s.b);
     mfma = mfma && al && al16(s.out) && mfma_ok(form, dtype, N, K, lda, ldc);
     vec = vec && al && s.lda % 4 == 0 && s.ldb % 4 == 0;
@@ -81,7 +79,7 @@ constexpr int kRouteSplits = 16;  // most token ranges of the router's weight gr
 
 struct BwdLayout {
   size_t xp, dyp, gates, zu, dh, dzu, hs, part, dl, offs, dxr, drp, total;
-  int ep, nsplit, parts;
+  int ep, halves, nsplit, parts;
   bool mfma;  // the bf16 kernels, with SwiGLU's step in the products' epilogue
 };
 
@@ -90,12 +88,17 @@ static BwdLayout bwd_layout(const moe_shape* s) {
   const size_t E = (size_t)s->n_ffn + s->n_zero, rows = (size_t)s->T * s->top_k;
   const size_t d = s->d_model, f = s->d_ff;
   BwdLayout w;
-  w.ep = (int)((E + 7) & ~(size_t)7);
+  // In bf16 dlogits enters the router's products as two bf16 values, the
+  // rounded one and the rest: scores and gates are fp32 in this layer, and so
+  // stay their gradients.  64: where the second part begins, a step's start.
+  w.halves = s->dtype == MOE_BF16 ? 2 : 1;
+  w.ep = (int)((E + 63) & ~(size_t)63);
   // the router's weight gradient has few tiles and a reduction over all
   // tokens: as many ranges of at least 256 of them as give every CU a tile
   const int cus = device_cu_count();
   w.nsplit = (int)std::max(1l, std::min({(long)kRouteSplits, (long)s->T / 256,
-                                         (cus > 0 ? cus : 256) / (cdiv(E, 256) * cdiv(d, 256))}));
+                                         (cus > 0 ? cus : 256) /
+                                             (cdiv(w.ep * w.halves, 256) * cdiv(d, 256))}));
   w.mfma = s->dtype == MOE_BF16 && s->d_model <= (1 << 20) && s->d_ff <= (1 << 19);
   w.parts = w.mfma ? swiglu_parts((int)rows, s->n_ffn, s->d_ff) : 1;
   size_t off = 0;
@@ -112,10 +115,10 @@ static BwdLayout bwd_layout(const moe_shape* s) {
   w.dzu = take(rows * 2 * f * es);
   w.hs = take(rows * f * es);
   w.part = take(rows * w.parts * 4);
-  w.dl = take((size_t)s->T * w.ep * es);
+  w.dl = take((size_t)s->T * w.ep * w.halves * es);
   w.offs = take((2 + kRouteSplits + 1) * sizeof(int32_t));
   w.dxr = take((size_t)s->T * d * 4);
-  w.drp = take(w.nsplit > 1 ? E * d * 4 * w.nsplit : 0);
+  w.drp = take((size_t)w.ep * w.halves * d * 4 * w.nsplit);
   w.total = off;
   return w;
 }
@@ -281,8 +284,8 @@ int moe_layer_backward(const moe_shape* s, const moe_backward_io* io, void* ws, 
   g.nsub = 1;
   g.s[0] = {dzu, io->w_gate, dx_rows, 2 * f, d, d, 0, d};
   g.b2 = io->w_up;
-  g.R = g.RB = 2 * f;
-  g.r_switch = f;
+  g.R = 2 * f;
+  g.RB = g.r_switch = f;
   g.accumulate = 0;
   if ((rc = run_gmm(MOE_GMM_DX, dt, MOE_F32, g, st))) return rc;
 
@@ -316,30 +319,29 @@ int moe_layer_backward(const moe_shape* s, const moe_backward_io* io, void* ws, 
     r.nsplit = 1;
     // dlogits W_router, fp32 (dlogits' rows have zeros behind E, where
     // w_router has none)
-    r.s[0] = {dl, io->w_router, dxr, w.ep, d, d, 0, d};
+    const int wide = w.ep * w.halves;
+    r.s[0] = {dl, io->w_router, dxr, wide, d, d, 0, d};
     r.offsets = route_offs;
     r.ngroups = 1;
-    r.R = w.ep;
+    r.R = wide;
     r.RB = E;
+    r.b2 = io->w_router;
+    r.r_switch = w.halves == 2 ? w.ep : 0;
     if ((rc = run_gmm(MOE_GMM_DX, dt, MOE_F32, r, st))) return rc;
-    // dlogits^T x, over ranges of the tokens that are joined
-    r.s[0] = {dl, io->x, w.nsplit > 1 ? (void*)drp : io->dw_router, w.ep, d, d, E, d};
-    r.out_group = (int64_t)E * d;
+    // dlogits^T x over ranges of the tokens, both parts, then their sum
+    r.s[0] = {dl, io->x, drp, wide, d, d, wide, d};
+    r.out_group = (int64_t)wide * d;
     r.offsets = split_offs;
     r.ngroups = w.nsplit;
-    if (w.nsplit > 1) {
-      if ((rc = run_gmm(MOE_GMM_DW, dt, MOE_F32, r, st, true))) return rc;
-      r.part = drp;
-      r.part_stride = (int64_t)E * d;
-      r.nsplit = w.nsplit;
-      r.ngroups = 1;
-      r.s[0].out = io->dw_router;
-      r.accumulate = acc;
-      rc = launch_gmm_join(MOE_GMM_DW, dt, r, st);
-    } else {
-      r.accumulate = acc;
-      rc = run_gmm(MOE_GMM_DW, dt, dt, r, st, true);
-    }
+    if ((rc = run_gmm(MOE_GMM_DW, dt, MOE_F32, r, st))) return rc;
+    r.part = drp;
+    r.part_stride = (int64_t)w.ep * d;
+    r.nsplit = w.nsplit * w.halves;
+    r.ngroups = 1;
+    r.s[0].out = io->dw_router;
+    r.s[0].I = E;
+    r.accumulate = acc;
+    rc = launch_gmm_join(MOE_GMM_DW, dt, r, st);
     if (rc) return rc;
   }
   return launch_dx(dt, dx_rows, io->dy, io->logits ? dxr : nullptr, io->topk_idx, io->topk_gate,

@@ -111,7 +111,10 @@ def test_gradients(case):
         assert torch.isfinite(got.double()).all(), name
         err = far(got, want)
         say(f"  {name} {err:.2e}")
-        assert err <= TOL[case[0]], (name, err)
+        # the router's operand keeps what its rounding leaves: its weight
+        # gradient is rounded once, by at most 2^-8 of each value
+        tol = 1.01 * 2.0 ** -8 if name == "dw_router" and case[0] == "bf16" else TOL[case[0]]
+        assert err <= tol, (name, err)
 
 
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
