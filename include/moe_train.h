@@ -123,7 +123,8 @@ size_t moe_layer_backward_workspace_bytes(const moe_shape* shape);
  * be NULL then, and dx holds the experts' part alone.  In bf16, dz, du,
  * gate h and dlogits are rounded to bf16 where they enter a product; all
  * else is fp32 until the results are rounded.
- * Shape limits as in moe.h, and T * top_k < 2^27; outputs must not overlap inputs or each other. */
+ * Shape limits as in moe.h, and T * top_k < 2^27, d_model <= 2^20, d_ff <=
+ * 2^19; outputs must not overlap inputs or each other. */
 int moe_layer_backward(const moe_shape* shape, const moe_backward_io* io, void* ws, void* stream);
 
 /* Hyper-parameters of an AdamW step (host struct, copied into the launch). */

@@ -817,8 +817,9 @@ static int launch_tile(const GmmArgs& g, hipStream_t st) {
 //       128x256       544   557  611   645          are 512 bytes of W
 //       256x256                              676   850
 // DW has 256 x 256 tiles, in steps of 32 (256 groups of 39 ragged rows: 847
-// us, steps of 64: 1034; 128 x 128 tiles 1210).  Where the largest tiles leave
-// CUs idle, 128 x 128.
+// us, steps of 64: 1034; 128 x 128 tiles 1210) where they give three CUs of
+// four a tile (the skewed layer's router, 240 tiles: 52 us, 128 x 128: 81).
+// Else, and in the other forms where 256 columns leave CUs idle, 128 x 128.
 template <int FORM, typename TO>
 static int launch_form(const GmmArgs& g, hipStream_t st) {
   const int cus = stream_cu_count(st);
@@ -830,7 +831,8 @@ static int launch_form(const GmmArgs& g, hipStream_t st) {
   t256 *= g.nsplit * (FORM == MOE_GMM_DW ? (long)g.ngroups
                                          : g.M / 256 + (g.M < g.ngroups ? g.M : g.ngroups));
   if constexpr (FORM == MOE_GMM_DW) {
-    if (t256 >= cus) return launch_tile<FORM, EPI_STORE, TO, 256, 256, 4, 2, 32, 4, 4>(g, st);
+    if (4 * t256 >= 3L * cus)
+      return launch_tile<FORM, EPI_STORE, TO, 256, 256, 4, 2, 32, 4, 4>(g, st);
     return launch_tile<FORM, EPI_STORE, TO, 128, 128, 2, 2, 32, 4, 4>(g, st);
   } else {
     if (per >= 128 && t256 >= cus)

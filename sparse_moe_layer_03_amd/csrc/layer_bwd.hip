@@ -24,48 +24,47 @@ __device__ __forceinline__ float block_max(float v, float* s) {
   return fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
 }
 
-template <typename T>
+// One workgroup per FFN row (gridDim.x = T * top_k).
 __global__ void __launch_bounds__(256)
 swiglu_bwd_kernel(const float* __restrict__ zu, const float* __restrict__ dh0,
                   const float* __restrict__ gate_rows, const int32_t* __restrict__ offsets,
-                  int n_ffn, int f, T* __restrict__ dzu, T* __restrict__ hs,
+                  int n_ffn, int f, float* __restrict__ dzu, float* __restrict__ hs,
                   float* __restrict__ part) {
   __shared__ float s[4];
-  const int p = blockIdx.x;  // gridDim.x = T * top_k
+  const int p = blockIdx.x;
   if (p >= offsets[n_ffn]) return;
   const float gt = gate_rows[p];
   const float* zr = zu + (size_t)p * 2 * f;
   const float* dr = dh0 + (size_t)p * f;
-  T* o = dzu + (size_t)p * 2 * f;
+  float* o = dzu + (size_t)p * 2 * f;
   float sum = 0.f;
   for (int c = threadIdx.x * 4; c < f; c += 1024) {
     const f32x4_t z = *reinterpret_cast<const f32x4_t*>(zr + c);
     const f32x4_t u = *reinterpret_cast<const f32x4_t*>(zr + f + c);
     const f32x4_t dh = *reinterpret_cast<const f32x4_t*>(dr + c);
+    f32x4_t dz, du, h;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float sg = 1.f / (1.f + expf(-z[k]));
-      const float si = z[k] * sg;
+      const float si = z[k] * sg, d = gt * dh[k];
       sum += dh[k] * (si * u[k]);
-      const float d = gt * dh[k];
-      o[c + k] = ElemOps<T>::from_f(d * u[k] * (sg * (1.f + z[k] * (1.f - sg))));
-      o[f + c + k] = ElemOps<T>::from_f(d * si);
-      hs[(size_t)p * f + c + k] = ElemOps<T>::from_f(gt * (si * u[k]));
+      dz[k] = d * u[k] * (sg * (1.f + z[k] * (1.f - sg)));
+      du[k] = d * si;
+      h[k] = gt * (si * u[k]);
     }
+    *reinterpret_cast<f32x4_t*>(o + c) = dz;
+    *reinterpret_cast<f32x4_t*>(o + f + c) = du;
+    *reinterpret_cast<f32x4_t*>(hs + (size_t)p * f + c) = h;
   }
   sum = block_sum(sum, s);
   if (threadIdx.x == 0) part[p] = sum;
 }
 
-int launch_swiglu_bwd(int dtype, const float* zu, const float* dh, const float* gate_rows,
-                      const int32_t* offsets, int n_ffn, int Tk, int f, void* dzu, void* hs,
+int launch_swiglu_bwd(const float* zu, const float* dh, const float* gate_rows,
+                      const int32_t* offsets, int n_ffn, int Tk, int f, float* dzu, float* hs,
                       float* dgate_part, hipStream_t st) {
-  if (dtype == MOE_BF16)
-    hipLaunchKernelGGL(swiglu_bwd_kernel<__bf16>, dim3(Tk), dim3(256), 0, st, zu, dh, gate_rows,
-                       offsets, n_ffn, f, (__bf16*)dzu, (__bf16*)hs, dgate_part);
-  else
-    hipLaunchKernelGGL(swiglu_bwd_kernel<float>, dim3(Tk), dim3(256), 0, st, zu, dh, gate_rows,
-                       offsets, n_ffn, f, (float*)dzu, (float*)hs, dgate_part);
+  hipLaunchKernelGGL(swiglu_bwd_kernel, dim3(Tk), dim3(256), 0, st, zu, dh, gate_rows, offsets,
+                     n_ffn, f, dzu, hs, dgate_part);
   return check_launch();
 }
 

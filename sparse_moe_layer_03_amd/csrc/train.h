@@ -84,11 +84,11 @@ int launch_gather2(int dtype, const void* x, const void* dy, const float* gate, 
                    const int32_t* offsets, int n_ffn, int Tk, int k, int d, void* xp, void* dyp,
                    float* gate_rows, hipStream_t st);
 
-// Per FFN row p: h, dz, du from z, u and dh (fp32 [rows, f], z and u in
-// `zu` [rows, 2 f]), the row's gate applied; dzu [rows, 2 f] and hs
-// [rows, f] in dtype, dgate_part[p] = <dh, h>.
-int launch_swiglu_bwd(int dtype, const float* zu, const float* dh, const float* gate_rows,
-                      const int32_t* offsets, int n_ffn, int Tk, int f, void* dzu, void* hs,
+// fp32 layers.  Per FFN row p: h, dz, du from z, u and dh ([rows, f], z and u
+// in `zu` [rows, 2 f]), the row's gate applied; dzu [rows, 2 f], hs [rows, f],
+// dgate_part[p] = <dh, h>.
+int launch_swiglu_bwd(const float* zu, const float* dh, const float* gate_rows,
+                      const int32_t* offsets, int n_ffn, int Tk, int f, float* dzu, float* hs,
                       float* dgate_part, hipStream_t st);
 
 // Per token: dgate (parts: partial sums per FFN row), then, with logits,

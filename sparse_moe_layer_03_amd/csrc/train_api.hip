@@ -80,7 +80,6 @@ constexpr int kRouteSplits = 16;  // most token ranges of the router's weight gr
 struct BwdLayout {
   size_t xp, dyp, gates, zu, dh, dzu, hs, part, dl, offs, dxr, drp, total;
   int ep, halves, nsplit, parts;
-  bool mfma;  // the bf16 kernels, with SwiGLU's step in the products' epilogue
 };
 
 static BwdLayout bwd_layout(const moe_shape* s) {
@@ -99,8 +98,7 @@ static BwdLayout bwd_layout(const moe_shape* s) {
   w.nsplit = (int)std::max(1l, std::min({(long)kRouteSplits, (long)s->T / 256,
                                          (cus > 0 ? cus : 256) /
                                              (cdiv(w.ep * w.halves, 256) * cdiv(d, 256))}));
-  w.mfma = s->dtype == MOE_BF16 && s->d_model <= (1 << 20) && s->d_ff <= (1 << 19);
-  w.parts = w.mfma ? swiglu_parts((int)rows, s->n_ffn, s->d_ff) : 1;
+  w.parts = s->dtype == MOE_BF16 ? swiglu_parts((int)rows, s->n_ffn, s->d_ff) : 1;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -110,7 +108,7 @@ static BwdLayout bwd_layout(const moe_shape* s) {
   w.xp = take(rows * d * es);   // with dyp behind it, later the rows' gradients:
   w.dyp = take(rows * d * es);  // fp32 [rows, d]
   w.gates = take(rows * 4);
-  w.zu = take(w.mfma ? 0 : rows * 2 * f * 4);
+  w.zu = take(s->dtype == MOE_BF16 ? 0 : rows * 2 * f * 4);
   w.dh = take(rows * f * 4);
   w.dzu = take(rows * 2 * f * es);
   w.hs = take(rows * f * es);
@@ -126,7 +124,10 @@ static BwdLayout bwd_layout(const moe_shape* s) {
 static int check_backward_shape(const moe_shape* s) {
   const int rc = check_shape(s);
   if (rc) return rc;
-  return (long)s->T * s->top_k < kGmmMaxRows ? MOE_OK : MOE_EUNSUPPORTED;
+  // (2 d_ff and d_model are row lengths of the products)
+  return (long)s->T * s->top_k < kGmmMaxRows && s->d_model <= (1 << 20) && s->d_ff <= (1 << 19)
+             ? MOE_OK
+             : MOE_EUNSUPPORTED;
 }
 
 static int check_backward(const moe_shape* s, const moe_backward_io* io) {
@@ -252,8 +253,8 @@ int moe_layer_backward(const moe_shape* s, const moe_backward_io* io, void* ws, 
   g.s[0] = {dyp, io->w_down, dh, d, f, f, 0, f};
   g.R = g.RB = d;
   if ((rc = run_gmm(MOE_GMM_DX, dt, MOE_F32, g, st))) return rc;
-  // z and u again, and SwiGLU's step
-  if (w.mfma) {
+  // z and u again, and SwiGLU's step (in bf16 behind the products' K loop)
+  if (dt == MOE_BF16) {
     g.s[0] = {xp, io->w_gate, nullptr, d, d, 0, 0, f};
     g.b2 = io->w_up;
     g.gate = gates;
@@ -267,7 +268,8 @@ int moe_layer_backward(const moe_shape* s, const moe_backward_io* io, void* ws, 
     g.s[0] = {xp, io->w_gate, zu, d, d, 2 * f, 0, f};
     g.s[1] = {xp, io->w_up, zu + f, d, d, 2 * f, 0, f};
     if ((rc = run_gmm(MOE_GMM_FWD, dt, MOE_F32, g, st))) return rc;
-    if ((rc = launch_swiglu_bwd(dt, zu, dh, gates, io->offsets, s->n_ffn, Tk, f, dzu, hs, part, st)))
+    if ((rc = launch_swiglu_bwd(zu, dh, gates, io->offsets, s->n_ffn, Tk, f, (float*)dzu,
+                                (float*)hs, part, st)))
       return rc;
   }
   // gradients of the experts' weights

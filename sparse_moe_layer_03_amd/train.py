@@ -324,10 +324,11 @@ def layer_backward(buf: B.LayerBuffers, tb: TrainBuffers, x, w_router, w_gate, w
 
 def train_step(buf: B.LayerBuffers, tb: TrainBuffers, x, w_router, bias, w_gate, w_up, w_down,
                loss_grad, params: MoeAdamwParams, tensors: AdamwTensors, state, logit_bias=None,
-               grad_scale: Optional[torch.Tensor] = None, stream=None):
-    """Forward, backward and AdamW step of one layer: dy = loss_grad(y)."""
+               grad_scale: Optional[torch.Tensor] = None):
+    """Forward, backward and AdamW step of one layer: dy = loss_grad(y).  On
+    the current stream, where loss_grad's own work runs too."""
     y = B.layer_forward(buf, x, w_router, bias, w_gate, w_up, w_down, logit_bias=logit_bias,
-                        logits_out=tb.logits, stream=stream)
-    dx = layer_backward(buf, tb, x, w_router, w_gate, w_up, w_down, loss_grad(y), stream=stream)
-    moe_adamw(params, tensors, state, grad_scale=grad_scale, stream=stream)
+                        logits_out=tb.logits)
+    dx = layer_backward(buf, tb, x, w_router, w_gate, w_up, w_down, loss_grad(y))
+    moe_adamw(params, tensors, state, grad_scale=grad_scale)
     return y, dx

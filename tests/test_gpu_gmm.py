@@ -223,6 +223,85 @@ def test_same_bits_on_another_stream_and_in_a_graph(form):
         assert torch.equal(out, want), k
 
 
+def near(new, ref, mag, n):
+    return not ((new.double() - ref).abs() > sum_bound(mag, n, ref, new.dtype)).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("form", FORMS)
+def test_rows_behind_32_bits(form, dtype):
+    # the last group's rows lie more than 2^32 bytes (and, in a, more than
+    # 2^31 elements) behind the array's start
+    N, K, counts = 64, 2048, [1_100_000, 50]
+    if dtype == "f32" and form == "dw":
+        counts = [0, 50]                # the first group is long enough in bf16
+    dt, dev = DT[dtype], "cuda"
+    M = 1_100_050
+    off = offsets_of(counts) if counts[0] else torch.tensor([0, M - 50, M], dtype=torch.int32, device=dev)
+    a = torch.zeros((M, K), dtype=dt, device=dev)
+    c = torch.zeros((M, N), dtype=dt, device=dev)
+    w = torch.randn((2, N, K), device=dev).to(dt)
+    a[-60:], c[-60:] = torch.randn((60, K), device=dev).to(dt), torch.randn((60, N), device=dev).to(dt)
+    s = T.make_gmm_shape(form, dtype, 2, M, N, K)
+    lhs, rhs, out = {"fwd": (a, w, c), "dx": (c, w, a), "dw": (c, a, w)}[form]
+    ra, rc = a[-60:].clone(), c[-60:].clone()
+    ws = torch.empty(T.moe_grouped_matmul_workspace_bytes(s), dtype=torch.uint8, device=dev)
+    T.moe_grouped_matmul(s, off, lhs, rhs, out, ws)
+    torch.cuda.synchronize()
+    if form == "dw":
+        ref, mag, n = gmm_ref(form, [10, 50], rc, ra)
+        assert near(out[1], ref[1], mag[1], 50)
+        if counts[0]:
+            assert near(out[0], ref[0], mag[0], 64)     # zeros but for ten rows
+    else:
+        ref, mag, n = gmm_ref(form, [10, 50], ra if form == "fwd" else rc, w)
+        assert near(out[-60:], ref, mag, n)
+        assert not out[:1000].any()
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_weights_behind_32_bits(form):
+    G, N, K = 1024, 1544, 1400            # 2.2e9 elements
+    counts = [0] * (G - 3) + [40, 0, 25]
+    s, lhs, rhs, out = make(form, "bf16", [65], N, K)
+    s.n_groups = G
+    w = torch.zeros((G, N, K), dtype=torch.bfloat16, device="cuda")
+    if form != "dw":
+        w[-3:] = torch.randn((3, N, K), device="cuda").bfloat16()
+        rhs = w
+    else:
+        w.fill_(5.0)
+        out = w
+    run(s, counts, lhs, rhs, out)
+    ref, mag, n = gmm_ref(form, counts[-3:], lhs, rhs[-3:] if form != "dw" else rhs)
+    assert near(out[-3:] if form == "dw" else out, ref, mag, n)
+    if form == "dw":
+        assert not out[: G - 3].any() and not out[G - 2].any()
+
+
+def test_two_streams_at_once():
+    jobs = []
+    for seed, form in enumerate(("fwd", "dw", "dx", "dw")):
+        counts, N, K = ([1999, 2100], 40, 56) if seed == 3 else (ragged(30, 90, seed), 264, 520)
+        s, lhs, rhs, out = make(form, "bf16", counts, N, K, seed=seed)
+        ws = torch.empty(T.moe_grouped_matmul_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+        jobs.append((s, offsets_of(counts), lhs, rhs, out, ws))
+    want = []
+    for j in jobs:
+        T.moe_grouped_matmul(*j)
+        torch.cuda.synchronize()
+        want.append(j[4].clone())
+        j[4].zero_()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for j, st in zip(jobs, streams):
+            T.moe_grouped_matmul(*j, stream=st)
+    torch.cuda.synchronize()
+    for j, w in zip(jobs, want):
+        assert torch.equal(j[4], w)
+
+
 def test_refusals():
     s, lhs, rhs, out = make("fwd", "bf16", [40, 24], 72, 64)
     off = offsets_of([40, 24])

@@ -98,6 +98,8 @@ CASES = [
     ("bf16", 777, 512, 100, 28, 64, 12, 9.0, 2.0),
     ("bf16", 300, 64, 1, 0, 128, 1, 1.0, 0.0),
     ("bf16", 2048, 320, 4, 4, 448, 2, 1.0, 0.0),
+    ("bf16", 50, 64, 300, 724, 64, 16, 1.0, 0.0),       # the most experts and slots
+    ("f32", 50, 64, 300, 723, 64, 16, 1.0, 0.0),
 ]
 
 

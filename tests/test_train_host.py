@@ -109,6 +109,8 @@ def test_layer_backward_refuses_bad_arguments():
     assert backward(s, logits=0, w_router=0, dlogits=0) == EINVAL
     assert backward(shape(d_ff=100)) == EUNSUPPORTED
     assert backward(shape(T=0)) == EINVAL
+    assert backward(shape(d_model=(1 << 20) + 64)) == EUNSUPPORTED
+    assert backward(shape(d_ff=(1 << 19) + 64)) == EUNSUPPORTED
     assert backward(shape(T=1 << 26)) == EUNSUPPORTED                         # T * top_k = 2^27
     assert T.lib().moe_layer_backward(ctypes.byref(s), None, P(A), None) == EINVAL
     assert T.moe_layer_backward_workspace_bytes(shape(T=0)) == 0
