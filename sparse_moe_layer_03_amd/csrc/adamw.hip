@@ -250,13 +250,15 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(AdamArgs a) {
       vk = a.b2 * vk + a.nb2 * gk * gk;
       m[k] = mk;
       v[k] = vk;
-      // the update itself takes the hardware's root and reciprocal (an ulp each)
+      // The root is sqrtf: the hardware's alone takes a v below the normal
+      // numbers for 0 and would leave eps in the denominator.  The reciprocal
+      // is the hardware's (an ulp): its operand is at least eps >= 1e-30.
       float root;
       if (Q8) {
         r[k] = sqrtf(vk);
         root = r[k] * sic2;
       } else {
-        root = __builtin_amdgcn_sqrtf(vk * ic2);
+        root = sqrtf(vk * ic2);
       }
       p[k] = p[k] * keep - (mk * lrc1) * __builtin_amdgcn_rcpf(root + a.eps);
     }

@@ -312,3 +312,20 @@ def test_refusals():
         T.moe_adamw(T.make_adamw_params(**HYPER), T.AdamwTensors(ts), torch.zeros(2, dtype=torch.int32, device="cuda"))
     with pytest.raises(B.MoeError, match="EINVAL"):
         T.moe_adamw(T.make_adamw_params(-1.0), T.AdamwTensors(ts), T.new_adamw_state())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("g", [1e-17, 1e-19, 3e-20])
+def test_second_moment_below_the_normal_numbers(bits, g):
+    # With beta1 = beta2 = 0 and p = 0 the step is lr g / (|g| + eps), here lr.
+    # g^2 is a multiple of 2^-149, so rounded by at most 2^-150; half of that,
+    # relative to g^2, is in its root.  The rest as in check().
+    say(f"[adamw] bits={bits} gradient {g}")
+    h = dict(lr=1e-2, beta1=0.0, beta2=0.0, eps=1e-30)
+    ts = make([300], F32, F32, False, bits, fresh=True)
+    ts[0]["param"].zero_()
+    ts[0]["grad"].fill_(g)
+    T.moe_adamw(T.make_adamw_params(**h, state_bits=bits), T.AdamwTensors(ts), T.new_adamw_state())
+    torch.cuda.synchronize()
+    off = (ts[0]["param"].double() / -h["lr"] - 1).abs().max().item()
+    assert off <= EPS + 2.0 ** -150 / g ** 2 / 2, off
