@@ -127,7 +127,8 @@ size_t moe_layer_backward_workspace_bytes(const moe_shape* shape);
  * 2^19; outputs must not overlap inputs or each other. */
 int moe_layer_backward(const moe_shape* shape, const moe_backward_io* io, void* ws, void* stream);
 
-/* Hyper-parameters of an AdamW step (host struct, copied into the launch). */
+/* Hyper-parameters of an AdamW step (host struct, copied into the launch);
+ * finite in fp32. */
 typedef struct {
   double lr;           /* learning rate, >= 0                                */
   double beta1, beta2; /* decay of the moments, in [0, 1)                    */
@@ -150,7 +151,7 @@ typedef struct {
   int64_t n;
   int32_t param_dtype;  /* moe_dtype                                         */
   int32_t grad_dtype;   /* moe_dtype                                         */
-  double weight_decay;  /* >= 0, finite                                      */
+  double weight_decay;  /* >= 0, finite in fp32                              */
 } moe_adamw_tensor;
 
 /* Memory of the optimizer; lives in DEVICE memory, caller-owned,

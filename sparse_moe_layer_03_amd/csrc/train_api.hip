@@ -354,7 +354,9 @@ int moe_adamw(const moe_adamw_params* hp, const moe_adamw_tensor* tensors, int32
               moe_adamw_state* state, const float* grad_scale, const float* lr_scale,
               void* stream) {
   if (!hp || !tensors || !state || n_tensors < 1) return MOE_EINVAL;
-  if (!isfinite(hp->lr) || !isfinite(hp->beta1) || !isfinite(hp->beta2) || !isfinite(hp->eps))
+  // as the kernel takes them: fp32
+  if (!isfinite((float)hp->lr) || !isfinite(hp->beta1) || !isfinite(hp->beta2) ||
+      !isfinite((float)hp->eps))
     return MOE_ENONFINITE;
   if (hp->lr < 0 || hp->beta1 < 0 || hp->beta1 >= 1 || hp->beta2 < 0 || hp->beta2 >= 1 ||
       (float)hp->eps < 1e-30f)
@@ -365,7 +367,7 @@ int moe_adamw(const moe_adamw_params* hp, const moe_adamw_tensor* tensors, int32
   for (int k = 0; k < n_tensors; ++k) {
     const moe_adamw_tensor& t = tensors[k];
     if (t.n < 0) return MOE_EINVAL;
-    if (!isfinite(t.weight_decay)) return MOE_ENONFINITE;
+    if (!isfinite((float)t.weight_decay)) return MOE_ENONFINITE;
     if (t.weight_decay < 0) return MOE_EINVAL;
     if ((t.param_dtype != MOE_F32 && t.param_dtype != MOE_BF16) ||
         (t.grad_dtype != MOE_F32 && t.grad_dtype != MOE_BF16))

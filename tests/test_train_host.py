@@ -175,3 +175,9 @@ def test_binding_refuses_tensors_that_the_call_cannot_read():
         T.BackwardIO(**names).check(shape())
     with pytest.raises(ValueError, match="dtype"):
         T.make_gmm_shape("fwd", torch.float16, 2, 4, 8, 8)
+
+
+def test_adamw_refuses_what_is_infinite_in_fp32():
+    assert adamw({"lr": 1e300}) == ENONFINITE
+    assert adamw({"eps": 1e39}) == ENONFINITE
+    assert adamw(weight_decay=1e39) == ENONFINITE
