@@ -143,7 +143,8 @@ typedef struct {
   void* param;          /* updated in place                                  */
   const void* grad;
   float* master;        /* fp32 copy that is updated, param being its
-                           rounding; NULL: param itself is the value         */
+                           rounding; NULL: param itself is the value; an
+                           fp32 param may be its own                         */
   void* m;              /* first moment: fp32 [n], or e4m3 codes [n]         */
   void* v;              /* second moment: fp32 [n], or e4m3 codes of its root*/
   float* m_scale;       /* 8-bit states: fp32 [ceil(n / 256)], else NULL     */
@@ -178,12 +179,13 @@ typedef struct {
  * largest magnitude / 448; element i stands for code * scale, for v the
  * square of that.  The new value is rounded at random to one of the two
  * neighbouring codes so that its mean (the mean of its square, for v) is
- * exact: rounding to nearest would hold on to an average that moves by less
- * than half a code each step.  A v > 0 never becomes 0.  The random numbers
- * depend on (seed, step, tensor's place in the list, i) only.  A gradient
+ * kept, to 2^-16 of the codes' distance: rounding to nearest would hold on to
+ * an average that moves by less than half a code each step.  A v > 0 never
+ * becomes 0.  The random numbers depend on (seed, step, tensor's place in the
+ * list, i) only.  A gradient
  * that is not finite reaches its own element (8 bits: its block); to leave a
- * step out, pass a grad_scale that is not finite.  No array may be in the
- * list twice. */
+ * step out, pass a grad_scale that is not finite.  An array that is written
+ * must not overlap any other of the list (a tied weight is listed once). */
 int moe_adamw(const moe_adamw_params* params, const moe_adamw_tensor* tensors, int32_t n_tensors,
               moe_adamw_state* state, const float* grad_scale, const float* lr_scale,
               void* stream);

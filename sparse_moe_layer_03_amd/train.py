@@ -235,7 +235,9 @@ def make_adamw_params(lr, beta1=0.9, beta2=0.999, eps=1e-8, state_bits=32, seed=
 class AdamwTensors:
     """The list of parameter tensors of one optimizer.  Each entry is a dict
     with param, grad, m, v, and where used master, m_scale, v_scale and
-    weight_decay (default 0)."""
+    weight_decay (default 0).  Arrays that are written may not overlap any
+    other (a tied weight is listed once); gradients may overlap each other, and
+    an fp32 param may be its own master."""
 
     def __init__(self, tensors):
         self.tensors = [dict(t) for t in tensors]
@@ -244,6 +246,7 @@ class AdamwTensors:
         self.device = self.tensors[0]["param"].device
         self.state_bits = 32 if self.tensors[0]["m"].dtype == torch.float32 else 8
         self.c = (MoeAdamwTensor * len(self.tensors))()
+        spans = []              # bytes from, to, name, written
         codes = (torch.float8_e4m3fn, torch.uint8)
         for i, t in enumerate(self.tensors):
             n, f32 = t["param"].numel(), torch.float32
@@ -256,14 +259,28 @@ class AdamwTensors:
             if t.get("master") is not None:
                 kinds["master"] = f32
             for name, dt in kinds.items():
-                _need(f"tensors[{i}].{name}", t.get(name), dt,
-                      blocks if name.endswith("_scale") else n, self.device)
+                held = blocks if name.endswith("_scale") else n
+                _need(f"tensors[{i}].{name}", t.get(name), dt, held, self.device)
+                at = t[name].data_ptr()
+                own = name == "master" and t["param"].dtype == f32 and at == t["param"].data_ptr()
+                if held and not own:
+                    spans.append((at, at + held * t[name].element_size(), f"tensors[{i}].{name}",
+                                  name != "grad"))
             if t["grad"].numel() != n:
                 raise ValueError(f"tensors[{i}].grad: {t['grad'].numel()} elements, needed {n}")
             self.c[i] = MoeAdamwTensor(
                 *[B._p(t.get(k)) for k in ("param", "grad", "master", "m", "v", "m_scale", "v_scale")],
                 n, _dtype_code(t["param"].dtype), _dtype_code(t["grad"].dtype),
                 float(t.get("weight_decay", 0.0)))
+        spans.sort(key=lambda x: x[:2])
+        last = written = (0, 0, "", False)      # of the spans so far, those that end last
+        for span in spans:
+            other = last if span[3] else written
+            if span[0] < other[1]:
+                raise ValueError(f"{other[2]} and {span[2]} overlap")
+            last = max(last, span, key=lambda x: x[1])
+            if span[3]:
+                written = max(written, span, key=lambda x: x[1])
 
 
 def new_adamw_state(device="cuda") -> torch.Tensor:

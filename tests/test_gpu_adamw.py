@@ -329,3 +329,20 @@ def test_second_moment_below_the_normal_numbers(bits, g):
     torch.cuda.synchronize()
     off = (ts[0]["param"].double() / -h["lr"] - 1).abs().max().item()
     assert off <= EPS + 2.0 ** -150 / g ** 2 / 2, off
+
+
+def test_refuses_arrays_that_overlap():
+    ts = make([512, 512])
+    T.AdamwTensors([ts[0], {**ts[1], "grad": ts[0]["grad"]}])               # read only: allowed
+    T.AdamwTensors([ts[0], {**ts[1], "grad": ts[0]["grad"][:512]}])
+    both = torch.zeros(1024, device="cuda")
+    T.AdamwTensors([{**ts[0], "m": both[:512], "v": both[512:]}])           # side by side: allowed
+    for bad in ([ts[0], ts[0]],                                             # a tied weight
+                [ts[0], {**ts[1], "m": ts[0]["m"]}],
+                [{**ts[0], "v": ts[0]["m"]}],
+                [{**ts[0], "grad": ts[0]["master"]}],
+                [ts[0], {**ts[1], "grad": ts[0]["v"]}],
+                [{**ts[0], "m": both[:512], "v": both[511:1023]}],
+                [{**ts[0], "m": both[256:768]}, {**ts[1], "grad": both[:512]}]):
+        with pytest.raises(ValueError, match="overlap"):
+            T.AdamwTensors(bad)
