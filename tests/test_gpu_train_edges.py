@@ -1,0 +1,40 @@
+"""The training operators at the edges of what moe_train.h allows: more tokens
+than a launch has workgroups."""
+
+import pytest
+import torch
+
+from tests.test_gpu_layer_backward import Case, TOL, far
+
+pytestmark = pytest.mark.gpu
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_more_tokens_than_workgroups(dtype):
+    # the kernels that have a token or row per workgroup walk over them in
+    # strides of 2^20; the second stride is 77 tokens long.  TOL holds: a weight
+    # gradient sums 2^17 rows in blocks of 128 (fp32) or runs of 32 (bf16), n
+    # additions of up to 2^-23 of the running sum, in the norm sqrt(n / 2) 2^-23
+    # with n = 2^10 or 2^12.
+    T = (1 << 20) + 77
+    say(f"[edges] {dtype} T={T}")
+    c = Case(dtype, T, 64, 6, 2, 64, 1, 1.5, 0.5)
+    for n in ("dx", "dgate", "dlogits", "dw_router", "dw_gate", "dw_up", "dw_down"):
+        getattr(c.tb, n).fill_(float("nan"))
+    tb, ref = c.backward(), c.reference()
+    for name, want in ref.items():
+        assert far(getattr(tb, name), want) <= TOL[dtype], name
+    assert far(tb.dx[-77:], ref["dx"][-77:]) <= TOL[dtype]
+    assert torch.isfinite(tb.dgate).all() and torch.isfinite(tb.dlogits).all()
+    # dgate of the last tokens by themselves
+    x, dy, idx = c.x[-99:].double(), c.dy[-99:].double(), c.buf.topk_idx[-99:, 0].long()
+    want = (x * dy).sum(1)
+    for e in range(c.n_ffn):
+        t = idx == e
+        h = torch.nn.functional.silu(x[t] @ c.wg[e].double().t()) * (x[t] @ c.wu[e].double().t())
+        want[t] = ((dy[t] @ c.wd[e].double()) * h).sum(1)
+    assert far(tb.dgate[-99:, 0], want) <= 1e-5
