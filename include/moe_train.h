@@ -114,11 +114,12 @@ size_t moe_layer_backward_workspace_bytes(const moe_shape* shape);
  *   dz = gate dh u silu'(z),  du = gate dh silu(z)
  *   dw_gate = dz^T x,  dw_up = du^T x,  dw_down = dy^T (gate h)
  *   dlogits = p (dp - sum_e p dp),  p = softmax(logits),
- *             dp[t, topk_idx[t,j]] = routed_scaling dgate[t,j], else 0
+ *             dp[t, e] = routed_scaling sum_{j: topk_idx[t,j] = e} dgate[t,j]
  *   dw_router = dlogits^T x
  *   dx[t] = sum_{FFN j} (dz Wg + du Wu) + (sum_{identity j} gate) dy[t]
  *           + dlogits[t] w_router
- * The selection itself and the bias that steers it have no gradient.  With
+ * The selection itself and the bias that steers it have no gradient; a
+ * selection that moe_route did not make may name an expert twice.  With
  * logits NULL the router is left out: w_router, dlogits and dw_router must
  * be NULL then, and dx holds the experts' part alone.  In bf16, dz, du,
  * gate h and dlogits are rounded to bf16 where they enter a product; all

@@ -170,8 +170,12 @@ __global__ void __launch_bounds__(256) token_bwd_kernel(TokenArgs a) {
     __syncthreads();
     if (tid < a.k) {
       a.dgate[t * a.k + tid] = s_dg[tid];
+      // the sum over the slots of the expert: a caller's own selection may name
+      // one twice (each of its slots writes the same sum)
       const int e = s_e[tid];
-      if ((unsigned)e < (unsigned)a.E) s_dp[e] = a.scaling * s_dg[tid];
+      float sum = 0.f;
+      for (int j = 0; j < a.k; ++j) sum += s_e[j] == e ? s_dg[j] : 0.f;
+      if ((unsigned)e < (unsigned)a.E) s_dp[e] = a.scaling * sum;
     }
     if (!a.logits) continue;
     __syncthreads();

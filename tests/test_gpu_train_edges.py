@@ -1,9 +1,10 @@
 """The training operators at the edges of what moe_train.h allows: more tokens
-than a launch has workgroups."""
+than a launch has workgroups, a selection that names an expert twice."""
 
 import pytest
 import torch
 
+from sparse_moe_layer_03_amd import binding as B
 from tests.test_gpu_layer_backward import Case, TOL, far
 
 pytestmark = pytest.mark.gpu
@@ -38,3 +39,34 @@ def test_more_tokens_than_workgroups(dtype):
         h = torch.nn.functional.silu(x[t] @ c.wg[e].double().t()) * (x[t] @ c.wu[e].double().t())
         want[t] = ((dy[t] @ c.wd[e].double()) * h).sum(1)
     assert far(tb.dgate[-99:, 0], want) <= 1e-5
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("k", [2, 5, 16])
+def test_an_expert_twice_in_a_token(dtype, k):
+    # a selection by other means than moe_route: FFN and identity experts come up
+    # to k times in a token; the gradient at an expert's logit sums its slots
+    say(f"[edges] twice {dtype} k={k}")
+    c = Case(dtype, 60, 64, 12, 5, 128, k, 1.5, 1.0)
+    g = torch.Generator(device="cuda").manual_seed(k)
+    idx = torch.randint(0, 17, (60, k), generator=g, device="cuda")
+    idx[:20] = torch.randint(0, 3, (20, k), generator=g, device="cuda")
+    idx[20:30] = 13
+    idx[30:40] = 4
+    idx = idx.sort(dim=1).values
+    c.buf.topk_idx.copy_(idx)
+    c.buf.topk_gate.copy_(c.scaling * torch.softmax(c.tb.logits, 1).gather(1, idx))
+    B.moe_dispatch(c.shape, c.buf.topk_idx, c.x, c.buf.counts, c.buf.offsets, c.buf.perm, c.buf.inv_perm, None,
+                   c.buf.ws)
+    tb, ref = c.backward(), c.reference()
+    for name, want in ref.items():
+        assert far(getattr(tb, name), want) <= TOL[dtype], name
+    p = torch.softmax(tb.logits.double(), 1)
+    dp = torch.zeros_like(p).scatter_add_(1, idx, c.scaling * tb.dgate.double())
+    want = p * (dp - (p * dp).sum(1, keepdim=True))
+    # fp32 from dgate on, sums of k slots and 17 experts: fewer than 32 roundings
+    # of 2^-24 of the terms p dp
+    assert ((tb.dlogits.double() - want).abs() <= 32 * 2.0 ** -23 * (p * (dp.abs() + (p * dp.abs()).sum(1, keepdim=True)))).all()
+    first = tb.dlogits.clone()
+    c.backward()
+    assert torch.equal(first, tb.dlogits)
