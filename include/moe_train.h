@@ -119,7 +119,9 @@ size_t moe_layer_backward_workspace_bytes(const moe_shape* shape);
  *   dx[t] = sum_{FFN j} (dz Wg + du Wu) + (sum_{identity j} gate) dy[t]
  *           + dlogits[t] w_router
  * The selection itself and the bias that steers it have no gradient; a
- * selection that moe_route did not make may name an expert twice.  With
+ * selection that moe_route did not make may name an expert twice.
+ * moe_route's logit_bias enters p as the logits do: its gradient is
+ * sum_t dlogits[t, :], which is left to the caller to form.  With
  * logits NULL the router is left out: w_router, dlogits and dw_router must
  * be NULL then, and dx holds the experts' part alone.  In bf16, dz, du,
  * gate h and dlogits are rounded to bf16 where they enter a product; all

@@ -343,7 +343,9 @@ def train_step(buf: B.LayerBuffers, tb: TrainBuffers, x, w_router, bias, w_gate,
                loss_grad, params: MoeAdamwParams, tensors: AdamwTensors, state, logit_bias=None,
                grad_scale: Optional[torch.Tensor] = None):
     """Forward, backward and AdamW step of one layer: dy = loss_grad(y).  On
-    the current stream, where loss_grad's own work runs too."""
+    the current stream, where loss_grad's own work runs too.  The step updates
+    what ``tensors`` lists; a logit_bias that is trained has the gradient
+    ``tb.dlogits.sum(0)``, which the step does not form."""
     y = B.layer_forward(buf, x, w_router, bias, w_gate, w_up, w_down, logit_bias=logit_bias,
                         logits_out=tb.logits)
     dx = layer_backward(buf, tb, x, w_router, w_gate, w_up, w_down, loss_grad(y))

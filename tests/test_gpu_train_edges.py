@@ -1,5 +1,6 @@
 """The training operators at the edges of what moe_train.h allows: more tokens
-than a launch has workgroups, a selection that names an expert twice."""
+than a launch has workgroups, a selection that names an expert twice;
+the gradient of the logits' offsets, which the caller forms."""
 
 import pytest
 import torch
@@ -70,3 +71,20 @@ def test_an_expert_twice_in_a_token(dtype, k):
     first = tb.dlogits.clone()
     c.backward()
     assert torch.equal(first, tb.dlogits)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradient_of_the_logits_offsets(dtype):
+    # moe_train.h: the sum of dlogits over the tokens.  dlogits are fp32 from end
+    # to end whatever the type: 1e-5 as in the test of dlogits itself, measured
+    # by the norm of what the differences p (dp - sum p dp) cancel from
+    c = Case(dtype, 300, 128, 9, 4, 128, 3, 2.5, 1.0)
+    tb = c.backward()
+    leaves = [v.detach() for v in c.leaves()]
+    lb = c.lb = c.lb.double().requires_grad_()
+    c.loss(*leaves).backward()
+    p = torch.softmax(tb.logits.double(), 1)
+    dp = torch.zeros_like(p).scatter_(1, c.buf.topk_idx.long(), c.scaling * tb.dgate.double())
+    room = 1e-5 * (p * dp).norm().item() * 300 ** 0.5
+    assert (tb.dlogits.double().sum(0) - lb.grad).norm().item() <= room
+    assert lb.grad.norm().item() > 100 * room
