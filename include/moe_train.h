@@ -123,9 +123,12 @@ size_t moe_layer_backward_workspace_bytes(const moe_shape* shape);
  * moe_route's logit_bias enters p as the logits do: its gradient is
  * sum_t dlogits[t, :], which is left to the caller to form.  With
  * logits NULL the router is left out: w_router, dlogits and dw_router must
- * be NULL then, and dx holds the experts' part alone.  In bf16, dz, du,
- * gate h and dlogits are rounded to bf16 where they enter a product; all
- * else is fp32 until the results are rounded.
+ * be NULL then, and dx holds the experts' part alone.  In bf16, dz, du and
+ * gate h are rounded to bf16 where they enter a product, and dlogits enters
+ * as two bf16 values, the rounded one and what the rounding leaves; all else
+ * is fp32 until the results are rounded.  With `accumulate` the old value is
+ * added in fp32 and the sum rounded to dtype: a bf16 gradient that is summed
+ * over many passes is rounded in each of them.
  * Shape limits as in moe.h, and T * top_k < 2^27, d_model <= 2^20, d_ff <=
  * 2^19; outputs must not overlap inputs or each other. */
 int moe_layer_backward(const moe_shape* shape, const moe_backward_io* io, void* ws, void* stream);
