@@ -258,14 +258,19 @@ int moe_eplb_plan(const moe_shape* shape, int32_t n_slots, int32_t n_devices,
  * clear != 0.  Release builds: MOE_EUNSUPPORTED, *flags untouched.
  * NULL flags: MOE_EINVAL; a HIP failure: MOE_EHIP. */
 #define MOE_CHECK_ROUTE_ID     (1u << 0) /* top-k wrote an expert id outside [0, E) */
-#define MOE_CHECK_DISPATCH_ID  (1u << 1) /* topk_idx given to dispatch outside [0, E) */
+#define MOE_CHECK_DISPATCH_ID  (1u << 1) /* topk_idx given to dispatch or to the backward pass
+                                            outside [0, E) */
 #define MOE_CHECK_DISPATCH_POS (1u << 2) /* dispatch computed a position outside [0, T*k) */
-#define MOE_CHECK_GEMM_ROW     (1u << 3) /* expert GEMM: gathered token outside [0, T) */
+#define MOE_CHECK_GEMM_ROW     (1u << 3) /* expert GEMM, backward pass: gathered token outside
+                                            [0, T) */
 #define MOE_CHECK_GEMM_ITEMS   (1u << 4) /* expert GEMM: a workgroup got more work items
                                             than it can track */
 #define MOE_CHECK_GEMM_TILE    (1u << 5) /* expert GEMM: a tile outside its expert's rows
                                             or the output columns */
-#define MOE_CHECK_COMBINE_ROW  (1u << 6) /* combine: a slot's y_perm row outside [0, T*k) */
+#define MOE_CHECK_COMBINE_ROW  (1u << 6) /* combine, backward pass: a slot's row outside
+                                            [0, T*k) */
+#define MOE_CHECK_GMM_OFFSETS  (1u << 7) /* grouped products: offsets outside [0, M] or not
+                                            ascending */
 int moe_debug_checks(uint32_t* flags, int clear);
 
 #ifdef __cplusplus

@@ -15,7 +15,7 @@
  *     checked on the host before anything is enqueued.  Offsets and routing
  *     arrays in device memory cannot be: the kernels keep every row that they
  *     name inside the arrays, so wrong ones give wrong values and never an
- *     access out of range.
+ *     access out of range (the debug build reports them, moe_debug_checks).
  *   - Sums are formed in a fixed order, without atomics: the same call gives
  *     the same bits.
  */

@@ -35,7 +35,7 @@ ENTRY_POINTS = ("moe_workspace_bytes", "moe_strerror", "moe_device_cu_count", "m
 CHECK_BITS = {1 << 0: "MOE_CHECK_ROUTE_ID", 1 << 1: "MOE_CHECK_DISPATCH_ID",
               1 << 2: "MOE_CHECK_DISPATCH_POS", 1 << 3: "MOE_CHECK_GEMM_ROW",
               1 << 4: "MOE_CHECK_GEMM_ITEMS", 1 << 5: "MOE_CHECK_GEMM_TILE",
-              1 << 6: "MOE_CHECK_COMBINE_ROW"}
+              1 << 6: "MOE_CHECK_COMBINE_ROW", 1 << 7: "MOE_CHECK_GMM_OFFSETS"}
 
 
 class MoeShape(ctypes.Structure):

@@ -392,7 +392,8 @@ int moe_debug_checks(uint32_t* flags, int clear) {
     return MOE_EHIP;
   }
   unsigned (*const words[])(bool) = {check_word_route, check_word_dispatch, check_word_gemm,
-                                     check_word_gemm_big, check_word_combine, check_word_layer_bwd};
+                                     check_word_gemm_big, check_word_combine, check_word_gmm_general,
+                                     check_word_gmm_mfma, check_word_layer_bwd};
   uint32_t v = 0;
   for (auto* fn : words) {
     const unsigned w = fn(clear != 0);

@@ -61,8 +61,10 @@ __device__ __forceinline__ void put(TO* p, float v, bool add) {
 
 // Rows [lo, hi) of a group, inside [0, M] whatever the offsets hold.
 __device__ __forceinline__ void group_rows(const int32_t* offsets, int e, int M, int& lo, int& hi) {
-  lo = min(max(offsets[e], 0), M);
-  hi = min(max(offsets[e + 1], lo), M);
+  const int first = offsets[e], end = offsets[e + 1];
+  MOE_CHECK(0 <= first && first <= end && end <= M, MOE_CHECK_GMM_OFFSETS);
+  lo = min(max(first, 0), M);
+  hi = min(max(end, lo), M);
 }
 
 template <typename T, typename TO, int FORM, int BM, bool VEC>
@@ -345,6 +347,8 @@ int launch_gmm_general(int form, int dtype, int out_dtype, bool vec, const GmmAr
   if (out_dtype == MOE_F32) return launch_general_form<__bf16, float>(form, vec, g, st);
   return launch_general_form<__bf16, __bf16>(form, vec, g, st);
 }
+
+MOE_CHECK_ACCESSOR(check_word_gmm_general)
 
 int launch_gmm_join(int form, int out_dtype, const GmmArgs& g, hipStream_t st) {
   const long n = (form == MOE_GMM_DW ? (long)g.ngroups * g.s[0].I : (long)g.M) * g.s[0].J;

@@ -77,8 +77,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t descriptor(const char* p, uint
 
 // Rows [lo, hi) of a group, inside [0, M] whatever the offsets hold.
 __device__ __forceinline__ void rows_of(const int32_t* offsets, int e, int M, int& lo, int& hi) {
-  lo = min(max(offsets[e], 0), M);
-  hi = min(max(offsets[e + 1], lo), M);
+  const int first = offsets[e], end = offsets[e + 1];
+  MOE_CHECK(0 <= first && first <= end && end <= M, MOE_CHECK_GMM_OFFSETS);
+  lo = min(max(first, 0), M);
+  hi = min(max(end, lo), M);
 }
 
 // The same for a group known to be one for all lanes, through the scalar
@@ -86,6 +88,7 @@ __device__ __forceinline__ void rows_of(const int32_t* offsets, int e, int M, in
 __device__ __forceinline__ void rows_of_uniform(const int32_t* offsets, int e, int M, int& lo, int& hi) {
   typedef const __attribute__((address_space(4))) int32_t* const_ptr_t;
   const const_ptr_t o = (const_ptr_t)(offsets + e);
+  MOE_CHECK(0 <= o[0] && o[0] <= o[1] && o[1] <= M, MOE_CHECK_GMM_OFFSETS);
   lo = min(max(o[0], 0), M);
   hi = min(max(o[1], lo), M);
 }
@@ -768,6 +771,8 @@ gmm_mfma_kernel(GmmArgs g) {
   }
 #endif
 }
+
+MOE_CHECK_ACCESSOR(check_word_gmm_mfma)
 
 bool mfma_ok(int form, int dtype, int N, int K, int64_t lda, int64_t ldc) {
   if (dtype != MOE_BF16 || K % 8 != 0 || lda % 8 != 0) return false;

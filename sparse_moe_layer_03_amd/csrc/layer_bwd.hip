@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(256) token_bwd_kernel(TokenArgs a) {
       s_e[tid] = e;
       float dg = 0.f;
       const bool inside = (unsigned)row < (unsigned)(a.T * a.k);
+      MOE_CHECK((unsigned)e < (unsigned)a.E, MOE_CHECK_DISPATCH_ID);
       MOE_CHECK(e >= a.n_ffn || inside, MOE_CHECK_COMBINE_ROW);
       if (e < a.n_ffn && inside)
         for (int q = 0; q < a.parts; ++q) dg += a.part[(size_t)row * a.parts + q];

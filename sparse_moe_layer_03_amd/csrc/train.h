@@ -74,9 +74,12 @@ int launch_adamw(const moe_adamw_params* hp, const moe_adamw_tensor* tensors, in
                  hipStream_t st);
 uint64_t adamw_max_elements();
 
-// ---- the layer's backward pass beside its products
+// as the accessors of internal.h
+unsigned check_word_gmm_general(bool clear);
+unsigned check_word_gmm_mfma(bool clear);
+unsigned check_word_layer_bwd(bool clear);
 
-unsigned check_word_layer_bwd(bool clear);  // as the accessors of internal.h
+// ---- the layer's backward pass beside its products
 
 // The FFN rows of x and dy grouped by expert, and their gates: for p <
 // offsets[n_ffn], row perm[p] / k of each, gate_rows[p] = gate[perm[p]].
