@@ -1,12 +1,18 @@
 """The training operators at the edges of what moe_train.h allows: more tokens
 than a launch has workgroups, a selection that names an expert twice;
-the gradient of the logits' offsets, which the caller forms."""
+the gradient of the logits' offsets, which the caller forms; errors in the
+norm, real widths, streams that have a part of the CUs."""
 
 import pytest
 import torch
 
 from sparse_moe_layer_03_amd import binding as B
+from sparse_moe_layer_03_amd import scmoe
+from sparse_moe_layer_03_amd import train as T
+from tests.test_gpu_adamw import HYPER, clone, make as make_adamw
+from tests.test_gpu_gmm import make, ragged, run
 from tests.test_gpu_layer_backward import Case, TOL, far
+from tests.train_util import U, gmm_ref, offsets_of
 
 pytestmark = pytest.mark.gpu
 
@@ -22,9 +28,9 @@ def test_more_tokens_than_workgroups(dtype):
     # gradient sums 2^17 rows in blocks of 128 (fp32) or runs of 32 (bf16), n
     # additions of up to 2^-23 of the running sum, in the norm sqrt(n / 2) 2^-23
     # with n = 2^10 or 2^12.
-    T = (1 << 20) + 77
-    say(f"[edges] {dtype} T={T}")
-    c = Case(dtype, T, 64, 6, 2, 64, 1, 1.5, 0.5)
+    Tn = (1 << 20) + 77
+    say(f"[edges] {dtype} T={Tn}")
+    c = Case(dtype, Tn, 64, 6, 2, 64, 1, 1.5, 0.5)
     for n in ("dx", "dgate", "dlogits", "dw_router", "dw_gate", "dw_up", "dw_down"):
         getattr(c.tb, n).fill_(float("nan"))
     tb, ref = c.backward(), c.reference()
@@ -88,3 +94,94 @@ def test_gradient_of_the_logits_offsets(dtype):
     room = 1e-5 * (p * dp).norm().item() * 300 ** 0.5
     assert (tb.dlogits.double().sum(0) - lb.grad).norm().item() <= room
     assert lb.grad.norm().item() > 100 * room
+
+
+@pytest.mark.parametrize("form", ("fwd", "dx", "dw"))
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("f32", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("odd", [0, 1])
+@pytest.mark.parametrize("split", [False, True])
+def test_errors_in_the_norm(form, dtype, out, odd, split):
+    # A sum of n products has n additions, each off by at most 2^-23 of the
+    # running sum; with products of random signs that grows like the root of the
+    # terms so far, and independent errors add up to sqrt(n / 2) 2^-23 of the
+    # result in the norm: 4e-6 at n = 2048, where partial sums in bf16 would
+    # leave 1e-3.  The result is rounded once (at most U of each value).
+    n = 2048
+    counts, N, K = ([n - 5, n], 136, 264) if form == "dw" else ([300, 7, 90], n, n)
+    if form != "dw":
+        N, K = (136, n) if form == "fwd" else (n, 136)
+    if split:                               # few tiles: the reduction in ranges
+        counts, N, K = ([n, n], 40, 56) if form == "dw" else ([3, 20], min(N, 264), min(K, 264))
+        N, K = (N, n) if form == "fwd" else (n, K) if form == "dx" else (N, K)
+    N, K = N + odd, K + odd
+    say(f"[edges] norm {form} {dtype} {out} {counts} {N} {K}")
+    s, lhs, rhs, o = make(form, dtype, counts, N, K, out=out)
+    if split:
+        assert T.moe_grouped_matmul_workspace_bytes(s) > 0
+    run(s, counts, lhs, rhs, o)
+    ref, _, longest = gmm_ref(form, counts, lhs, rhs)
+    err = far(o, ref)
+    say(f"  {err:.2e}")
+    assert err <= (longest / 2) ** 0.5 * 2.0 ** -23 + (U[o.dtype] if out == "bf16" else 0.0)
+
+
+@pytest.mark.parametrize("case", [("bf16", 4096, 2048, 24, 8, 1024, 4, 1.0, 1.0),
+                                  ("bf16", 1500, 4096, 12, 6, 1536, 3, 2.5, 2.0),
+                                  ("f32", 700, 2048, 6, 3, 1024, 3, 1.0, 1.0)], ids=lambda c: "-".join(map(str, c)))
+def test_layers_of_real_widths(case):
+    say("[edges]", case)
+    c = Case(*case)
+    tb, ref = c.backward(), c.reference()
+    for name, want in ref.items():
+        err = far(getattr(tb, name), want)
+        say(f"  {name} {err:.2e}")
+        assert err <= TOL[case[0]], (name, err)
+
+
+@pytest.mark.parametrize("cus", [32, 64])
+def test_on_a_part_of_the_cus(cus):
+    # tiles and grids go by the CUs that the stream has; the order of every sum
+    # does not, so the results are the whole chip's bit for bit
+    jobs = []
+    for form, dtype, counts, N, K in (
+            ("fwd", "bf16", ragged(40, 90), 1112, 264), ("fwd", "bf16", ragged(60, 200), 2056, 328),
+            ("dx", "bf16", ragged(48, 80), 264, 2056), ("dx", "bf16", ragged(60, 200), 328, 2056),
+            ("dw", "bf16", ragged(40, 50), 776, 1032), ("dw", "bf16", ragged(9, 700), 264, 520),
+            ("dw", "bf16", [1999, 2100], 40, 56), ("fwd", "f32", ragged(30, 90), 392, 136),
+            ("dx", "f32", ragged(30, 20), 136, 392), ("dw", "f32", ragged(30, 90), 137, 391),
+            ("fwd", "bf16", [3, 20], 48, 2056)):
+        s, lhs, rhs, out = make(form, dtype, counts, N, K)
+        run(s, counts, lhs, rhs, out)
+        ws = torch.empty(T.moe_grouped_matmul_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+        jobs.append((out.clone(), (s, offsets_of(counts), lhs, rhs, out, ws)))
+    layers = [Case("bf16", 600, 256, 12, 6, 192, 4, 1.0, 1.0), Case("f32", 200, 64, 5, 2, 128, 3, 1.0, 1.0)]
+    names = ("dx", "dgate", "dlogits", "dw_router", "dw_gate", "dw_up", "dw_down")
+    grads = [{n: getattr(c.backward(), n).clone() for n in names} for c in layers]
+    ts = make_adamw([300_001, 77], bits=8)
+    twin = clone(ts)
+    params = T.make_adamw_params(**HYPER, state_bits=8, seed=3)
+    T.moe_adamw(params, T.AdamwTensors(ts), T.new_adamw_state())
+    ms = scmoe.MaskedStream(scmoe.cu_mask(B.moe_device_cu_count(), 0, cus, "contiguous"))
+    try:
+        for want, job in jobs:
+            job[4].zero_()
+            torch.cuda.synchronize()
+            T.moe_grouped_matmul(*job, stream=ms.stream)
+            torch.cuda.synchronize()
+            say(f"[edges] {cus} CUs, {job[0].form} N={job[0].N} K={job[0].K}")
+            assert torch.equal(job[4], want), (job[0].form, job[0].N, job[0].K)
+        for c, want in zip(layers, grads):
+            c.backward(stream=ms.stream)
+            for n in names:
+                assert torch.equal(getattr(c.tb, n), want[n]), n
+        state = T.new_adamw_state()
+        tensors = T.AdamwTensors(twin)
+        torch.cuda.synchronize()
+        T.moe_adamw(params, tensors, state, stream=ms.stream)
+        torch.cuda.synchronize()
+        for a, b in zip(ts, twin):
+            for k in a:
+                if isinstance(a[k], torch.Tensor):
+                    assert torch.equal(a[k].view(torch.uint8), b[k].view(torch.uint8)), k
+    finally:
+        ms.close()
