@@ -124,6 +124,8 @@ def _workspace(ws, need, device):
 def _on(device, call, stream):
     """call(stream's handle) with `device` as the current one; the stream is
     the device's current one by default."""
+    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        raise ValueError(f"stream: on {stream.device}, needed on {device}")
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return call(B._stream(stream))
