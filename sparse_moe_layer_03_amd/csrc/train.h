@@ -35,7 +35,8 @@ struct GmmArgs {
   int RB;                  // DX: rows that a group of b, and of b2, holds; behind
                            // them the reduction reads zeros
   int r_switch;            // DX: reduction rows from here on (a multiple of 64)
-                           // come from b2, from its first one (0: none)
+                           // come from b2, from its first one (0: none; bf16:
+                           // on the MFMA kernels' 16-byte rows only)
   const void* b2;          // DX: see r_switch; SwiGLU step: w_up
   int64_t b_group;         // elements between groups of b (FWD, DX)
   int64_t out_group;       // elements between groups of out (DW)
@@ -51,10 +52,8 @@ struct GmmArgs {
   float* dpart;            // [rows, swiglu_parts()]
 };
 
-// Any sizes, strides and element types.  vec: rows of a and b start at
-// multiples of four elements.
-int launch_gmm_general(int form, int dtype, int out_dtype, bool vec, const GmmArgs& g,
-                       hipStream_t st);
+// Any sizes, strides and element types.
+int launch_gmm_general(int form, int dtype, int out_dtype, const GmmArgs& g, hipStream_t st);
 // bf16 products on bf16 MFMAs (gmm_mfma.hip; FWD: one product).
 // Whether a product can run there: 16-byte rows and row starts, and sizes
 // that 32-bit offsets within a tile reach.

@@ -34,18 +34,20 @@ static int check_gmm(const moe_gmm_shape* s) {
 // A product with too few output tiles to fill the chip has its reduction cut
 // into this many ranges, each at least 256 long, whose fp32 partial outputs
 // are joined by a second kernel.  A function of the sizes and the device's CU
-// count only: it sizes the workspace (at most a tile per CU: 16 MiB).
-static int gmm_nsplit(int form, long G, long M, long I, long J, long R, int cus) {
+// count only: it sizes the workspace (at most `fill` tiles per CU: 16 MiB each).
+static int gmm_nsplit(int form, long G, long M, long I, long J, long R, int fill, int cus) {
   const long jt = cdiv(J, 128);
   const long tiles = form == MOE_GMM_DW ? G * cdiv(I, 128) * jt : (M / 128 + std::min(G, M)) * jt;
   const long red = form == MOE_GMM_DW ? M / G : R;
   if (tiles < 1) return 1;
-  return (int)std::max(1l, std::min({64l, cus / tiles, red / 256}));
+  return (int)std::max(1l, std::min({64l, (long)fill * cus / tiles, red / 256}));
 }
 
 static int gmm_splits_of(const moe_gmm_shape* s, int cus) {
   const bool fwd = s->form == MOE_GMM_FWD;
-  return gmm_nsplit(s->form, s->n_groups, s->M, s->N, fwd ? s->N : s->K, fwd ? s->K : s->N, cus);
+  // fp32 MFMAs are busy with two workgroups on a CU
+  const int fill = s->dtype == MOE_F32 ? 2 : 1;
+  return gmm_nsplit(s->form, s->n_groups, s->M, s->N, fwd ? s->N : s->K, fwd ? s->K : s->N, fill, cus);
 }
 
 static size_t gmm_part_bytes(const moe_gmm_shape* s, int nsplit) {
@@ -58,17 +60,15 @@ static size_t gmm_part_bytes(const moe_gmm_shape* s, int nsplit) {
 // Runs products, a split reduction joined.
 static int run_gmm(int form, int dtype, int out_dtype, const GmmArgs& g, hipStream_t st) {
   const bool fwd = form == MOE_GMM_FWD, dx = form == MOE_GMM_DX;
-  bool mfma = !(fwd && g.nsub > 1), vec = g.b_group % 4 == 0;
+  bool mfma = !(fwd && g.nsub > 1);
   for (int q = 0; q < g.nsub; ++q) {
     const GmmSub& s = g.s[q];
     const int64_t lda = dx ? s.ldo : fwd ? s.lda : s.ldb, ldc = fwd ? s.ldo : s.lda;
     const int N = fwd ? s.J : dx ? g.R : s.I, K = fwd ? g.R : s.J;
-    const bool al = al16(s.a) && al16(s.b);
-    mfma = mfma && al && al16(s.out) && mfma_ok(form, dtype, N, K, lda, ldc);
-    vec = vec && al && s.lda % 4 == 0 && s.ldb % 4 == 0;
+    mfma = mfma && al16(s.a) && al16(s.b) && al16(s.out) && mfma_ok(form, dtype, N, K, lda, ldc);
   }
   const int rc = mfma ? launch_gmm_mfma(form, out_dtype, g, st)
-                      : launch_gmm_general(form, dtype, out_dtype, vec, g, st);
+                      : launch_gmm_general(form, dtype, out_dtype, g, st);
   if (rc || g.nsplit <= 1) return rc;
   return launch_gmm_join(form, out_dtype, g, st);
 }

@@ -1,0 +1,99 @@
+"""moe_grouped_matmul where rows are not multiples of 16 bytes, and in fp32:
+every remainder of a 16-byte chunk on each side, rows shorter than a chunk,
+reductions that end inside a chunk next to NaN, each tile shape's range, more
+tiles than workgroups.  References and bounds as in test_gpu_gmm.py; there and
+in test_gpu_train_guards.py are the strides and what may be written."""
+
+import pytest
+import torch
+
+from sparse_moe_layer_03_amd import train as T
+from tests.test_gpu_gmm import FORMS, check, make, ragged, run
+from tests.train_util import gmm_ref, sum_bound
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("k", range(9))
+def test_every_remainder(form, dtype, k):
+    for n in range(9):
+        check(form, dtype, [3, 0, 70, 18], 64 + n, 72 + k, spare=1, lda=72 + k + n, ldc=64 + n + k)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("small", range(1, 9))
+def test_rows_shorter_than_a_chunk(form, dtype, small):
+    check(form, dtype, [3, 0, 70, 18], small, 130)
+    check(form, dtype, [3, 0, 70, 18], 130, small, accumulate=True)
+    check(form, dtype, [3, 0, 70, 18], small, small, lda=small + 1, ldc=small + 3)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,K", [(67, 101), (130, 133), (3, 5)])
+def test_neighbours_do_not_leak(form, dtype, N, K):
+    # NaN in the other groups' rows and weights, behind the last group and in
+    # the gaps: a chunk at a row's or a group's end reads none of it
+    counts = [5, 70, 0, 33, 64, 1]
+    s, lhs, rhs, out = make(form, dtype, counts, N, K, lda=K + 2, ldc=N + 1, spare=6)
+    nan, rows = float("nan"), sum(counts)
+    mine = slice(5, 75)
+    for t in (lhs, rhs) if form == "dw" else (lhs,):
+        keep = t[mine].clone()
+        whole = torch.as_strided(t, (t.shape[0] - 1, t.stride(0)), (t.stride(0), 1), t.storage_offset())
+        whole.fill_(nan)
+        t[-1].fill_(nan)
+        t[mine] = keep
+    if form != "dw":
+        keep = rhs[1].clone()
+        rhs.fill_(nan)
+        rhs[1] = keep
+    run(s, counts, lhs, rhs, out)
+    if form == "dw":
+        ref, mag, n = gmm_ref(form, [70], lhs[mine], rhs[mine])
+        new = out[1:2]
+    else:
+        ref, mag, n = gmm_ref(form, [70], lhs[mine], rhs[1:2])
+        new = out[mine]
+    assert torch.isfinite(new).all()
+    assert not ((new.double() - ref).abs() > sum_bound(mag, n, ref, out.dtype)).any()
+    assert rows == 173
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("mean", [4, 30, 40, 70, 200])
+def test_tiles_by_rows_per_group(form, dtype, out, mean):
+    check(form, dtype, ragged(48, mean), 257, 391, out=out, spare=9)
+    check(form, dtype, ragged(48, mean), 392, 260, out=out, spare=9, accumulate=True)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_hot_group(form, dtype):
+    # bands of row tiles, a last band that is not full, and empty groups behind
+    check(form, dtype, [1, 0, 3001, 2, 0, 130] + [0] * 30, 129, 517)
+
+
+@pytest.mark.parametrize("form,counts,N,K", [
+    ("dw", [(i * 5) % 7 for i in range(1024)], 333, 261), ("dw", [40] * 300, 515, 515),
+    ("fwd", [3] * 1024, 1031, 9), ("dx", [3] * 1024, 9, 1031), ("fwd", [70] * 200, 1029, 33),
+])
+def test_more_tiles_than_workgroups(form, counts, N, K):
+    for dtype in ("bf16", "f32"):
+        check(form, dtype, counts, N, K)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("R", [2048 + 1, 4096 - 3, 1000])
+def test_split_reductions_of_any_length(form, R):
+    # the last range ends inside a chunk
+    for dtype in ("bf16", "f32"):
+        counts, N, K = ([R, R - 7], 41, 57) if form == "dw" else ([3, 20], 49, R)
+        N, K = (K, N) if form == "dx" else (N, K)
+        s = make(form, dtype, counts, N, K)[0]
+        assert T.moe_grouped_matmul_workspace_bytes(s) > 0
+        check(form, dtype, counts, N, K, spare=7)
