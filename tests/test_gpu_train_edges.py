@@ -23,8 +23,8 @@ def say(*a):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_more_tokens_than_workgroups(dtype):
-    # the kernels that have a token or row per workgroup walk over them in
-    # strides of 2^20; the second stride is 77 tokens long.  TOL holds: a weight
+    # the kernels that have a token or row per workgroup hold them in planes of
+    # 2^20; the second plane is 77 tokens long.  TOL holds: a weight
     # gradient sums 2^17 rows in blocks of 128 (fp32) or runs of 32 (bf16), n
     # additions of up to 2^-23 of the running sum, in the norm sqrt(n / 2) 2^-23
     # with n = 2^10 or 2^12.
