@@ -97,3 +97,37 @@ def test_split_reductions_of_any_length(form, R):
         s = make(form, dtype, counts, N, K)[0]
         assert T.moe_grouped_matmul_workspace_bytes(s) > 0
         check(form, dtype, counts, N, K, spare=7)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,K", [(64, 128), (37, 53)])
+def test_values_below_the_normal_numbers(form, dtype, N, K):
+    # 2^-130 is subnormal in both types; none of it may be flushed
+    counts = [5, 70, 33]
+    s, lhs, rhs, out = make(form, dtype, counts, N, K, out="f32")
+    lhs.fill_(2.0 ** -130)
+    rhs.mul_(2.0 ** 110)
+    run(s, counts, lhs, rhs, out)
+    ref, mag, n = gmm_ref(form, counts, lhs, rhs)
+    assert ref.abs().max() > 0
+    assert not ((out.double() - ref).abs() > sum_bound(mag, n, ref, out.dtype)).any()
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,K", [(72, 136), (37, 53), (131, 267)])
+def test_an_infinity_stays_in_its_row_and_column(form, dtype, N, K):
+    # in a row's last element and a group's last row, next to the zeros that
+    # fill a chunk or a step
+    counts = [5, 70, 33]
+    s, lhs, rhs, out = make(form, dtype, counts, N, K)
+    lhs[74, -1] = float("inf")
+    run(s, counts, lhs, rhs, out)
+    if form == "dw":        # column N - 1 of lhs: row N - 1 of the group's W
+        bad = torch.zeros_like(out, dtype=torch.bool)
+        bad[1, -1] = True
+    else:
+        bad = torch.zeros_like(out, dtype=torch.bool)
+        bad[74] = True
+    assert torch.equal(~torch.isfinite(out), bad)
