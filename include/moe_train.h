@@ -180,7 +180,8 @@ typedef struct {
  * in fp32.  grad_scale (device, one fp32, or NULL for 1): a clipping factor
  * or an inverse loss scale computed on the device; when it is not finite
  * nothing changes but `skipped`.  lr_scale (device, one fp32, or NULL for
- * 1) multiplies lr, for a schedule under graph replay.
+ * 1) multiplies lr, for a schedule under graph replay; it is not checked, and
+ * one that is not finite reaches every parameter.
  * 8-bit states: elements 256 b .. 256 b + 255 share a scale, the block's
  * largest magnitude / 448; element i stands for code * scale, for v the
  * square of that.  The new value is rounded at random to one of the two

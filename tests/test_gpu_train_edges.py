@@ -185,3 +185,23 @@ def test_on_a_part_of_the_cus(cus):
                     assert torch.equal(a[k].view(torch.uint8), b[k].view(torch.uint8)), k
     finally:
         ms.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_saturated_gates(dtype):
+    # gate projections of up to some hundred either way, where exp(-z) is infinite
+    # or zero: silu and its slope go to z and 1, or to 0, and nothing is NaN.  The
+    # slope's sum 1 + z (1 - s) loses no more than |z| 2^-24 for the z of about 10
+    # that weigh in it: within TOL.
+    c = Case(dtype, 200, 128, 6, 2, 128, 3, 1.0, 0.5)
+    c.wg.mul_(100.0)
+    c.forward()
+    tb, ref = c.backward(), c.reference()
+    z = c.x.double() @ c.wg[0].double().t()
+    assert z.max() > 200 and z.min() < -200
+    for name, want in ref.items():
+        got = getattr(tb, name)
+        assert torch.isfinite(got).all(), name
+        err = far(got, want)
+        say(f"  {name} {err:.2e}")
+        assert err <= TOL[dtype], (name, err)
