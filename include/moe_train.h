@@ -48,7 +48,8 @@ typedef struct {
   int32_t out_dtype;  /* of the array that is written: dtype or MOE_F32    */
   int32_t accumulate; /* nonzero: add to what the written array holds      */
   int32_t n_groups;   /* experts                                           */
-  int32_t M;          /* rows that a and c have room for                   */
+  int32_t M;          /* rows that a and c have room for; the tiles go by
+                         it, so the rows in use where the host knows them  */
   int32_t N, K;       /* output and input width of the map                 */
   int64_t lda, ldc;   /* elements between rows of a and of c               */
 } moe_gmm_shape;
