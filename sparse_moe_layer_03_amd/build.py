@@ -24,7 +24,13 @@ ARCH = "gfx950"
 
 SOURCES = ["api.hip", "gemm.hip", "gemm_big.hip", "route.hip", "dispatch.hip", "combine.hip", "pid.hip",
            "noalloc.hip", "eplb.hip", "train_api.hip", "gmm_general.hip",
-           "gmm_mfma.hip", "layer_bwd.hip", "adamw.hip"]
+           "gmm_mfma.hip", "layer_bwd.hip", "adamw.hip", "block_api.hip", "select.hip", "norm.hip",
+           "quant.hip", "gmm_i8.hip", "i8_general.hip"]
+
+# Integer accumulators that leave the reduction's loop at several places are
+# taken apart into single registers by default, and copied at each of them
+# (256 x 256 tiles: 1500 spilled registers instead of a few).
+FILE_FLAGS = {"gmm_i8.hip": ["-mllvm", "-amdgpu-codegenprepare-break-large-phis=false"]}
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -50,7 +56,7 @@ SANITIZE_FLAGS = ["-O1", "-g", "-Xarch_host", "-fno-omit-frame-pointer",
 def _compile(src: str, obj_dir: str = OBJ, extra=()) -> str:
     obj = os.path.join(obj_dir, os.path.splitext(src)[0] + ".o")
     flags = [f for f in CFLAGS if not (any(x.startswith("-O") for x in extra) and f == "-O3")]
-    cmd = [HIPCC, *flags, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [HIPCC, *flags, *FILE_FLAGS.get(src, ()), *extra, "-c", os.path.join(CSRC, src), "-o", obj]
     p = subprocess.run(cmd, capture_output=True, text=True)
     if p.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{p.stdout}\n{p.stderr}")

@@ -9,6 +9,7 @@
 
 #include <algorithm>
 
+#include "block.h"
 #include "common.h"
 #include "internal.h"
 #include "plan.h"
@@ -156,6 +157,34 @@ static int router_big_tiles(const moe_shape* s) {
   return router_ksplit(s->T, E, s->d_model, s->dtype) == 1 && (long)(s->T / 128) * ((E + 127) / 128) >= 256;
 }
 
+// The router's product: its K-split partial logits, in the workspace.
+static int router_partials(const moe_shape* s, const void* x, const void* w_router, void* ws,
+                           float** partials, int* nsplit, hipStream_t st) {
+  const RouterPlan rp = router_plan(s);
+  *nsplit = rp.ksplit;
+  *partials = (float*)((char*)ws + ws_layout(s).logits);
+  GemmArgs g{};
+  g.a = x;
+  g.b0 = w_router;
+  g.c = *partials;
+  g.M = s->T;
+  g.N = s->n_ffn + s->n_zero;
+  g.K = s->d_model;
+  g.ngroups = 1;
+  g.top_k = s->top_k;
+  g.ksplit = rp.ksplit;
+  return rp.big ? launch_gemm_big(0, g, st) : launch_gemm(s->dtype, 0, router_big_tiles(s), g, st);
+}
+
+int run_router_logits(const moe_shape* s, const void* x, const void* w_router,
+                      const float* logit_bias, float* logits, void* ws, hipStream_t st) {
+  float* partials;
+  int nsplit;
+  const int rc = router_partials(s, x, w_router, ws, &partials, &nsplit, st);
+  if (rc) return rc;
+  return launch_logits(partials, nsplit, logit_bias, s->T, s->n_ffn + s->n_zero, logits, st);
+}
+
 int dispatch_checks(const moe_shape* s, const int32_t* topk_idx, const void* x,
                     int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv_perm,
                     void* x_perm) {
@@ -222,21 +251,9 @@ int moe_route(const moe_shape* s, const void* x, const void* w_router, const flo
     return launch_router_topk(x, w_router, (char*)ws + ws_layout(s).wrp, logit_bias, logits_out,
                               bias, s->T, E, s->d_model, s->top_k, s->routed_scaling, topk_idx,
                               topk_gate, st);
-  const RouterPlan rp = router_plan(s);
-  const int nsplit = rp.ksplit;
-  float* partials = (float*)((char*)ws + ws_layout(s).logits);
-  GemmArgs g{};
-  g.a = x;
-  g.b0 = w_router;
-  g.c = partials;
-  g.M = s->T;
-  g.N = E;
-  g.K = s->d_model;
-  g.ngroups = 1;
-  g.top_k = s->top_k;
-  g.ksplit = nsplit;
-  rc = rp.big ? launch_gemm_big(0, g, st) : launch_gemm(s->dtype, 0, router_big_tiles(s), g, st);
-  if (rc) return rc;
+  float* partials;
+  int nsplit;
+  if ((rc = router_partials(s, x, w_router, ws, &partials, &nsplit, st))) return rc;
   return launch_topk(partials, nsplit, logit_bias, logits_out, bias, s->T, E, s->top_k,
                      s->routed_scaling, topk_idx, topk_gate, st);
 }
@@ -393,7 +410,8 @@ int moe_debug_checks(uint32_t* flags, int clear) {
   }
   unsigned (*const words[])(bool) = {check_word_route, check_word_dispatch, check_word_gemm,
                                      check_word_gemm_big, check_word_combine, check_word_gmm_general,
-                                     check_word_gmm_mfma, check_word_layer_bwd};
+                                     check_word_gmm_mfma, check_word_layer_bwd, check_word_select,
+                                     check_word_quant, check_word_gmm_i8, check_word_i8_general};
   uint32_t v = 0;
   for (auto* fn : words) {
     const unsigned w = fn(clear != 0);

@@ -1,0 +1,103 @@
+// Internal host-side interface of the kernels behind moe_block.h.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/moe_block.h"
+#include "train.h"
+
+namespace moe {
+
+// ---- selection (select.hip)
+
+struct SelectArgs {
+  const float* logits;
+  int64_t ld;
+  const float* bias;  // may be null
+  int32_t* idx;
+  float* gate;
+  float scaling, eps;
+  int T, E, k;
+  int score, n_groups, top_groups, group_best, renorm;
+};
+int launch_select(const SelectArgs& a, hipStream_t st);
+
+// Sums the K-split partial logits in split order, adds col_bias (nullable).
+int launch_logits(const float* partials, int nsplit, const float* col_bias, int T, int E,
+                  float* logits, hipStream_t st);
+// The router's product (api.hip): logits [T, E], ws as moe_route's.
+int run_router_logits(const moe_shape* s, const void* x, const void* w_router,
+                      const float* logit_bias, float* logits, void* ws, hipStream_t st);
+
+// moe_layer_backward, with another selection rule where `select` is given
+// (train_api.hip).
+int run_layer_backward(const moe_shape* s, const moe_select_params* select,
+                       const moe_backward_io* io, void* ws, hipStream_t st);
+
+// The gradient at the logits; `dl` as in TokenArgs (ep elements a row, halves
+// of them), either of dlogits and dl may be null.
+struct SelectBwdArgs {
+  const float* logits;
+  int64_t ld;
+  const int32_t* idx;
+  const float* dgate;
+  float* dlogits;
+  void* dl;
+  float scaling, eps;
+  int T, E, k;
+  int score, renorm;
+  int ep, halves;
+  int32_t* route_offs;  // with dl: 0, T and the bounds of nsplit token ranges,
+  int32_t* split_offs;  // as in TokenArgs
+  int nsplit;
+};
+int launch_select_bwd(const SelectBwdArgs& a, hipStream_t st);
+
+// ---- 8-bit rows and products (quant.hip, gmm_i8.hip, i8_general.hip)
+
+// Quantises the rows of x; the rows' codes of a bf16 or fp32 array.
+int launch_quantize(int dtype, const void* x, int64_t ldx, int M, int K, int8_t* q, int64_t ldq,
+                    float* scale, const int32_t* m_used, hipStream_t st);
+
+// Codes and scales of the FFN rows, sorted by expert: for p < offsets[n_ffn],
+// row perm[p] / k.
+int launch_gather_i8(const int8_t* xq, const float* xs, const int32_t* perm, const int32_t* offsets,
+                     int n_ffn, int Tk, int k, int d, int8_t* rows, float* row_scale,
+                     hipStream_t st);
+
+// out[p, j] = (sum_r a[p, r] b_e[j, r]) sa[p] sb[e, j]; with b2, SwiGLU of the
+// products by b (gate) and b2 (up).
+struct I8Args {
+  const int8_t* a;
+  const float* sa;
+  const int8_t *b, *b2;
+  const float *sb, *sb2;
+  void* out;
+  const int32_t* offsets;  // may be null with one group
+  int64_t lda, ldo;
+  int ngroups, M, N, K;
+  int nsplit;              // ranges of the reduction, their sums in `part`
+  int32_t* part;           // [nsplit, M, N]
+};
+bool i8_mfma_ok(int N, int K, int64_t lda, int64_t ldo);
+int launch_i8_mfma(int out_dtype, const I8Args& g, hipStream_t st);
+int launch_i8_general(int out_dtype, const I8Args& g, hipStream_t st);
+int launch_i8_join(int out_dtype, const I8Args& g, hipStream_t st);
+
+// ---- norms (norm.hip)
+
+int launch_norm(const moe_norm_shape& s, const moe_norm_io& io, hipStream_t st);
+// Workgroups of the backward pass, and so rows of its partial sums.
+int norm_bwd_groups(int T, int d, int cus);
+size_t norm_bwd_ws_bytes(const moe_norm_shape& s, int cus);
+int launch_norm_bwd(const moe_norm_shape& s, const moe_norm_grad_io& io, void* ws, int cus,
+                    hipStream_t st);
+
+// as the accessors of internal.h
+unsigned check_word_select(bool clear);
+unsigned check_word_quant(bool clear);
+unsigned check_word_gmm_i8(bool clear);
+unsigned check_word_i8_general(bool clear);
+
+}  // namespace moe

@@ -1,0 +1,488 @@
+// Grouped products of 8-bit rows and weights on int8 MFMAs, for rows that are
+// multiples of 16 bytes: with the scales of rows and output channels applied
+// behind the reduction, or SwiGLU of the gate's and the up product.
+//
+// The 16x16x64 int8 MFMA takes 16 bytes a lane and operand and as many cycles as
+// the bf16 one over half the depth: a tile has the bytes of a bf16 tile and
+// twice its products, so geometry and pipeline are those of the bf16 products'
+// forward form (direct-to-LDS loads, swizzled slots, rings of stages with one
+// barrier a step, a persistent grid that works out the next tile and asks for
+// its first stages before this tile's stores).  Sums are whole numbers, exact
+// in 32 bits, and so do not depend on the split of a long reduction.
+
+#include <algorithm>
+#include <type_traits>
+
+#include "block.h"
+#include "common.h"
+#include "gmm_tile.h"
+
+namespace moe {
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+// silu(z) u; in 64 bits for an fp32 H.
+__device__ __forceinline__ float swiglu(float z, float u) {
+  return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504f)) * u;
+}
+__device__ __forceinline__ double swiglu(double z, double u) { return z / (1.0 + exp(-z)) * u; }
+
+// The rows of a group; all M where there are no offsets.
+__device__ __forceinline__ void i8_rows(const int32_t* offsets, int e, int M, int& lo, int& hi) {
+  if (offsets == nullptr) {
+    lo = 0;
+    hi = M;
+  } else {
+    rows_of_uniform(offsets, e, M, lo, hi);
+  }
+}
+
+// SW: with b2, the tile's first half of columns are gate's, the second up's.
+template <bool SW, typename TO, int BM, int BN, int WM, int WN, int SA, int SB>
+__global__ void __launch_bounds__(64 * WM * WN, 2)
+gmm_i8_kernel(I8Args g) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int NW = WM * WN, NT = 64 * NW, KS = 128;  // bytes a step
+  using TA = Tile<false, BM, NW, KS / 2>;
+  using TB = Tile<false, BN, NW, KS / 2>;
+  constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
+  constexpr int A_PW = TA::PW, B_PW = TB::PW, PW = A_PW + B_PW;
+  constexpr int HN = SW ? BN / 2 : BN;  // output columns per tile
+  constexpr int MG = 4;
+  constexpr int DA = SA - 1, DB = SB - 1;
+  static_assert(!SW || (NB % 2 == 0 && B_PW % 2 == 0), "tile");
+  static_assert(TB::BYTES > kMfmaMaxGroups * 4, "the groups' prefix fits a stage");
+  static_assert(DA >= 1 && DB >= DA && SB <= 5 && SA * TA::BYTES + SB * TB::BYTES <= 160 * 1024, "LDS");
+  __shared__ __attribute__((aligned(1024))) char s_a0[TA::BYTES];
+  __shared__ __attribute__((aligned(1024))) char s_a1[TA::BYTES];
+  __shared__ __attribute__((aligned(1024))) char s_a2[SA > 2 ? TA::BYTES : 16];
+  __shared__ __attribute__((aligned(1024))) char s_a3[SA > 3 ? TA::BYTES : 16];
+  __shared__ __attribute__((aligned(1024))) char s_a4[SA > 4 ? TA::BYTES : 16];
+  __shared__ __attribute__((aligned(1024))) char s_b0[TB::BYTES];
+  __shared__ __attribute__((aligned(1024))) char s_b1[TB::BYTES];
+  __shared__ __attribute__((aligned(1024))) char s_b2[SB > 2 ? TB::BYTES : 16];
+  __shared__ __attribute__((aligned(1024))) char s_b3[SB > 3 ? TB::BYTES : 16];
+  __shared__ __attribute__((aligned(1024))) char s_b4[SB > 4 ? TB::BYTES : 16];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = uni(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int l16 = lane & 15, l4 = lane >> 4;
+  // a wave's row blocks interleave with the other waves', so that a short tile
+  // loads all of them
+  const int a_lane = TA::lane_base(lane, wm);
+  const int b_lane = TB::lane_base(lane, SW ? wn * (NB / 2) : wn * NB);
+
+  const int G = gridDim.x, bid = blockIdx.x;
+  const int jt = (g.N + HN - 1) / HN;
+  // tiles that run together on an XCD are neighbours
+  const int vid = G % 8 == 0 ? (bid % 8) * (G / 8) + bid / 8 : bid;
+
+  // (first row tile << 10 | group) of this workgroup's next 64 tiles, one per
+  // lane, and the number of tiles
+  uint32_t desc = 0;
+  long tiles = 0;
+  auto describe = [&](int k0) {
+    int* s_pref = reinterpret_cast<int*>(s_b0);
+    int* s_scan = reinterpret_cast<int*>(s_b1);
+    constexpr int PER = (kMfmaMaxGroups + NT - 1) / NT;
+    // ascending offsets give at most this many row tiles; more are cut off
+    // here and computed nowhere
+    const int most = g.M / BM + g.ngroups;
+    int loc[PER], run = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int e = tid * PER + k;
+      if (e < g.ngroups) {
+        int lo = 0, hi = g.M;
+        if (g.offsets != nullptr) rows_of(g.offsets, e, g.M, lo, hi);
+        run = min(run + (hi - lo + BM - 1) / BM, most + 1);
+      }
+      loc[k] = run;
+    }
+    const int base = block_inclusive_scan<NT>(run, s_scan) - run;
+    if (tid == 0) s_pref[0] = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+      if (tid * PER + k < g.ngroups) s_pref[tid * PER + k + 1] = base + loc[k];
+    __syncthreads();
+    const int row_tiles = uni(s_pref[g.ngroups]);
+    tiles = row_tiles <= most ? (long)row_tiles * jt : 0;
+    const long t = (vid + (long)(k0 + lane) * G) / g.nsplit;
+    desc = 0;
+    if (t < tiles) {
+      const int m = (int)(t / jt);
+      int lo = 0, hi = g.ngroups - 1;  // last group with s_pref <= m
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_pref[mid] <= m) lo = mid; else hi = mid - 1;
+      }
+      desc = ((uint32_t)s_pref[lo] << 10) | (uint32_t)lo;
+    }
+    __syncthreads();
+  };
+
+  // ---- one tile's place, the same in all lanes
+  struct Place {
+    int e, i0, i_end, j0, split, rows, row0;
+    int k_lo, k_hi, r_end;  // its steps, and the end of its reduction
+    const char *a_base, *b_base, *b_base2;
+    uint32_t a_bytes, b_bytes;
+    bool once;              // no other tile reads this tile's part of b
+  };
+  const uint32_t lda = (uint32_t)g.lda, ldb = (uint32_t)g.K;
+  // lane offsets of the first load instructions of each kind
+  uint32_t a_off[TA::NP], b_off[TB::NP];
+#pragma unroll
+  for (int q = 0; q < TA::NP; ++q)
+    a_off[q] = (uint32_t)TA::row(q, wave, lane) * lda + TA::chunk(q, wave, lane) * 16;
+#pragma unroll
+  for (int q = 0; q < TB::NP; ++q)
+    b_off[q] = (uint32_t)TB::row(q, wave, lane) * ldb + TB::chunk(q, wave, lane) * 16;
+
+  // Tile number k of this workgroup; false behind the last one.
+  auto setup = [&](int k, Place& t) -> bool {
+    const long item = vid + (long)k * G;
+    if (item >= tiles * g.nsplit) return false;
+    long n = item;
+    t.split = 0;
+    if (g.nsplit > 1) {
+      n = item / g.nsplit;
+      t.split = (int)(item - n * g.nsplit);
+    }
+    const uint32_t d = (uint32_t)__builtin_amdgcn_readlane((int)desc, k & 63);
+    t.e = uni((int)(d & 1023u));
+    int lo, hi;
+    i8_rows(g.offsets, t.e, g.M, lo, hi);
+    t.row0 = uni(lo);
+    t.rows = uni(hi - lo);
+    // in a group: bands of MG row tiles, column by column, so that tiles that
+    // run together share row and weight slices in L2
+    const int mt = (t.rows + BM - 1) / BM;
+    const int local = (int)(n - (long)(d >> 10) * jt);
+    const int m0 = (local / (MG * jt)) * MG;
+    const int mg = max(1, min(MG, mt - m0));
+    const int in = local - m0 * jt;
+    t.j0 = uni((in / mg) * HN);
+    const int h = ((t.rows + mt - 1) / mt + 15) & ~15;  // balanced height
+    t.i0 = uni((m0 + in % mg) * h);
+    t.once = mt == 1;
+    t.i_end = uni(min(t.rows, t.i0 + h));
+    t.split = uni(t.split);
+    const int steps = (g.K + KS - 1) / KS;
+    const int per = g.nsplit > 1 ? (steps + g.nsplit - 1) / g.nsplit : steps;
+    t.k_lo = min(t.split * per, steps), t.k_hi = min(steps, t.k_lo + per);
+    t.r_end = min(g.K, t.k_hi * KS);
+    t.a_base = uni((const char*)g.a + (t.row0 + t.i0) * (int64_t)lda);
+    t.a_bytes = t.i_end > t.i0 ? (uint32_t)(t.i_end - t.i0 - 1) * lda + (uint32_t)g.K : 0u;
+    const int64_t at = ((int64_t)t.e * g.N + t.j0) * ldb;
+    t.b_base = uni((const char*)g.b + at);
+    t.b_base2 = SW ? uni((const char*)g.b2 + at) : nullptr;
+    t.b_bytes = (uint32_t)min(HN, g.N - t.j0) * ldb;
+    return true;
+  };
+
+  auto stage_a = [&](auto sc) -> char* {
+    constexpr int N = decltype(sc)::value % SA;
+    return N == 0 ? s_a0 : N == 1 ? s_a1 : N == 2 ? s_a2 : N == 3 ? s_a3 : s_a4;
+  };
+  auto stage_b = [&](auto sc) -> char* {
+    constexpr int N = decltype(sc)::value % SB;
+    return N == 0 ? s_b0 : N == 1 ? s_b1 : N == 2 ? s_b2 : N == 3 ? s_b3 : s_b4;
+  };
+  // Load instruction q of step ks into a stage.  What its wave-uniform part
+  // adds to the lane offset goes through the scalar offset.
+  auto load_a = [&](const Place& t, auto sc, int ks, int q) {
+    char* dst = stage_a(sc) + (wave + q * NW) * 1024;
+    const int add = (int)((uint32_t)(q - q % TA::NP) * (NW * TA::RPI) * lda);
+    const auto rs = descriptor(t.a_base, t.a_bytes);
+    const int left = t.r_end - ks * KS;
+    uint32_t off = a_off[q % TA::NP];
+    if (left < KS) off = TA::chunk(q, wave, lane) * 16 < left ? off : kOutside;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)off, ks * KS + add, 0, 0);
+  };
+  auto load_b1 = [&](const Place& t, auto sc, int ks, int q, auto cache) {
+    constexpr int AUX = decltype(cache)::value;
+    char* dst = stage_b(sc) + (wave + q * NW) * 1024;
+    // SwiGLU: gate rows fill the first half of the tile, up rows the second
+    const bool second = SW && q >= B_PW / 2;
+    const int h = second ? q - B_PW / 2 : q;
+    const int add = (int)((uint32_t)(h - h % TB::NP) * (NW * TB::RPI) * ldb);
+    const auto rs = descriptor(second ? t.b_base2 : t.b_base, t.b_bytes);
+    const int left = t.r_end - ks * KS;
+    uint32_t off = b_off[h % TB::NP];
+    if (left < KS) off = TB::chunk(q, wave, lane) * 16 < left ? off : kOutside;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)off, ks * KS + add, 0, AUX);
+  };
+  // The step's b loads; weights that one tile reads are loaded non-temporally.
+  auto load_b = [&](const Place& t, auto sc, int ks) {
+    if (t.once) {
+#pragma unroll
+      for (int q = 0; q < B_PW; ++q) load_b1(t, sc, ks, q, std::integral_constant<int, kCpolNT>{});
+    } else {
+#pragma unroll
+      for (int q = 0; q < B_PW; ++q) load_b1(t, sc, ks, q, std::integral_constant<int, 0>{});
+    }
+  };
+
+  constexpr int UNROLL = SA == SB ? SA : SA * SB;
+  // A tile's first DA and DB steps, in the order in which the loop would
+  // have asked for them.
+  auto prologue = [&](const Place& t) {
+    auto one = [&](auto vc) {  // what step V of -DB .. -1 would load
+      constexpr int V = decltype(vc)::value - DB;
+      if constexpr (V + DA >= 0) {
+        if (t.k_lo + V + DA < t.k_hi) {
+#pragma unroll
+          for (int q = 0; q < A_PW; ++q)
+            load_a(t, std::integral_constant<int, V + DA>{}, t.k_lo + V + DA, q);
+        }
+      }
+      if (t.k_lo + V + DB < t.k_hi)
+        load_b(t, std::integral_constant<int, V + DB>{}, t.k_lo + V + DB);
+    };
+    one(std::integral_constant<int, 0>{});
+    if constexpr (DB > 1) one(std::integral_constant<int, 1>{});
+    if constexpr (DB > 2) one(std::integral_constant<int, 2>{});
+    if constexpr (DB > 3) one(std::integral_constant<int, 3>{});
+  };
+  // Loads issued after the last one that a step with `behind` steps behind it
+  // needs.
+  auto later = [](int behind) constexpr {
+    const int na = behind < DA - 1 ? behind : DA - 1;
+    const int lo = DB == DA ? 1 : DB - DA, hi = behind < DB - 1 ? behind : DB - 1;
+    return na * A_PW + (hi >= lo ? hi - lo + 1 : 0) * B_PW;
+  };
+
+  describe(0);
+  Place t, next;
+  if (!setup(0, t)) return;
+  prologue(t);
+  for (int k = 0;; ++k) {
+    // the next tile's place, while this one's first loads are under way
+    const bool early = ((k + 1) & 63) != 0;  // else it is not known yet
+    bool have = early && setup(k + 1, next);
+    i32x4_t acc[MB][NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+
+    // Step ks, at place N of the unrolled loop, with MBA active row blocks.
+    auto step = [&](auto mbac, auto nc, int ks) {
+      constexpr int MBA = decltype(mbac)::value, N = decltype(nc)::value;
+      const char* sa = stage_a(nc);
+      const char* sb = stage_b(nc);
+      const int behind = t.k_hi - 1 - ks;
+      if (DB == 1 || behind >= DB - 1) wait_vm<later(DB - 1)>();
+      else if (DB > 3 && behind == 2) wait_vm<later(DB > 3 ? 2 : 0)>();
+      else if (DB > 2 && behind == 1) wait_vm<later(DB > 2 ? 1 : 0)>();
+      else wait_vm<later(0)>();
+      barrier_all();
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        i32x4_t fa[MBA], fb[NB];
+#pragma unroll
+        for (int i = 0; i < MBA; ++i)
+          fa[i] = __builtin_bit_cast(i32x4_t, TA::frag(sa, a_lane, i * WM, kk));
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+          fb[j] = __builtin_bit_cast(
+              i32x4_t, TB::frag(sb, b_lane, SW && j >= NB / 2 ? BN / 32 + j - NB / 2 : j, kk));
+        // into the stages that every wave has left at this step's barrier
+        if (kk == 0 && behind >= DA) {
+#pragma unroll
+          for (int q = 0; q < A_PW; ++q) load_a(t, std::integral_constant<int, N + DA>{}, ks + DA, q);
+        }
+        if (kk == 1 && behind >= DB) load_b(t, std::integral_constant<int, N + DB>{}, ks + DB);
+#pragma unroll
+        for (int i = 0; i < MBA; ++i)
+#pragma unroll
+          for (int j = 0; j < NB; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      __builtin_amdgcn_s_setprio(0);
+    };
+
+    auto loop = [&](auto mbac) {
+      for (int ks = t.k_lo; ks < t.k_hi; ks += UNROLL) {
+        step(mbac, std::integral_constant<int, 0>{}, ks);
+        if (ks + 1 >= t.k_hi) break;
+        step(mbac, std::integral_constant<int, 1>{}, ks + 1);
+        if constexpr (UNROLL > 2) {
+          if (ks + 2 >= t.k_hi) break;
+          step(mbac, std::integral_constant<int, 2>{}, ks + 2);
+        }
+        if constexpr (UNROLL > 3) {
+          if (ks + 3 >= t.k_hi) break;
+          step(mbac, std::integral_constant<int, 3>{}, ks + 3);
+        }
+        if constexpr (UNROLL > 4) {
+          if (ks + 4 >= t.k_hi) break;
+          step(mbac, std::integral_constant<int, 4>{}, ks + 4);
+        }
+        if constexpr (UNROLL > 5) {
+          if (ks + 5 >= t.k_hi) break;
+          step(mbac, std::integral_constant<int, 5>{}, ks + 5);
+        }
+      }
+    };
+    if constexpr (MB == 1) {
+      loop(std::integral_constant<int, MB>{});
+    } else {
+      // row blocks of this wave that hold rows (a wave without any still
+      // loads and waits with the others, on one block that is not stored)
+      const int nrb = (t.i_end - t.i0 + 15) / 16;
+      const int mba = min(MB, (nrb - wm + WM - 1) / WM);
+      if (mba >= 4 && MB >= 4) loop(std::integral_constant<int, MB >= 4 ? 4 : MB>{});
+      else if (mba == 3 && MB >= 3) loop(std::integral_constant<int, MB >= 3 ? 3 : MB>{});
+      else if (mba == 2) loop(std::integral_constant<int, 2>{});
+      else loop(std::integral_constant<int, 1>{});
+    }
+
+    // ---- out.  b was the MFMA's row operand: lane (l16, l4) holds columns
+    // 4 l4 .. 4 l4 + 3 of row l16 of a 16 x 16 block.
+    const int J = g.N;
+    const int jw = t.j0 + wn * (SW ? NB / 2 : NB) * 16;  // the wave's first column
+    const int high = max(0, t.i_end - t.i0);             // rows of the tile
+    // The scales, before the next tile's loads: a load waits for older ones only.
+    constexpr int NC = SW ? NB / 2 : NB;
+    float sa[MB];
+    f32x4_t sb[NC], sb2[SW ? NC : 1];
+    if (g.nsplit == 1) {
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+        sa[i] = g.sa[t.row0 + min(t.i0 + (i * WM + wm) * 16 + l16, t.rows - 1)];
+      const float* col = g.sb + (int64_t)t.e * J;
+      const float* col2 = SW ? g.sb2 + (int64_t)t.e * J : nullptr;
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const int jj = jw + j * 16 + l4 * 4;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          sb[j][v] = col[min(jj + v, J - 1)];
+          if constexpr (SW) sb2[j][v] = col2[min(jj + v, J - 1)];
+        }
+      }
+    }
+    // the next tile's first loads, before this one's stores: every wave is done
+    // with the stages, and no load of theirs is outstanding
+    if (early) {
+      barrier_all();
+      if (have) prologue(next);
+    }
+    // Stores go through a descriptor that ends with the tile's last row; columns
+    // behind the last one are sent outside it.
+    if (g.nsplit > 1) {
+      const auto ro = descriptor(
+          (const char*)(g.part + ((int64_t)t.split * g.M + t.row0 + t.i0) * J), (uint32_t)high * J * 4);
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const int jj = jw + j * 16 + l4 * 4;
+          const uint32_t off = (uint32_t)((wm + i * WM) * 16 + l16) * J * 4 + jj * 4;
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[i][j]), ro,
+                                                 jj < J ? off : kOutside, 0, 0);
+        }
+    } else {
+      const auto ro = descriptor(
+          uni((const char*)g.out + (int64_t)(t.row0 + t.i0) * g.ldo * (int64_t)sizeof(TO)),
+          high > 0 ? ((uint32_t)(high - 1) * (uint32_t)g.ldo + J) * (uint32_t)sizeof(TO) : 0u);
+      const uint32_t ldo_b = (uint32_t)g.ldo * (uint32_t)sizeof(TO);
+      const bool wide = ((J | (int)g.ldo) & 7) == 0;
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        const uint32_t row = (uint32_t)((wm + i * WM) * 16 + l16) * ldo_b;
+        auto at = [&](int jj) { return jj < J ? row + (uint32_t)jj * (uint32_t)sizeof(TO) : kOutside; };
+        f32x4_t o[NC];
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            if constexpr (!SW) {
+              o[j][v] = (float)acc[i][j][v] * sa[i] * sb[j][v];
+            } else if constexpr (sizeof(TO) == 4) {
+              o[j][v] = (float)swiglu((double)acc[i][j][v] * (double)sa[i] * (double)sb[j][v],
+                                      (double)acc[i][j + NC][v] * (double)sa[i] * (double)sb2[j][v]);
+            } else {
+              o[j][v] = swiglu((float)acc[i][j][v] * sa[i] * sb[j][v],
+                               (float)acc[i][j + NC][v] * sa[i] * sb2[j][v]);
+            }
+          }
+        if constexpr (sizeof(TO) == 4) {
+#pragma unroll
+          for (int j = 0; j < NC; ++j)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, o[j]), ro,
+                                                   at(jw + j * 16 + l4 * 4), 0, 0);
+        } else if (NC % 2 == 0 && wide) {  // whole 16-byte pieces
+#pragma unroll
+          for (int j = 0; j + 1 < NC; j += 2)
+            __builtin_amdgcn_raw_buffer_store_b128(bf16x8(o[j], o[j + 1]), ro,
+                                                   at(jw + j * 16 + bf16_col(l4)), 0, 0);
+        } else {
+#pragma unroll
+          for (int j = 0; j < NC; ++j)
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, bf16x4(o[j])), ro,
+                                                  at(jw + j * 16 + l4 * 4), 0, 0);
+        }
+      }
+    }
+    if (!early) {
+      // the next 64 tiles' places are worked out in the stages
+      wait_vm<0>();
+      __syncthreads();
+      describe(k + 1);
+      have = setup(k + 1, next);
+      if (have) prologue(next);
+    }
+    if (!have) break;
+    t = next;
+  }
+#endif
+}
+
+MOE_CHECK_ACCESSOR(check_word_gmm_i8)
+
+bool i8_mfma_ok(int N, int K, int64_t lda, int64_t ldo) {
+  // 16-byte rows; a lane stores 4 neighbouring columns; a descriptor spans at
+  // most 256 rows
+  return K % 16 == 0 && lda % 16 == 0 && lda <= (1 << 20) && N % 4 == 0 && ldo % 4 == 0 && ldo <= (1 << 20);
+}
+
+template <bool SW, typename TO, int BM, int BN, int WM, int WN, int SA, int SB>
+static int launch_tile(const I8Args& g, hipStream_t st) {
+  const int cus = stream_cu_count(st);
+  if (cus <= 0) return MOE_EHIP;
+  constexpr int HN = SW ? BN / 2 : BN;
+  const long most = (long)(g.M / BM + std::min(g.M, g.ngroups)) * ((g.N + HN - 1) / HN) * g.nsplit;
+  constexpr int LDS = (BM * SA + BN * SB) * 128;
+  long grid = (long)cus * std::min(2, 160 * 1024 / LDS);
+  if (grid > most) grid = most;
+  if (grid > 8) grid -= grid % 8;
+  if (grid < 1) return MOE_OK;
+  hipLaunchKernelGGL((gmm_i8_kernel<SW, TO, BM, BN, WM, WN, SA, SB>), dim3((unsigned)grid),
+                     dim3(64 * WM * WN), 0, st, g);
+  return check_launch();
+}
+
+template <bool SW, typename TO>
+static int launch_any(const I8Args& g, hipStream_t st) {
+  const int cus = stream_cu_count(st);
+  if (cus <= 0) return MOE_EHIP;
+  const long per = g.M / g.ngroups;
+  const long t256 = (long)(g.M / 256 + std::min(g.M, g.ngroups)) * ((g.N + (SW ? 127 : 255)) / (SW ? 128 : 256)) * g.nsplit;
+  if (per >= 128 && t256 >= cus) return launch_tile<SW, TO, 256, 256, 4, 2, 2, 3>(g, st);
+  if (per < 64) return launch_tile<SW, TO, 64, 128, 1, 4, 3, 3>(g, st);
+  return launch_tile<SW, TO, 128, 128, 2, 2, 2, 3>(g, st);
+}
+
+int launch_i8_mfma(int out_dtype, const I8Args& g, hipStream_t st) {
+  const bool f32 = out_dtype == MOE_F32;
+  if (g.b2 != nullptr) return f32 ? launch_any<true, float>(g, st) : launch_any<true, __bf16>(g, st);
+  return f32 ? launch_any<false, float>(g, st) : launch_any<false, __bf16>(g, st);
+}
+
+}  // namespace moe

@@ -7,6 +7,7 @@
 
 #include <algorithm>
 
+#include "block.h"
 #include "common.h"
 #include "train.h"
 
@@ -150,6 +151,159 @@ static int check_backward(const moe_shape* s, const moe_backward_io* io) {
   return MOE_OK;
 }
 
+int run_layer_backward(const moe_shape* s, const moe_select_params* select,
+                       const moe_backward_io* io, void* ws, hipStream_t st) {
+  int rc = check_backward(s, io);
+  if (rc) return rc;
+  if (!ws) return MOE_EINVAL;
+  if (!al16(ws)) return MOE_EALIGN;
+  const BwdLayout w = bwd_layout(s);
+  char* base = (char*)ws;
+  const int E = s->n_ffn + s->n_zero, Tk = s->T * s->top_k;
+  const int d = s->d_model, f = s->d_ff, dt = s->dtype, es = elem_size(dt);
+  char *xp = base + w.xp, *dyp = base + w.dyp, *dzu = base + w.dzu, *hs = base + w.hs;
+  float *zu = (float*)(base + w.zu), *dh = (float*)(base + w.dh), *part = (float*)(base + w.part);
+  float *dxr = (float*)(base + w.dxr), *drp = (float*)(base + w.drp);
+  char* dl = base + w.dl;
+  int32_t *route_offs = (int32_t*)(base + w.offs), *split_offs = route_offs + 2;
+
+  float* gates = (float*)(base + w.gates);
+  const int acc = io->accumulate != 0;
+  if ((rc = launch_gather2(dt, io->x, io->dy, io->topk_gate, io->perm, io->offsets, s->n_ffn, Tk,
+                           s->top_k, d, xp, dyp, gates, st)))
+    return rc;
+
+  GmmArgs g{};
+  g.offsets = io->offsets;
+  g.ngroups = s->n_ffn;
+  g.M = Tk;
+  g.nsplit = 1;
+  g.b_group = g.out_group = (int64_t)d * f;
+  // the gradient at H, before the gate
+  g.nsub = 1;
+  g.s[0] = {dyp, io->w_down, dh, d, f, f, 0, f};
+  g.R = g.RB = d;
+  if ((rc = run_gmm(MOE_GMM_DX, dt, MOE_F32, g, st))) return rc;
+  // z and u again, and SwiGLU's step (in bf16 behind the products' K loop)
+  if (dt == MOE_BF16) {
+    g.s[0] = {xp, io->w_gate, nullptr, d, d, 0, 0, f};
+    g.b2 = io->w_up;
+    g.gate = gates;
+    g.dh = dh;
+    g.dzu = dzu;
+    g.hs = hs;
+    g.dpart = part;
+    if ((rc = launch_swiglu_mfma(g, st))) return rc;
+  } else {
+    g.nsub = 2;
+    g.s[0] = {xp, io->w_gate, zu, d, d, 2 * f, 0, f};
+    g.s[1] = {xp, io->w_up, zu + f, d, d, 2 * f, 0, f};
+    if ((rc = run_gmm(MOE_GMM_FWD, dt, MOE_F32, g, st))) return rc;
+    if ((rc = launch_swiglu_bwd(zu, dh, gates, io->offsets, s->n_ffn, Tk, f, (float*)dzu,
+                                (float*)hs, part, st)))
+      return rc;
+  }
+  // gradients of the experts' weights
+  g.nsub = 3;
+  g.s[0] = {dzu, xp, io->dw_gate, 2 * f, d, d, f, d};
+  g.s[1] = {dzu + (size_t)f * es, xp, io->dw_up, 2 * f, d, d, f, d};
+  g.s[2] = {dyp, hs, io->dw_down, d, f, f, d, f};
+  g.accumulate = acc;
+  if ((rc = run_gmm(MOE_GMM_DW, dt, dt, g, st))) return rc;
+  // gradients of the rows, one reduction over gate's and up's columns, in fp32
+  // (a bf16 rounding of each row would be a third of dx's error) over x's and
+  // dy's rows, which are not needed any more
+  float* dx_rows = (float*)xp;
+  g.nsub = 1;
+  g.s[0] = {dzu, io->w_gate, dx_rows, 2 * f, d, d, 0, d};
+  g.b2 = io->w_up;
+  g.R = 2 * f;
+  g.RB = g.r_switch = f;
+  g.accumulate = 0;
+  if ((rc = run_gmm(MOE_GMM_DX, dt, MOE_F32, g, st))) return rc;
+
+  // gradients at the gates and logits, and the router's products
+  TokenArgs a{};
+  a.x = io->x;
+  a.dy = io->dy;
+  // (another selection rule than moe_route's: its own kernel takes dgate on)
+  a.logits = select ? nullptr : io->logits;
+  a.idx = io->topk_idx;
+  a.inv_perm = io->inv_perm;
+  a.part = part;
+  a.dgate = io->dgate;
+  a.dlogits = io->dlogits;
+  a.dl = dl;
+  a.route_offs = route_offs;
+  a.split_offs = split_offs;
+  a.scaling = s->routed_scaling;
+  a.T = s->T;
+  a.d = d;
+  a.E = E;
+  a.k = s->top_k;
+  a.n_ffn = s->n_ffn;
+  a.parts = w.parts;
+  a.ep = w.ep;
+  a.nsplit = w.nsplit;
+  if ((rc = launch_token_bwd(dt, a, st))) return rc;
+  if (select) {
+    SelectBwdArgs b{};
+    b.logits = io->logits;
+    b.ld = E;
+    b.idx = io->topk_idx;
+    b.dgate = io->dgate;
+    b.dlogits = io->dlogits;
+    b.dl = dl;
+    b.scaling = s->routed_scaling;
+    b.eps = select->renorm_eps;
+    b.T = s->T;
+    b.E = E;
+    b.k = s->top_k;
+    b.score = select->score;
+    b.renorm = select->renorm != 0;
+    b.ep = w.ep;
+    b.halves = w.halves;
+    b.route_offs = route_offs;
+    b.split_offs = split_offs;
+    b.nsplit = w.nsplit;
+    if ((rc = launch_select_bwd(b, st))) return rc;
+  }
+  if (io->logits) {
+    GmmArgs r{};
+    r.nsub = 1;
+    r.M = s->T;
+    r.nsplit = 1;
+    // dlogits W_router, fp32 (dlogits' rows have zeros behind E, where
+    // w_router has none)
+    const int wide = w.ep * w.halves;
+    r.s[0] = {dl, io->w_router, dxr, wide, d, d, 0, d};
+    r.offsets = route_offs;
+    r.ngroups = 1;
+    r.R = wide;
+    r.RB = E;
+    r.b2 = io->w_router;
+    r.r_switch = w.halves == 2 ? w.ep : 0;
+    if ((rc = run_gmm(MOE_GMM_DX, dt, MOE_F32, r, st))) return rc;
+    // dlogits^T x over ranges of the tokens, both parts, then their sum
+    r.s[0] = {dl, io->x, drp, wide, d, d, wide, d};
+    r.out_group = (int64_t)wide * d;
+    r.offsets = split_offs;
+    r.ngroups = w.nsplit;
+    if ((rc = run_gmm(MOE_GMM_DW, dt, MOE_F32, r, st))) return rc;
+    r.part = drp;
+    r.part_stride = (int64_t)w.ep * d;
+    r.nsplit = w.nsplit * w.halves;
+    r.ngroups = 1;
+    r.s[0].out = io->dw_router;
+    r.s[0].I = E;
+    r.accumulate = acc;
+    rc = launch_gmm_join(MOE_GMM_DW, dt, r, st);
+    if (rc) return rc;
+  }
+  return launch_dx(dt, dx_rows, io->dy, io->logits ? dxr : nullptr, io->topk_idx, io->topk_gate,
+                   io->inv_perm, s->T, d, s->top_k, s->n_ffn, io->dx, st);
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -221,133 +375,7 @@ size_t moe_layer_backward_workspace_bytes(const moe_shape* s) {
 }
 
 int moe_layer_backward(const moe_shape* s, const moe_backward_io* io, void* ws, void* stream) {
-  int rc = check_backward(s, io);
-  if (rc) return rc;
-  if (!ws) return MOE_EINVAL;
-  if (!al16(ws)) return MOE_EALIGN;
-  hipStream_t st = (hipStream_t)stream;
-  const BwdLayout w = bwd_layout(s);
-  char* base = (char*)ws;
-  const int E = s->n_ffn + s->n_zero, Tk = s->T * s->top_k;
-  const int d = s->d_model, f = s->d_ff, dt = s->dtype, es = elem_size(dt);
-  char *xp = base + w.xp, *dyp = base + w.dyp, *dzu = base + w.dzu, *hs = base + w.hs;
-  float *zu = (float*)(base + w.zu), *dh = (float*)(base + w.dh), *part = (float*)(base + w.part);
-  float *dxr = (float*)(base + w.dxr), *drp = (float*)(base + w.drp);
-  char* dl = base + w.dl;
-  int32_t *route_offs = (int32_t*)(base + w.offs), *split_offs = route_offs + 2;
-
-  float* gates = (float*)(base + w.gates);
-  const int acc = io->accumulate != 0;
-  if ((rc = launch_gather2(dt, io->x, io->dy, io->topk_gate, io->perm, io->offsets, s->n_ffn, Tk,
-                           s->top_k, d, xp, dyp, gates, st)))
-    return rc;
-
-  GmmArgs g{};
-  g.offsets = io->offsets;
-  g.ngroups = s->n_ffn;
-  g.M = Tk;
-  g.nsplit = 1;
-  g.b_group = g.out_group = (int64_t)d * f;
-  // the gradient at H, before the gate
-  g.nsub = 1;
-  g.s[0] = {dyp, io->w_down, dh, d, f, f, 0, f};
-  g.R = g.RB = d;
-  if ((rc = run_gmm(MOE_GMM_DX, dt, MOE_F32, g, st))) return rc;
-  // z and u again, and SwiGLU's step (in bf16 behind the products' K loop)
-  if (dt == MOE_BF16) {
-    g.s[0] = {xp, io->w_gate, nullptr, d, d, 0, 0, f};
-    g.b2 = io->w_up;
-    g.gate = gates;
-    g.dh = dh;
-    g.dzu = dzu;
-    g.hs = hs;
-    g.dpart = part;
-    if ((rc = launch_swiglu_mfma(g, st))) return rc;
-  } else {
-    g.nsub = 2;
-    g.s[0] = {xp, io->w_gate, zu, d, d, 2 * f, 0, f};
-    g.s[1] = {xp, io->w_up, zu + f, d, d, 2 * f, 0, f};
-    if ((rc = run_gmm(MOE_GMM_FWD, dt, MOE_F32, g, st))) return rc;
-    if ((rc = launch_swiglu_bwd(zu, dh, gates, io->offsets, s->n_ffn, Tk, f, (float*)dzu,
-                                (float*)hs, part, st)))
-      return rc;
-  }
-  // gradients of the experts' weights
-  g.nsub = 3;
-  g.s[0] = {dzu, xp, io->dw_gate, 2 * f, d, d, f, d};
-  g.s[1] = {dzu + (size_t)f * es, xp, io->dw_up, 2 * f, d, d, f, d};
-  g.s[2] = {dyp, hs, io->dw_down, d, f, f, d, f};
-  g.accumulate = acc;
-  if ((rc = run_gmm(MOE_GMM_DW, dt, dt, g, st))) return rc;
-  // gradients of the rows, one reduction over gate's and up's columns, in fp32
-  // (a bf16 rounding of each row would be a third of dx's error) over x's and
-  // dy's rows, which are not needed any more
-  float* dx_rows = (float*)xp;
-  g.nsub = 1;
-  g.s[0] = {dzu, io->w_gate, dx_rows, 2 * f, d, d, 0, d};
-  g.b2 = io->w_up;
-  g.R = 2 * f;
-  g.RB = g.r_switch = f;
-  g.accumulate = 0;
-  if ((rc = run_gmm(MOE_GMM_DX, dt, MOE_F32, g, st))) return rc;
-
-  // gradients at the gates and logits, and the router's products
-  TokenArgs a{};
-  a.x = io->x;
-  a.dy = io->dy;
-  a.logits = io->logits;
-  a.idx = io->topk_idx;
-  a.inv_perm = io->inv_perm;
-  a.part = part;
-  a.dgate = io->dgate;
-  a.dlogits = io->dlogits;
-  a.dl = dl;
-  a.route_offs = route_offs;
-  a.split_offs = split_offs;
-  a.scaling = s->routed_scaling;
-  a.T = s->T;
-  a.d = d;
-  a.E = E;
-  a.k = s->top_k;
-  a.n_ffn = s->n_ffn;
-  a.parts = w.parts;
-  a.ep = w.ep;
-  a.nsplit = w.nsplit;
-  if ((rc = launch_token_bwd(dt, a, st))) return rc;
-  if (io->logits) {
-    GmmArgs r{};
-    r.nsub = 1;
-    r.M = s->T;
-    r.nsplit = 1;
-    // dlogits W_router, fp32 (dlogits' rows have zeros behind E, where
-    // w_router has none)
-    const int wide = w.ep * w.halves;
-    r.s[0] = {dl, io->w_router, dxr, wide, d, d, 0, d};
-    r.offsets = route_offs;
-    r.ngroups = 1;
-    r.R = wide;
-    r.RB = E;
-    r.b2 = io->w_router;
-    r.r_switch = w.halves == 2 ? w.ep : 0;
-    if ((rc = run_gmm(MOE_GMM_DX, dt, MOE_F32, r, st))) return rc;
-    // dlogits^T x over ranges of the tokens, both parts, then their sum
-    r.s[0] = {dl, io->x, drp, wide, d, d, wide, d};
-    r.out_group = (int64_t)wide * d;
-    r.offsets = split_offs;
-    r.ngroups = w.nsplit;
-    if ((rc = run_gmm(MOE_GMM_DW, dt, MOE_F32, r, st))) return rc;
-    r.part = drp;
-    r.part_stride = (int64_t)w.ep * d;
-    r.nsplit = w.nsplit * w.halves;
-    r.ngroups = 1;
-    r.s[0].out = io->dw_router;
-    r.s[0].I = E;
-    r.accumulate = acc;
-    rc = launch_gmm_join(MOE_GMM_DW, dt, r, st);
-    if (rc) return rc;
-  }
-  return launch_dx(dt, dx_rows, io->dy, io->logits ? dxr : nullptr, io->topk_idx, io->topk_gate,
-                   io->inv_perm, s->T, d, s->top_k, s->n_ffn, io->dx, st);
+  return run_layer_backward(s, nullptr, io, ws, (hipStream_t)stream);
 }
 
 int moe_adamw(const moe_adamw_params* hp, const moe_adamw_tensor* tensors, int32_t n_tensors,

@@ -1,0 +1,292 @@
+"""Host-side checks of the operators around the layer: the library exports what
+moe_block.h declares, sizes its workspaces, and refuses bad arguments before it
+touches the GPU (no compute call is made here)."""
+
+import ctypes
+import math
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+from sparse_moe_layer_03_amd import binding as B
+from sparse_moe_layer_03_amd import block as K
+from sparse_moe_layer_03_amd import train as T
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, EINVAL, EUNSUPPORTED, EHIP, ENONFINITE, EALIGN = 0, -1, -2, -3, -4, -5
+A = 0x1000                                  # an aligned address that is never followed
+P = ctypes.c_void_p
+ref = ctypes.byref
+
+
+def test_library_exports_every_declared_symbol():
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "moe_block.h")).read(), flags=re.S)
+    names = set(re.findall(r"^\s*[a-z_0-9]+\s*\*?\s*(moe_[a-z_0-9]+)\s*\(", text, flags=re.M))
+    assert names == set(K.ENTRY_POINTS)
+    for path in (B.LIB_PATH, B.LIB_CHECKS_PATH):
+        L = ctypes.CDLL(path)
+        for n in names:
+            assert hasattr(L, n), (path, n)
+
+
+def test_struct_sizes_match_the_header(tmp_path):
+    src = tmp_path / "s.c"
+    names = ("moe_select_params", "moe_quant_shape", "moe_i8_shape", "moe_ffn_i8_io", "moe_norm_shape", "moe_rows",
+             "moe_norm_io", "moe_norm_grad_io")
+    src.write_text('#include <stdio.h>\n#include "moe_block.h"\nint main(void) { printf("' + "%zu " * len(names) + '", ' +
+                   ", ".join(f"sizeof({n})" for n in names) + "); return 0; }\n")
+    exe = tmp_path / "s"
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
+    assert got == [ctypes.sizeof(c) for c in (K.MoeSelectParams, K.MoeQuantShape, K.MoeI8Shape, K.MoeFfnI8IO, K.MoeNormShape,
+                                              K.MoeRows, K.MoeNormIO, K.MoeNormGradIO)]
+
+
+# ---- selection
+
+
+def layer(T_=16, d=128, n=64, z=32, f=64, k=8, dt="bf16", scaling=1.0):
+    return B.make_shape(T_, d, n, z, f, k, dt, scaling)
+
+
+def select(s, p, logits=A, ld=96, bias=A, idx=A, gate=A):
+    return K.lib().moe_select(ref(s), ref(p) if p is not None else None, P(logits), ld, P(bias), P(idx), P(gate), None)
+
+
+def select_bwd(s, p, logits=A, ld=96, idx=A, dgate=A, dlogits=A):
+    return K.lib().moe_select_backward(ref(s), ref(p), P(logits), ld, P(idx), P(dgate), P(dlogits), None)
+
+
+def route(s, p, x=A, w=A, lb=A, bias=A, idx=A, gate=A, logits=A, ws=A):
+    return K.lib().moe_route_select(ref(s), ref(p), *map(P, (x, w, lb, bias, idx, gate, logits, ws)), None)
+
+
+def rule(**kw):
+    p = K.make_select("sigmoid", 4, 2, 2, True)
+    for n, v in kw.items():
+        setattr(p, n, v)
+    return p
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(score=2), EINVAL), (dict(score=-1), EINVAL), (dict(n_groups=0), EINVAL), (dict(n_groups=5), EINVAL),
+    (dict(top_groups=0), EINVAL), (dict(top_groups=5), EINVAL), (dict(group_best=0), EINVAL), (dict(group_best=3), EINVAL),
+    (dict(n_groups=96, top_groups=90, group_best=2), EINVAL), (dict(n_groups=96, top_groups=7, group_best=1), EINVAL),
+    (dict(n_groups=96, top_groups=90, group_best=1), EUNSUPPORTED), (dict(renorm_eps=math.nan), ENONFINITE),
+    (dict(renorm_eps=math.inf), ENONFINITE), (dict(renorm_eps=-1.0), EINVAL),
+])
+def test_selection_rules_are_refused(change, code):
+    p = rule(**change)
+    assert select(layer(), p) == code
+    assert select_bwd(layer(), p) == code
+    assert route(layer(), p) == code
+    io = T.MoeBackwardIO(*[A] * len(T._IO_IN + T._IO_OUT), 0, 0)
+    assert K.lib().moe_layer_backward_select(ref(layer()), ref(p), ref(io), P(A), None) == code
+
+
+def test_selection_refuses_shapes_and_pointers():
+    assert select(layer(), None) == EINVAL
+    for s, code in ((layer(T_=0), EINVAL), (layer(k=0), EINVAL), (layer(k=17), EUNSUPPORTED), (layer(n=1000, z=100), EUNSUPPORTED),
+                    (layer(d=100), EUNSUPPORTED), (layer(T_=1 << 27, k=1), EUNSUPPORTED), (layer(scaling=math.inf), ENONFINITE)):
+        assert select(s, K.make_select(), ld=2000) == code
+        assert select_bwd(s, K.make_select(), ld=2000) == code
+        assert route(s, K.make_select()) == code
+    p = rule()
+    assert select(layer(), p, ld=95) == EINVAL and select_bwd(layer(), p, ld=95) == EINVAL
+    for n in ("logits", "idx", "gate"):
+        assert select(layer(), p, **{n: 0}) == EINVAL and select(layer(), p, **{n: A + 2}) == EALIGN, n
+    assert select(layer(), p, bias=A + 2) == EALIGN
+    for n in ("logits", "idx", "dgate", "dlogits"):
+        assert select_bwd(layer(), p, **{n: 0}) == EINVAL and select_bwd(layer(), p, **{n: A + 2}) == EALIGN, n
+    for n in ("x", "w", "idx", "gate", "logits", "ws"):
+        assert route(layer(), p, **{n: 0}) == EINVAL, n
+    for n in ("x", "w", "lb", "bias", "idx", "gate", "logits", "ws"):
+        assert route(layer(), p, **{n: A + 2}) == EALIGN, n
+
+
+def test_layer_backward_of_a_selection_needs_logits():
+    io = T.MoeBackwardIO(*[A] * len(T._IO_IN + T._IO_OUT), 0, 0)
+    io.w_router = io.logits = io.dlogits = io.dw_router = None
+    assert K.lib().moe_layer_backward_select(ref(layer()), ref(rule()), ref(io), P(A), None) == EINVAL
+    assert K.lib().moe_layer_backward_select(ref(layer()), ref(rule()), None, P(A), None) == EINVAL
+    io = T.MoeBackwardIO(*[A] * len(T._IO_IN + T._IO_OUT), 0, 0)
+    assert K.lib().moe_layer_backward_select(ref(layer()), ref(rule()), ref(io), None, None) == EINVAL
+    io.x = A + 8
+    assert K.lib().moe_layer_backward_select(ref(layer()), ref(rule()), ref(io), P(A), None) == EALIGN
+
+
+# ---- 8-bit integers
+
+
+def quant(x=A, q=A, scale=A, **kw):
+    s = K.make_quant_shape("bf16", 16, 24)
+    for n, v in kw.items():
+        setattr(s, n, v)
+    return K.lib().moe_quantize_rows(ref(s), P(x), P(q), P(scale), None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(dtype=2), EUNSUPPORTED), (dict(M=-1), EINVAL), (dict(K=0), EINVAL), (dict(ldx=23), EINVAL), (dict(ldq=23), EINVAL),
+    (dict(reserved=1), EINVAL), (dict(M=1 << 27), EUNSUPPORTED), (dict(K=1 << 17, ldx=1 << 17, ldq=1 << 17), EUNSUPPORTED),
+    (dict(ldx=1 << 24), EUNSUPPORTED), (dict(ldq=1 << 24), EUNSUPPORTED), (dict(x=0), EINVAL), (dict(q=0), EINVAL),
+    (dict(scale=0), EINVAL), (dict(x=A + 8), EALIGN), (dict(q=A + 8), EALIGN), (dict(scale=A + 2), EALIGN),
+    (dict(M=0, x=0, q=0, scale=0), OK),
+])
+def test_quantize_rows_refuses(change, code):
+    assert quant(**change) == code
+
+
+def matmul(offsets=A, a=A, sa=A, w=A, sw=A, c=A, ws=A, **kw):
+    s = K.make_i8_shape("bf16", 4, 16, 8, 32)
+    for n, v in kw.items():
+        setattr(s, n, v)
+    return s, K.lib().moe_matmul_i8(ref(s), *map(P, (offsets, a, sa, w, sw, c, ws)), None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(out_dtype=2), EUNSUPPORTED), (dict(n_groups=0), EINVAL), (dict(M=-1), EINVAL), (dict(N=0), EINVAL), (dict(K=0), EINVAL),
+    (dict(lda=31), EINVAL), (dict(ldc=7), EINVAL), (dict(reserved=1), EINVAL), (dict(n_groups=1025), EUNSUPPORTED),
+    (dict(M=1 << 27), EUNSUPPORTED), (dict(N=(1 << 20) + 1, ldc=(1 << 20) + 1), EUNSUPPORTED),
+    (dict(K=1 << 17, lda=1 << 17), EUNSUPPORTED), (dict(lda=1 << 24), EUNSUPPORTED), (dict(ldc=1 << 24), EUNSUPPORTED),
+])
+def test_matmul_refuses_shapes(change, code):
+    s, rc = matmul(**change)
+    assert rc == code
+    assert K.moe_matmul_i8_workspace_bytes(s) == 0
+
+
+def test_matmul_refuses_pointers():
+    for n in ("offsets", "a", "sa", "w", "sw", "c"):
+        assert matmul(**{n: 0})[1] == EINVAL, n
+        assert matmul(**{n: A + 2})[1] == EALIGN, n
+    assert matmul(ws=A + 2)[1] == EALIGN
+
+
+def ffn(s, **kw):
+    io = K.MoeFfnI8IO(*[A] * len(K._FFN_IO))
+    io.xq = io.x_scale = None
+    ws = kw.pop("ws", A)
+    for n, v in kw.items():
+        setattr(io, n, v)
+    return K.lib().moe_expert_ffn_i8(ref(s), ref(io), P(ws), None)
+
+
+def test_ffn_refuses():
+    s = layer()
+    for n in ("x", "perm", "offsets", "w_gate", "w_up", "w_down", "s_gate", "s_up", "s_down", "y_perm"):
+        assert ffn(s, **{n: None}) == EINVAL, n
+        assert ffn(s, **{n: A + 2}) == EALIGN, n
+    assert ffn(s, ws=0) == EINVAL and ffn(s, ws=A + 8) == EALIGN
+    assert ffn(s, xq=A) == EINVAL                                  # both x and xq
+    assert ffn(s, x=None, xq=A) == EINVAL                          # without its scales
+    assert ffn(s, x_scale=A) == EINVAL
+    assert ffn(s, x=None, xq=A + 8, x_scale=A) == EALIGN
+    assert K.lib().moe_expert_ffn_i8(ref(s), None, P(A), None) == EINVAL
+    for bad, code in ((layer(T_=0), EINVAL), (layer(d=100), EUNSUPPORTED), (layer(T_=1 << 24), EUNSUPPORTED),
+                      (layer(d=1 << 17), EUNSUPPORTED), (layer(f=1 << 17), EUNSUPPORTED)):
+        assert ffn(bad) == code
+        assert K.moe_expert_ffn_i8_workspace_bytes(bad) == 0
+    rows = 16 * 8
+    assert K.moe_expert_ffn_i8_workspace_bytes(s) >= 16 * 128 + rows * 128 + rows * 64 * 3
+
+
+# ---- norms
+
+
+def R(p=A, ld=64):
+    return K.MoeRows(p, ld)
+
+
+def norm(shape=None, **kw):
+    s = K.make_norm_shape(16, 64, "bf16", 1e-6, 1.0, 4)
+    for n, v in (shape or {}).items():
+        setattr(s, n, v)
+    io = K.MoeNormIO(R(), R(), A, A, A, R(), R(), A, A)
+    for n, v in kw.items():
+        setattr(io, n, v)
+    return K.lib().moe_norm_residual(ref(s), ref(io), None)
+
+
+def norm_bwd(shape=None, ws=A, **kw):
+    s = K.make_norm_shape(16, 64, "bf16", 1e-6, 1.0, 4)
+    for n, v in (shape or {}).items():
+        setattr(s, n, v)
+    io = K.MoeNormGradIO(R(), R(), A, A, A, R(), R(), R(), R(), A, A, A, 0, 0)
+    for n, v in kw.items():
+        setattr(io, n, v)
+    return K.lib().moe_norm_residual_backward(ref(s), ref(io), P(ws), None)
+
+
+NONE = R(0, 0)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(T=-1), EINVAL), (dict(d_model=0), EINVAL), (dict(rows_per_gate=0), EINVAL), (dict(dtype=2), EUNSUPPORTED),
+    (dict(T=1 << 27), EUNSUPPORTED), (dict(d_model=32769), EUNSUPPORTED), (dict(eps=math.nan), ENONFINITE),
+    (dict(eps=-1.0), EINVAL), (dict(res_scale=math.inf), ENONFINITE),
+])
+def test_norm_refuses_shapes(change, code):
+    assert norm(change) == code and norm_bwd(change) == code
+    s = K.make_norm_shape(16, 64, "bf16", 1e-6, 1.0, 4)
+    assert K.lib().moe_norm_residual(None, None, None) == EINVAL
+    for n, v in change.items():
+        setattr(s, n, v)
+    assert K.moe_norm_residual_backward_workspace_bytes(s) == 0
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(r=NONE), EINVAL), (dict(h=NONE, q=None, q_scale=None), EINVAL), (dict(q=None), EINVAL), (dict(q_scale=None), EINVAL),
+    (dict(w_pre=None), EINVAL), (dict(w_pre=None, h=NONE), EINVAL), (dict(y=NONE), EINVAL), (dict(y=NONE, x=NONE), EINVAL),
+    (dict(y=NONE, r=NONE, w_post=None), EINVAL), (dict(y=NONE, r=NONE, gate=None), EINVAL),
+    (dict(x=R(A + 8)), EALIGN), (dict(y=R(A + 8)), EALIGN), (dict(r=R(A + 8)), EALIGN), (dict(h=R(A + 8)), EALIGN),
+    (dict(x=R(A, 63)), EINVAL), (dict(y=R(A, 63)), EINVAL), (dict(r=R(A, 63)), EINVAL), (dict(h=R(A, 63)), EINVAL),
+    (dict(x=R(A, 1 << 24)), EUNSUPPORTED), (dict(w_post=A + 8), EALIGN), (dict(gate=A + 8), EALIGN), (dict(w_pre=A + 8), EALIGN),
+    (dict(q=A + 8), EALIGN), (dict(q_scale=A + 2), EALIGN),
+])
+def test_norm_refuses_arrays(kw, code):
+    assert norm(**kw) == code
+
+
+def test_norm_before_the_first_block_has_no_residual_scale():
+    assert norm(dict(res_scale=0.5), y=NONE, r=NONE, w_post=None, gate=None) == EINVAL
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dh=NONE), EINVAL), (dict(w_pre=None), EINVAL), (dict(r=NONE), EINVAL), (dict(dy=NONE), EINVAL), (dict(y=NONE), EINVAL),
+    (dict(y=NONE, dy=NONE), EINVAL), (dict(gate=None), EINVAL), (dict(w_post=None), EINVAL), (dict(reserved=1), EINVAL),
+    (dict(w_pre=None, dh=NONE), EINVAL), (dict(w_pre=None, dh=NONE, dw_pre=None, dr=NONE), EINVAL),
+    (dict(ws=0), EINVAL), (dict(ws=A + 8), EALIGN), (dict(dgate=A + 8), EALIGN), (dict(dw_post=A + 8), EALIGN),
+    (dict(dw_pre=A + 8), EALIGN), (dict(dx=R(A + 8)), EALIGN), (dict(dr=R(A, 1)), EINVAL), (dict(dx=R(A, 1 << 24)), EUNSUPPORTED),
+])
+def test_norm_backward_refuses_arrays(kw, code):
+    assert norm_bwd(**kw) == code
+
+
+# ---- the binding's own checks
+
+
+def test_binding_refuses_tensors_off_the_gpu():
+    s = layer()
+    x = torch.zeros(16, 96)
+    for call in (lambda: K.moe_select(s, K.make_select(), x, None, x, x),
+                 lambda: K.moe_quantize_rows(K.make_quant_shape("f32", 16, 96), x, x, x),
+                 lambda: K.moe_matmul_i8(K.make_i8_shape("f32", 1, 16, 96, 96), None, x, x, x, x, x),
+                 lambda: K.moe_norm_residual(K.make_norm_shape(16, 96, "f32"), x=x, w_pre=x, h=x)):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_binding_refuses_overlaps():
+    t = torch.zeros(100)
+    a, b = t[:60].view(6, 10), t[50:].view(5, 10)
+    with pytest.raises(ValueError, match="overlap"):
+        K._apart([("a", a)], [("b", b)])
+    with pytest.raises(ValueError, match="overlap"):
+        K._apart([("a", a), ("b", b)])
+    K._apart([("a", a)], [("a2", a)], {("a", "a2")})
+    with pytest.raises(ValueError, match="overlap"):
+        K._apart([("a", a)], [("a2", a[:5])], {("a", "a2")})
+    K._apart([("a", a[:5]), ("b", b), ("c", None)], [("d", None)])

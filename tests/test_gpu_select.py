@@ -1,0 +1,319 @@
+"""moe_select, moe_select_backward and moe_route_select against the definition in
+64 bits: scores, groups, ties, masked and non-finite logits, keys that fp32
+cannot tell apart, row strides, many tokens, other streams, captured graphs."""
+
+import math
+
+import pytest
+import torch
+
+from sparse_moe_layer_03_amd import binding as B
+from sparse_moe_layer_03_amd import block as K
+from tests.block_util import U, say, score_error, scores, select_bwd_ref, select_ref
+
+pytestmark = pytest.mark.gpu
+
+# score, groups, kept, best, renorm, eps
+RULES = [("softmax", 1, 1, 1, False, 0.0), ("softmax", 1, 1, 1, True, 0.0), ("sigmoid", 1, 1, 1, True, 1e-20),
+         ("sigmoid", 4, 2, 2, True, 0.0), ("softmax", 4, 3, 1, False, 0.0), ("sigmoid", 2, 1, 2, False, 0.0),
+         ("softmax", 8, 3, 2, True, 1e-3)]
+
+
+def rule(r):
+    return K.make_select(*r)
+
+
+def shape(T, E, k, scaling=1.0):
+    return B.make_shape(T, 64, E, 0, 64, k, "bf16", scaling)
+
+
+def run(s, p, logits, bias, stream=None):
+    idx = torch.full((s.T, s.top_k), -7, dtype=torch.int32, device="cuda")
+    gate = torch.full((s.T, s.top_k), math.nan, device="cuda")
+    K.moe_select(s, p, logits, bias, idx, gate, stream=stream)
+    torch.cuda.synchronize()
+    return idx, gate
+
+
+def check(T, E, k, r, logits=None, bias="random", seed=0, scaling=2.5, spread=1.0):
+    say(f"[select] T={T} E={E} k={k} {r} seed={seed}")
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    if logits is None:
+        logits = torch.randn((T, E), generator=g, device="cuda") * spread
+    if isinstance(bias, str):
+        bias = torch.randn(E, generator=g, device="cuda") * 0.05
+    s, p = shape(T, E, k, scaling), rule(r)
+    idx, gate = run(s, p, logits, bias)
+    want, wg, _ = select_ref(p, logits, bias, k, scaling)
+    bad = (idx != want).any(1)
+    assert not bad.any(), (int(bad.sum()), idx[bad][:2], want[bad][:2])
+    err = (gate.double() - wg).abs()
+    same = torch.isnan(gate) & torch.isnan(wg)
+    assert (same | (err <= 2 * score_error(p, logits) * wg.abs() + 2.0 ** -125 * scaling)).all(), float(err.max())
+    return idx, gate
+
+
+@pytest.mark.parametrize("r", RULES)
+@pytest.mark.parametrize("T,E,k", [(1, 8, 2), (3, 96, 8), (257, 384, 8), (128, 768, 12), (65, 1024, 16), (5, 200, 1),
+                                   (1000, 16, 8)])
+def test_sizes(T, E, k, r):
+    if E % r[1] or k > r[2] * (E // r[1]) or r[3] > E // r[1]:
+        pytest.skip("not a shape of this rule")
+    check(T, E, k, r)
+
+
+@pytest.mark.parametrize("E,G,kept,k", [(1023, 33, 17, 16), (63, 63, 20, 16), (64, 64, 64, 3), (60, 20, 7, 16), (1020, 12, 1, 16),
+                                        (1020, 17, 9, 12), (6, 3, 2, 4), (990, 2, 1, 1)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_odd_groups(E, G, kept, k, score):
+    check(70, E, k, (score, G, kept, 1, True, 0.0))
+    if E // G > 1:
+        check(70, E, k, (score, G, kept, 2, False, 0.0), seed=1)
+
+
+@pytest.mark.parametrize("E,k", [(5, 5), (1, 1), (16, 16), (64, 16), (65, 16), (130, 3), (1000, 7)])
+def test_all_or_few_experts(E, k):
+    check(37, E, k, ("softmax", 1, 1, 1, True, 0.0))
+    check(37, E, k, ("sigmoid", 1, 1, 1, False, 0.0), bias=None)
+
+
+@pytest.mark.parametrize("r", RULES)
+def test_equal_keys_go_to_the_lowest_id(r):
+    T, E, k = 33, 96, 8
+    check(T, E, k, r, logits=torch.zeros((T, E), device="cuda"), bias=None)
+    check(T, E, k, r, logits=torch.full((T, E), 3.25, device="cuda"), bias=torch.full((E,), -0.5, device="cuda"))
+    g = torch.Generator(device="cuda").manual_seed(5)
+    few = torch.randint(0, 3, (T, E), generator=g, device="cuda").float()
+    check(T, E, k, r, logits=few, bias=None)
+
+
+@pytest.mark.parametrize("r", RULES)
+def test_keys_that_fp32_cannot_tell_apart(r):
+    """Logits within a few steps of each other: scores equal in fp32, not in 64
+    bits; with a bias that takes logits' order away."""
+    T, E, k = 200, 96, 8
+    g = torch.Generator(device="cuda").manual_seed(7)
+    steps = torch.randint(0, 64, (T, E), generator=g, device="cuda")
+    check(T, E, k, r, logits=(1.0 + steps * 2.0 ** -23).float(), bias=None)
+    check(T, E, k, r, logits=(1.0 + steps * 2.0 ** -23).float(), bias=(torch.arange(E, device="cuda") % 3) * 2.0 ** -30)
+    check(T, E, k, r, logits=torch.randn((T, E), generator=g, device="cuda") * 1e-7, bias=None)
+
+
+def test_large_random_batches():
+    check(16384, 768, 12, ("softmax", 1, 1, 1, False, 0.0), seed=3)
+    check(16385, 768, 12, ("sigmoid", 8, 4, 2, True, 0.0), seed=4)
+    check(40000, 96, 8, ("sigmoid", 1, 1, 1, True, 0.0), seed=5, spread=4.0)
+
+
+@pytest.mark.parametrize("r", RULES)
+def test_bias_switches_experts_off_and_on(r):
+    T, E, k = 40, 96, 8
+    bias = torch.zeros(E, device="cuda")
+    bias[::3] = -math.inf
+    bias[5] = math.inf
+    idx, _ = check(T, E, k, r, bias=bias)
+    assert (idx == 5).any(1).all()
+    bias = torch.full((E,), -math.inf, device="cuda")
+    bias[40] = 0.0                              # fewer experts than slots
+    idx, _ = check(T, E, k, r, bias=bias)
+    assert (idx == 40).any(1).all()
+    check(T, E, k, r, bias=torch.full((E,), math.inf, device="cuda"))
+    check(T, E, k, r, bias=torch.full((E,), math.nan, device="cuda"))
+
+
+@pytest.mark.parametrize("r", RULES)
+@pytest.mark.parametrize("low", [-math.inf, torch.finfo(torch.float32).min])
+def test_masked_logits(r, low):
+    T, E, k = 50, 96, 8
+    g = torch.Generator(device="cuda").manual_seed(9)
+    logits = torch.randn((T, E), generator=g, device="cuda")
+    logits[torch.rand((T, E), generator=g, device="cuda") < 0.7] = low
+    logits[3], logits[4, 1:] = low, low
+    idx, gate = check(T, E, k, r, logits=logits)
+    if low == -math.inf or r[0] == "sigmoid":   # a row without anything: scores of 0
+        assert (gate[3] == 0).all()
+
+
+def test_non_finite_logits():
+    T, E, k = 6, 32, 4
+    logits = torch.randn((T, E), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    logits[1, 7] = math.nan
+    logits[2, 9] = math.inf
+    logits[3, 9] = logits[3, 30] = math.inf
+    idx, gate = check(T, E, k, ("sigmoid", 1, 1, 1, False, 0.0), logits=logits, bias=None)
+    assert not (idx[1] == 7).any()
+    idx, gate = check(T, E, k, ("softmax", 1, 1, 1, False, 0.0), logits=logits, bias=None)
+    assert torch.isnan(gate[1]).all() and (idx[1] == torch.arange(k, device="cuda")).all()
+
+
+def test_row_strides_and_far_rows():
+    g = torch.Generator(device="cuda").manual_seed(11)
+    wide = torch.randn((300, 1000), generator=g, device="cuda")
+    check(300, 96, 8, RULES[0], logits=wide[:, 17:113])
+    E, T = 1024, (1 << 21) + 3                  # offsets behind 2^31 elements
+    big = torch.empty((T, E), device="cuda")
+    big[:4].normal_(generator=g), big[-4:].normal_(generator=g)
+    big[4:-4] = 0
+    s, p = shape(T, E, 8), rule(RULES[3])
+    idx, gate = run(s, p, big, None)
+    for part in (slice(0, 4), slice(T - 4, T)):
+        want, wg, _ = select_ref(p, big[part], None, 8, 1.0)
+        assert torch.equal(idx[part].long(), want)
+    assert torch.equal(idx[5], idx[T - 5])
+
+
+# ---- gradient
+
+
+def check_bwd(T, E, k, r, logits=None, idx=None, seed=0, scaling=2.5):
+    say(f"[select_backward] T={T} E={E} k={k} {r}")
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    if logits is None:
+        logits = torch.randn((T, E), generator=g, device="cuda")
+    p, s = rule(r), shape(T, E, k, scaling)
+    if idx is None:
+        idx = select_ref(p, logits, None, k, scaling)[0].to(torch.int32)
+    dgate = torch.randn((T, k), generator=g, device="cuda")
+    out = torch.full((T, E), math.nan, device="cuda")
+    K.moe_select_backward(s, p, logits, idx, dgate, out)
+    torch.cuda.synchronize()
+    ref, mag = select_bwd_ref(p, logits, idx.long(), dgate, scaling)
+    err = (out.double() - ref).abs()
+    # p, D and the sums each carry a score's error
+    assert (err <= 8 * score_error(p, logits) * mag + 2.0 ** -120).all(), float(err.max())
+    return out, ref
+
+
+@pytest.mark.parametrize("r", RULES)
+@pytest.mark.parametrize("T,E,k", [(1, 8, 2), (300, 96, 8), (65, 768, 12), (130, 1024, 16), (64, 65, 1), (2000, 16, 8)])
+def test_gradient(T, E, k, r):
+    if E % r[1] or k > r[2] * (E // r[1]) or r[3] > E // r[1]:
+        pytest.skip("not a shape of this rule")
+    check_bwd(T, E, k, r)
+
+
+@pytest.mark.parametrize("r", RULES)
+def test_gradient_against_autograd_and_differences(r):
+    """For a fixed selection: the gradient of sum(gate * c), by automatic
+    differentiation and by central differences, in 64 bits."""
+    T, E, k, scaling = 7, 96, 8, 1.7
+    g = torch.Generator(device="cuda").manual_seed(2)
+    logits, p = torch.randn((T, E), generator=g, device="cuda"), rule(r)
+    idx = select_ref(p, logits, None, k, scaling)[0]
+    c = torch.randn((T, k), generator=g, device="cuda").double()
+
+    def value(x):
+        f = (torch.sigmoid(x) if p.score else torch.softmax(x, 1)).gather(1, idx)
+        if p.renorm:
+            f = f / (f.sum(1, keepdim=True) + p.renorm_eps)
+        return (scaling * f * c).sum()
+
+    x = logits.double().requires_grad_()
+    value(x).backward()
+    out = torch.empty((T, E), device="cuda")
+    K.moe_select_backward(shape(T, E, k, scaling), p, logits, idx.to(torch.int32), c.float(), out)
+    assert (out.double() - x.grad).abs().max() < 1e-5
+    h = 1e-5
+    for t, e in ((0, int(idx[0, 0])), (3, int(idx[3, 5])), (6, 40)):
+        d = torch.zeros((T, E), dtype=torch.float64, device="cuda")
+        d[t, e] = h
+        diff = (value(logits.double() + d) - value(logits.double() - d)) / (2 * h)
+        assert abs(float(diff) - float(out[t, e])) < 1e-5
+
+
+@pytest.mark.parametrize("r", RULES)
+def test_gradient_of_odd_selections(r):
+    """An expert named twice, ids outside, rows without scores."""
+    T, E, k = 20, 96, 8
+    g = torch.Generator(device="cuda").manual_seed(3)
+    idx = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    idx[0] = 5
+    idx[1, 3] = idx[1, 0]
+    check_bwd(T, E, k, r, idx=idx)
+    idx[2, 1], idx[3, 2], idx[4, 0] = -1, E, 1 << 30
+    check_bwd(T, E, k, r, idx=idx)
+    logits = torch.randn((T, E), generator=g, device="cuda")
+    logits[5] = -math.inf
+    logits[6, 1:] = -math.inf
+    out, _ = check_bwd(T, E, k, r, logits=logits, idx=idx)
+    assert (out[5] == 0).all()
+
+
+# ---- router, streams, graphs
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,n,z,k", [(1, 128, 8, 4, 2), (300, 256, 64, 32, 8), (1024, 1024, 96, 0, 8), (700, 2048, 512, 256, 12)])
+def test_route_select_is_the_product_and_select(dtype, T, d, n, z, k):
+    g = torch.Generator(device="cuda").manual_seed(4)
+    s = B.make_shape(T, d, n, z, 64, k, dtype, 1.5)
+    E, dt = n + z, torch.bfloat16 if dtype == "bf16" else torch.float32
+    x = torch.randn((T, d), generator=g, device="cuda").to(dt)
+    w = (torch.randn((E, d), generator=g, device="cuda") * d ** -0.5).to(dt)
+    lb = torch.randn(E, generator=g, device="cuda")
+    ws = torch.empty(B.moe_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+    p = K.make_select("sigmoid", 4, 3, 2, True)
+    for logit_bias, bias in ((None, None), (lb, lb * 0.01)):
+        idx = torch.empty((T, k), dtype=torch.int32, device="cuda")
+        gate, logits = torch.empty((T, k), device="cuda"), torch.empty((T, E), device="cuda")
+        K.moe_route_select(s, p, x, w, logit_bias, bias, idx, gate, logits, ws)
+        torch.cuda.synchronize()
+        ref = x.double() @ w.double().t()
+        mag = x.double().abs() @ w.double().abs().t()
+        if logit_bias is not None:
+            ref, mag = ref + lb.double(), mag + lb.double().abs()
+        assert ((logits.double() - ref).abs() <= (d + 16) * 2.0 ** -23 * mag).all()
+        want, wg, _ = select_ref(p, logits, bias, k, 1.5)
+        assert torch.equal(idx.long(), want)
+        assert ((gate.double() - wg).abs() <= 2 * score_error(p, logits) * wg).all()
+
+
+def test_softmax_without_groups_is_moe_route():
+    """The case that moe_route computes: the same experts but where fp32 keys
+    tie or round another way, and the same gates."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    s = B.make_shape(2000, 256, 64, 32, 64, 8, "bf16", 1.5)
+    x = torch.randn((2000, 256), generator=g, device="cuda").bfloat16()
+    w = (torch.randn((96, 256), generator=g, device="cuda") / 16).bfloat16()
+    bias = torch.randn(96, generator=g, device="cuda") * 0.01
+    ws = torch.empty(B.moe_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+    new = lambda d, *n: torch.empty(n, dtype=d, device="cuda")  # noqa: E731
+    i1, g1, l1 = new(torch.int32, 2000, 8), new(torch.float32, 2000, 8), new(torch.float32, 2000, 96)
+    B.moe_route(s, x, w, None, bias, i1, g1, l1, ws)
+    i2, g2 = torch.empty_like(i1), torch.empty_like(g1)
+    K.moe_select(s, K.make_select(), l1, bias, i2, g2)
+    torch.cuda.synchronize()
+    same = (i1 == i2).all(1)
+    assert same.float().mean() > 0.999
+    assert ((g1 - g2).abs() <= 1e-5 * g1)[same].all()
+
+
+def test_streams_graphs_and_repeats():
+    T, E, k = 513, 384, 8
+    g = torch.Generator(device="cuda").manual_seed(8)
+    a, b = (torch.randn((T, E), generator=g, device="cuda") for _ in range(2))
+    s, p = shape(T, E, k), rule(RULES[6][:1] + (8, 3, 2, True, 0.0))
+    want = {}
+    for name, x in (("a", a), ("b", b)):
+        want[name] = run(s, p, x, None)
+    side = torch.cuda.Stream()
+    idx, gate = run(s, p, a, None, stream=side)
+    assert torch.equal(idx, want["a"][0]) and torch.equal(gate, want["a"][1])
+    x, dgate = a.clone(), torch.randn((T, k), generator=g, device="cuda")
+    out = torch.empty((T, E), device="cuda")
+    K.moe_select(s, p, x, None, idx, gate)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        K.moe_select(s, p, x, None, idx, gate)
+        K.moe_select_backward(s, p, x, idx, dgate, out)
+    for name, v in (("b", b), ("a", a), ("b", b)):
+        x.copy_(v)
+        idx.zero_(), gate.zero_(), out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(idx, want[name][0]) and torch.equal(gate, want[name][1])
+        eager = torch.empty_like(out)
+        K.moe_select_backward(s, p, x, idx, dgate, eager)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager)
