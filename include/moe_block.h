@@ -17,7 +17,9 @@
  *     and permutations in device memory cannot be: the kernels keep every row
  *     that they name inside the arrays, so wrong ones give wrong values and
  *     never an access out of range (the debug build reports them,
- *     moe_debug_checks).
+ *     moe_debug_checks).  An array that is written must not overlap any other
+ *     of the call (MOE_EINVAL) but where the call says that it may be another's
+ *     memory.
  *   - Sums are formed in a fixed order, without atomics: the same call gives
  *     the same bits.
  */
@@ -96,7 +98,7 @@ int moe_route_select(const moe_shape* shape, const moe_select_params* params, co
  * and bias have no gradient.  A slot whose id is outside [0, E) counts as an
  * expert of score 0.
  *   logits [T, E] fp32, ld_logits >= E; topk_idx, dgate [T, top_k];
- *   dlogits [T, E] fp32, contiguous, must not overlap logits. */
+ *   dlogits [T, E] fp32, contiguous. */
 int moe_select_backward(const moe_shape* shape, const moe_select_params* params,
                         const float* logits, int64_t ld_logits, const int32_t* topk_idx,
                         const float* dgate, float* dlogits, void* stream);
@@ -155,7 +157,7 @@ size_t moe_matmul_i8_workspace_bytes(const moe_i8_shape* shape);
  *   rows.  Rows behind offsets[n_groups] are neither read nor written.
  * The sum is exact in 32 bits whatever the codes (-128 too); it is converted
  * to fp32 once, multiplied by a_scale, then by w_scale, and rounded to
- * out_dtype.  c must not overlap the inputs.  16-byte aligned a, W, c; offsets
+ * out_dtype.  16-byte aligned a, W, c; offsets
  * and scales 4; a, a_scale and c may be NULL when M = 0. */
 int moe_matmul_i8(const moe_i8_shape* shape, const int32_t* offsets, const int8_t* a,
                   const float* a_scale, const int8_t* w, const float* w_scale, void* c, void* ws,
@@ -232,8 +234,7 @@ typedef struct {
  * parts fall out: without y the call is the norm before the first block, h =
  * x rstd(x) w_pre (x needed, res_scale 1, w_post, gate and r absent); without
  * x the residual term is missing.  q and q_scale are moe_quantize_rows of h.
- * r may be x itself (same p and ld); otherwise outputs must not overlap inputs
- * or each other.  16-byte aligned arrays, any strides. */
+ * r may be x itself (same p and ld).  16-byte aligned arrays, any strides. */
 int moe_norm_residual(const moe_norm_shape* shape, const moe_norm_io* io, void* stream);
 
 typedef struct {
@@ -266,9 +267,8 @@ size_t moe_norm_residual_backward_workspace_bytes(const moe_norm_shape* shape);
  *   dw_post = sum_t g gate n,  c = g gate w_post
  *   dy = rstd(y) (c - n mean(c n))       (without w_post: n = y, dy = g gate)
  * in fp32, rounded once; the rounding of r in the forward pass is passed over.
- * A gradient whose forward value was absent must be absent.  dx may be dr, and
- * dy may be y or dr may be dy's memory (same p and ld); otherwise outputs must
- * not overlap inputs or each other.  With T = 0 the vectors' gradients are
+ * A gradient whose forward value was absent must be absent.  dx and dy may each
+ * be one of r, y, dr and dh themselves (same p and ld).  With T = 0 the vectors' gradients are
  * zeros (or stay, accumulating).  16-byte aligned arrays, any strides. */
 int moe_norm_residual_backward(const moe_norm_shape* shape, const moe_norm_grad_io* io, void* ws,
                                void* stream);

@@ -3,10 +3,10 @@ other selection rules for its router, its experts in 8-bit integers, and the
 norms before and after a block.
 
 Each ``moe_*`` function has the name of the C entry point it calls and takes
-torch tensors.  As in ``train``, the library checks sizes and alignment, the
-binding what only it can see: that every tensor lies on one GPU, is laid out as
-the call reads it, and is as large as the shape says.  Calls run on the
-tensors' device, on its current stream unless ``stream`` names another.
+torch tensors.  As in ``train``, the library checks sizes, alignment and
+overlaps, the binding what only it can see: that every tensor lies on one GPU,
+is laid out as the call reads it, and is as large as the shape says.  Calls run
+on the tensors' device, on its current stream unless ``stream`` names another.
 """
 
 from __future__ import annotations
@@ -17,7 +17,7 @@ import torch
 
 from . import binding as B
 from . import train as T
-from .train import _DTYPE, _dtype_code, _need, _on, _workspace
+from .train import _DTYPE, _dtype_code
 
 SCORES = {"softmax": 0, "sigmoid": 1}
 
@@ -56,21 +56,20 @@ class MoeNormShape(ctypes.Structure):
                [("eps", ctypes.c_float), ("res_scale", ctypes.c_float)]
 
 
-class MoeRows(ctypes.Structure):
-    _fields_ = [("p", ctypes.c_void_p), ("ld", ctypes.c_int64)]
+def _rows_fields(*names):
+    """moe_rows members, each as a pointer and the elements between rows."""
+    return [f for n in names for f in ((n, ctypes.c_void_p), (n + "_ld", ctypes.c_int64))]
 
 
 class MoeNormIO(ctypes.Structure):
-    _fields_ = [("x", MoeRows), ("y", MoeRows), ("w_post", ctypes.c_void_p), ("gate", ctypes.c_void_p),
-                ("w_pre", ctypes.c_void_p), ("r", MoeRows), ("h", MoeRows), ("q", ctypes.c_void_p),
-                ("q_scale", ctypes.c_void_p)]
+    _fields_ = _rows_fields("x", "y") + [(n, ctypes.c_void_p) for n in ("w_post", "gate", "w_pre")] + \
+        _rows_fields("r", "h") + [("q", ctypes.c_void_p), ("q_scale", ctypes.c_void_p)]
 
 
 class MoeNormGradIO(ctypes.Structure):
-    _fields_ = [("r", MoeRows), ("y", MoeRows), ("w_post", ctypes.c_void_p), ("gate", ctypes.c_void_p),
-                ("w_pre", ctypes.c_void_p), ("dr", MoeRows), ("dh", MoeRows), ("dx", MoeRows), ("dy", MoeRows),
-                ("dgate", ctypes.c_void_p), ("dw_post", ctypes.c_void_p), ("dw_pre", ctypes.c_void_p),
-                ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+    _fields_ = _rows_fields("r", "y") + [(n, ctypes.c_void_p) for n in ("w_post", "gate", "w_pre")] + \
+        _rows_fields("dr", "dh", "dx", "dy") + [(n, ctypes.c_void_p) for n in ("dgate", "dw_post", "dw_pre")] + \
+        [("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -101,37 +100,84 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-def _matrix(name, t, dtype, rows, width, device):
-    """t holds rows x width values, each row contiguous; returns the elements
-    between rows."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name}: a tensor on {device or 'a GPU'} is needed")
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: {t.dtype}, needed {dtype}")
-    shape, stride = t.shape, t.stride()
-    ld = stride[0] if len(shape) == 2 and shape[0] > 1 else width
-    if len(shape) != 2 or shape[0] < rows or shape[1] != width or (width > 1 and stride[1] != 1) or ld < width:
-        raise ValueError(f"{name}: shape {tuple(shape)} strides {stride}, needed [{rows}, {width}] in whole rows")
-    return ld
+# Checks of a tensor; each returns what the call takes of it.  Small calls are
+# as long as these, so they ask for as little as they can.
 
 
-def _apart(outs, ins=(), same=()):
-    """No output overlaps another or an input; pairs in `same` may be one and
-    the same memory (equal start and strides)."""
-    def span(t):
-        n = 1 + sum((s - 1) * st for s, st in zip(t.shape, t.stride())) if t.numel() else 0
-        return t.data_ptr(), t.data_ptr() + n * t.element_size()
+def _device(name, t):
+    """The index of the tensor's GPU."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: a tensor on a GPU is needed")
+    return t.get_device()
 
-    outs = [(n, t) for n, t in outs if t is not None]
-    ins = [(n, t) for n, t in ins if t is not None]
-    for i, (n, t) in enumerate(outs):
-        a0, a1 = span(t)
-        for m, u in outs[i + 1:] + ins:
-            b0, b1 = span(u)
-            if a0 < b1 and b0 < a1:
-                if (n, m) in same and a0 == b0 and t.shape == u.shape and t.stride() == u.stride():
-                    continue
-                raise ValueError(f"{n} and {m} overlap")
+
+def _flat(name, t, dtype, numel, dev):
+    """The address of a contiguous tensor of dtype on GPU dev with at least
+    numel elements."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or \
+            t.numel() < numel or not t.is_contiguous():
+        _refuse(name, t, f"{numel} contiguous elements of {dtype}", dev)
+    return t.data_ptr()
+
+
+def _opt(name, t, dtype, numel, dev):
+    return None if t is None else _flat(name, t, dtype, numel, dev)
+
+
+def _matrix(name, t, dtype, rows, width, dev):
+    """Address and elements between rows of a tensor of rows x width values, each
+    row contiguous; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.dim() == 2:
+        shape, (ld, one) = t.shape, t.stride()
+        if shape[0] <= 1:
+            ld = width
+        if shape[0] >= rows and shape[1] == width and (one == 1 or width == 1) and ld >= width:
+            return t.data_ptr(), ld
+    _refuse(name, t, f"[{rows}, {width}] of {dtype} in whole rows", dev)
+
+
+def _refuse(name, t, need, dev):
+    have = "no tensor"
+    if isinstance(t, torch.Tensor):
+        have = f"{tuple(t.shape)} of {t.dtype} on {t.device}, strides {t.stride()}"
+    raise ValueError(f"{name}: {have}, needed {need} on cuda:{dev}")
+
+
+def _scratch(ws, need, dev):
+    """The address of at least `need` bytes on GPU dev (None: 0)."""
+    if need and (ws is None or ws.get_device() != dev or not ws.is_contiguous()
+                 or ws.numel() * ws.element_size() < need):
+        raise ValueError(f"ws: {need} bytes on cuda:{dev} are needed")
+    return None if ws is None else ws.data_ptr()
+
+
+def _on(dev, call, *args):
+    """call(*args) with GPU dev as the current one (workspaces go by its CUs)."""
+    if dev == torch.cuda.current_device():
+        return call(*args)
+    with torch.cuda.device(dev):
+        return call(*args)
+
+
+def _run(name, dev, stream, *args):
+    """The entry point's call on GPU dev, on `stream` or its current one."""
+    fn = getattr(lib(), name)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _run(name, dev, stream, *args)
+    if stream is None:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != dev:
+            raise ValueError(f"stream: on {stream.device}, needed on cuda:{dev}")
+        handle = stream.cuda_stream
+    else:
+        handle = int(stream)
+    rc = fn(*args, handle)
+    if rc:
+        B._check(name, rc)
 
 
 # ---- selection of experts
@@ -147,71 +193,50 @@ def make_select(score="softmax", n_groups=1, top_groups=None, group_best=1, reno
                            group_best, int(bool(renorm)), renorm_eps)
 
 
-def _check_select(s, logits, topk_idx, other, other_name, bias=None):
-    E, Tk = s.n_ffn + s.n_zero, s.T * s.top_k
-    if s.T < 1 or E < 1:
-        return logits.device, E     # (the library refuses it)
-    ld = _matrix("logits", logits, torch.float32, s.T, E, None)
-    dev = logits.device
-    _need("topk_idx", topk_idx, torch.int32, Tk, dev)
-    _need(other_name, other, torch.float32, Tk, dev)
-    if bias is not None:
-        _need("bias", bias, torch.float32, E, dev)
-    return dev, ld
+def _sizes(s):
+    return s.T, s.n_ffn + s.n_zero, s.T * s.top_k
 
 
 def moe_select(shape: B.MoeShape, params: MoeSelectParams, logits, bias, topk_idx, topk_gate, stream=None):
     """topk_idx, topk_gate of the experts that logits [T, E] and bias select."""
-    dev, ld = _check_select(shape, logits, topk_idx, topk_gate, "topk_gate", bias)
-    _apart([("topk_idx", topk_idx), ("topk_gate", topk_gate)], [("logits", logits), ("bias", bias)])
-    B._check("moe_select", _on(dev, lambda st: lib().moe_select(
-        ctypes.byref(shape), ctypes.byref(params), B._p(logits), ld, B._p(bias), B._p(topk_idx),
-        B._p(topk_gate), st), stream))
+    T_, E, Tk = _sizes(shape)
+    dev = _device("logits", logits)
+    f32 = torch.float32
+    x, ld = _matrix("logits", logits, f32, T_, E, dev)
+    _run("moe_select", dev, stream, ctypes.byref(shape), ctypes.byref(params), x, ld,
+         _opt("bias", bias, f32, E, dev), _flat("topk_idx", topk_idx, torch.int32, Tk, dev),
+         _flat("topk_gate", topk_gate, f32, Tk, dev))
 
 
 def moe_route_select(shape: B.MoeShape, params: MoeSelectParams, x, w_router, logit_bias, bias, topk_idx,
                      topk_gate, logits_out, ws, stream=None):
     """binding.moe_route with another selection rule; logits_out is needed."""
-    s, E = shape, shape.n_ffn + shape.n_zero
-    dev = x.device
-    if s.dtype in _DTYPE and s.T >= 1:
-        _need("x", x, _DTYPE[s.dtype], s.T * s.d_model)
-        _need("w_router", w_router, _DTYPE[s.dtype], E * s.d_model, dev)
-        _check_select(s, logits_out, topk_idx, topk_gate, "topk_gate", bias)
-        _need("logits_out", logits_out, torch.float32, s.T * E, dev)
-        if logit_bias is not None:
-            _need("logit_bias", logit_bias, torch.float32, E, dev)
-
-    def call(st):
-        _workspace(ws, B.moe_workspace_bytes(s), dev)
-        return lib().moe_route_select(ctypes.byref(s), ctypes.byref(params), B._p(x), B._p(w_router),
-                                      B._p(logit_bias), B._p(bias), B._p(topk_idx), B._p(topk_gate),
-                                      B._p(logits_out), B._p(ws), st)
-
-    B._check("moe_route_select", _on(dev, call, stream))
+    s, (T_, E, Tk) = shape, _sizes(shape)
+    dev, dt, f32 = _device("x", x), _DTYPE.get(s.dtype), torch.float32
+    _run("moe_route_select", dev, stream, ctypes.byref(s), ctypes.byref(params),
+         _flat("x", x, dt, T_ * s.d_model, dev), _flat("w_router", w_router, dt, E * s.d_model, dev),
+         _opt("logit_bias", logit_bias, f32, E, dev), _opt("bias", bias, f32, E, dev),
+         _flat("topk_idx", topk_idx, torch.int32, Tk, dev), _flat("topk_gate", topk_gate, f32, Tk, dev),
+         _flat("logits_out", logits_out, f32, T_ * E, dev), _scratch(ws, _on(dev, B.moe_workspace_bytes, s), dev))
 
 
 def moe_select_backward(shape: B.MoeShape, params: MoeSelectParams, logits, topk_idx, dgate, dlogits, stream=None):
     """dlogits [T, E] from the gradient dgate [T, top_k] at topk_gate."""
-    dev, ld = _check_select(shape, logits, topk_idx, dgate, "dgate")
-    _need("dlogits", dlogits, torch.float32, shape.T * (shape.n_ffn + shape.n_zero), dev)
-    _apart([("dlogits", dlogits)], [("logits", logits), ("topk_idx", topk_idx), ("dgate", dgate)])
-    B._check("moe_select_backward", _on(dev, lambda st: lib().moe_select_backward(
-        ctypes.byref(shape), ctypes.byref(params), B._p(logits), ld, B._p(topk_idx), B._p(dgate),
-        B._p(dlogits), st), stream))
+    T_, E, Tk = _sizes(shape)
+    dev = _device("logits", logits)
+    f32 = torch.float32
+    x, ld = _matrix("logits", logits, f32, T_, E, dev)
+    _run("moe_select_backward", dev, stream, ctypes.byref(shape), ctypes.byref(params), x, ld,
+         _flat("topk_idx", topk_idx, torch.int32, Tk, dev), _flat("dgate", dgate, f32, Tk, dev),
+         _flat("dlogits", dlogits, f32, T_ * E, dev))
 
 
 def moe_layer_backward_select(shape: B.MoeShape, params: MoeSelectParams, io: T.BackwardIO, ws, stream=None):
     """train.moe_layer_backward of a layer whose experts moe_select chose."""
     io.check(shape)
-    dev = io.tensors["x"].device
-
-    def call(st):
-        _workspace(ws, T.moe_layer_backward_workspace_bytes(shape), dev)
-        return lib().moe_layer_backward_select(ctypes.byref(shape), ctypes.byref(params), ctypes.byref(io.c),
-                                               B._p(ws), st)
-
-    B._check("moe_layer_backward_select", _on(dev, call, stream))
+    dev = _device("x", io.tensors["x"])
+    _run("moe_layer_backward_select", dev, stream, ctypes.byref(shape), ctypes.byref(params), ctypes.byref(io.c),
+         _scratch(ws, _on(dev, T.moe_layer_backward_workspace_bytes, shape), dev))
 
 
 # ---- products in 8-bit integers
@@ -221,16 +246,19 @@ def make_quant_shape(dtype, M, K, ldx=None, ldq=None) -> MoeQuantShape:
     return MoeQuantShape(_dtype_code(dtype), M, K, 0, K if ldx is None else ldx, K if ldq is None else ldq)
 
 
+def _strided(name, t, dtype, rows, width, ld, dev):
+    """The address of rows x width values, `ld` elements between rows."""
+    p, have = _matrix(name, t, dtype, rows, width, dev)
+    if have != ld and t.shape[0] > 1:
+        _refuse(name, t, f"{ld} elements between rows", dev)
+    return p
+
+
 def moe_quantize_rows(shape: MoeQuantShape, x, q, scale, stream=None):
     """q [M, K] int8 and scale [M]: x's rows in 8-bit codes."""
-    s = shape
-    if s.dtype in _DTYPE and s.M >= 0:
-        T._rows("x", x, _DTYPE[s.dtype], s.M, s.K, s.ldx, x.device)
-        T._rows("q", q, torch.int8, s.M, s.K, s.ldq, x.device)
-        _need("scale", scale, torch.float32, s.M, x.device)
-        _apart([("q", q), ("scale", scale)], [("x", x)])
-    B._check("moe_quantize_rows", _on(x.device, lambda st: lib().moe_quantize_rows(
-        ctypes.byref(s), B._p(x), B._p(q), B._p(scale), st), stream))
+    s, dev = shape, _device("x", x)
+    _run("moe_quantize_rows", dev, stream, ctypes.byref(s), _strided("x", x, _DTYPE.get(s.dtype), s.M, s.K, s.ldx, dev),
+         _strided("q", q, torch.int8, s.M, s.K, s.ldq, dev), _flat("scale", scale, torch.float32, s.M, dev))
 
 
 def quantize_rows(x, stream=None):
@@ -258,24 +286,13 @@ def moe_matmul_i8_workspace_bytes(shape: MoeI8Shape) -> int:
 def moe_matmul_i8(shape: MoeI8Shape, offsets, a, a_scale, w, w_scale, out, ws=None, stream=None):
     """out[p] = (a[p] w_e^T) a_scale[p] w_scale[e] for the rows p of group e;
     offsets None: one group of all rows."""
-    s = shape
-    dev = w.device
-    if s.out_dtype in _DTYPE and s.M >= 0 and s.n_groups >= 1:
-        if offsets is not None:
-            _need("offsets", offsets, torch.int32, s.n_groups + 1, dev)
-        T._rows("a", a, torch.int8, s.M, s.K, s.lda, dev)
-        _need("a_scale", a_scale, torch.float32, s.M, dev)
-        _need("w", w, torch.int8, s.n_groups * s.N * s.K, dev)
-        _need("w_scale", w_scale, torch.float32, s.n_groups * s.N, dev)
-        T._rows("out", out, _DTYPE[s.out_dtype], s.M, s.N, s.ldc, dev)
-        _apart([("out", out)], [("a", a), ("a_scale", a_scale), ("w", w), ("w_scale", w_scale), ("offsets", offsets)])
-
-    def call(st):
-        _workspace(ws, moe_matmul_i8_workspace_bytes(s), dev)
-        return lib().moe_matmul_i8(ctypes.byref(s), B._p(offsets), B._p(a), B._p(a_scale), B._p(w), B._p(w_scale),
-                                   B._p(out), B._p(ws), st)
-
-    B._check("moe_matmul_i8", _on(dev, call, stream))
+    s, dev, f32, i8 = shape, _device("w", w), torch.float32, torch.int8
+    GN = s.n_groups * s.N
+    _run("moe_matmul_i8", dev, stream, ctypes.byref(s), _opt("offsets", offsets, torch.int32, s.n_groups + 1, dev),
+         _strided("a", a, i8, s.M, s.K, s.lda, dev), _flat("a_scale", a_scale, f32, s.M, dev),
+         _flat("w", w, i8, GN * s.K, dev), _flat("w_scale", w_scale, f32, GN, dev),
+         _strided("out", out, _DTYPE.get(s.out_dtype), s.M, s.N, s.ldc, dev),
+         _scratch(ws, _on(dev, moe_matmul_i8_workspace_bytes, s), dev))
 
 
 class FfnI8IO:
@@ -288,24 +305,18 @@ class FfnI8IO:
         self.tensors = {n: given[n] for n in _FFN_IO}
         self.c = MoeFfnI8IO(*[B._p(self.tensors[n]) for n in _FFN_IO])
 
-    def check(self, s: B.MoeShape):
-        t, dt, f32, i32, i8 = self.tensors, _DTYPE.get(s.dtype), torch.float32, torch.int32, torch.int8
-        if dt is None:
-            return
-        Tk, w, dev = s.T * s.top_k, s.n_ffn * s.d_ff * s.d_model, self.device
-        need = dict(x=(dt, s.T * s.d_model), xq=(i8, s.T * s.d_model), x_scale=(f32, s.T), perm=(i32, Tk),
-                    offsets=(i32, s.n_ffn + s.n_zero + 1), w_gate=(i8, w), w_up=(i8, w), w_down=(i8, w),
-                    s_gate=(f32, s.n_ffn * s.d_ff), s_up=(f32, s.n_ffn * s.d_ff),
-                    s_down=(f32, s.n_ffn * s.d_model), y_perm=(dt, Tk * s.d_model))
-        for n, (d, k) in need.items():
-            if t[n] is None and n in ("x", "xq", "x_scale"):
-                continue
-            _need(n, t[n], d, k, dev)
-        _apart([("y_perm", t["y_perm"])], [(n, t[n]) for n in _FFN_IO[:-1]])
-
-    @property
-    def device(self):
-        return self.tensors["w_gate"].device
+    def check(self, s: B.MoeShape, dev):
+        t, f32, i8 = self.tensors, torch.float32, torch.int8
+        Td, Tk, nf, w = s.T * s.d_model, s.T * s.top_k, s.n_ffn * s.d_ff, s.n_ffn * s.d_ff * s.d_model
+        _opt("x", t["x"], _DTYPE.get(s.dtype), Td, dev)
+        _opt("xq", t["xq"], i8, Td, dev)
+        _opt("x_scale", t["x_scale"], f32, s.T, dev)
+        _flat("perm", t["perm"], torch.int32, Tk, dev)
+        _flat("offsets", t["offsets"], torch.int32, s.n_ffn + s.n_zero + 1, dev)
+        for n, scales in (("gate", nf), ("up", nf), ("down", s.n_ffn * s.d_model)):
+            _flat("w_" + n, t["w_" + n], i8, w, dev)
+            _flat("s_" + n, t["s_" + n], f32, scales, dev)
+        _flat("y_perm", t["y_perm"], _DTYPE.get(s.dtype), Tk * s.d_model, dev)
 
 
 def moe_expert_ffn_i8_workspace_bytes(shape: B.MoeShape) -> int:
@@ -314,13 +325,10 @@ def moe_expert_ffn_i8_workspace_bytes(shape: B.MoeShape) -> int:
 
 def moe_expert_ffn_i8(shape: B.MoeShape, io: FfnI8IO, ws, stream=None):
     """binding.moe_expert_ffn with 8-bit weights and rows; fills io's y_perm."""
-    io.check(shape)
-
-    def call(st):
-        _workspace(ws, moe_expert_ffn_i8_workspace_bytes(shape), io.device)
-        return lib().moe_expert_ffn_i8(ctypes.byref(shape), ctypes.byref(io.c), B._p(ws), st)
-
-    B._check("moe_expert_ffn_i8", _on(io.device, call, stream))
+    dev = _device("w_gate", io.tensors["w_gate"])
+    io.check(shape, dev)
+    _run("moe_expert_ffn_i8", dev, stream, ctypes.byref(shape), ctypes.byref(io.c),
+         _scratch(ws, moe_expert_ffn_i8_workspace_bytes(shape), dev))
 
 
 # ---- norms around a block
@@ -332,42 +340,19 @@ def make_norm_shape(T_, d_model, dtype, eps=1e-6, res_scale=1.0, rows_per_gate=N
                         eps, res_scale)
 
 
-def _norm_arrays(s, matrices, vectors, gates):
-    """Checks the arrays of a norm call; (moe_rows by name, device)."""
-    given = [t for t in (*matrices.values(), *vectors.values(), *gates.values()) if t is not None]
-    if not given:
-        raise ValueError("no tensors")
-    dev, dt = given[0].device, _DTYPE.get(s.dtype)
-    rows = {}
-    for n, t in matrices.items():
-        ld = 0
-        if t is not None and dt is not None:
-            ld = _matrix(n, t, dt, s.T, s.d_model, dev)
-        rows[n] = MoeRows(B._p(t), ld)
-    n_gates = -(-s.T // s.rows_per_gate) if s.rows_per_gate > 0 else 0
-    for group, count in ((vectors, 1), (gates, n_gates)):
-        for n, t in group.items():
-            if t is not None and dt is not None:
-                _need(n, t, dt, count * s.d_model, dev)
-    return rows, dev
-
-
 def moe_norm_residual(shape: MoeNormShape, *, x=None, y=None, w_post=None, gate=None, w_pre=None, r=None, h=None,
                       q=None, q_scale=None, stream=None):
     """r = res_scale x + gate norm(y, w_post), h = norm(r, w_pre), and h's 8-bit
     codes q with q_scale; what is None falls out (see the header)."""
-    s = shape
-    rows, dev = _norm_arrays(s, dict(x=x, y=y, r=r, h=h), dict(w_post=w_post, w_pre=w_pre), dict(gate=gate))
-    if q is not None:
-        _need("q", q, torch.int8, s.T * s.d_model, dev)
-    if q_scale is not None:
-        _need("q_scale", q_scale, torch.float32, s.T, dev)
-    _apart([("r", r), ("h", h), ("q", q), ("q_scale", q_scale)],
-           [("x", x), ("y", y), ("w_post", w_post), ("gate", gate), ("w_pre", w_pre)], {("r", "x")})
-    io = MoeNormIO(rows["x"], rows["y"], B._p(w_post), B._p(gate), B._p(w_pre), rows["r"], rows["h"], B._p(q),
-                   B._p(q_scale))
-    B._check("moe_norm_residual", _on(dev, lambda st: lib().moe_norm_residual(
-        ctypes.byref(s), ctypes.byref(io), st), stream))
+    s, dev = shape, _device("x, y", x if y is None else y)
+    T_, d, dt = s.T, s.d_model, _DTYPE.get(s.dtype)
+    gates = -(-T_ // s.rows_per_gate) * d if gate is not None else 0
+    io = MoeNormIO(*_matrix("x", x, dt, T_, d, dev), *_matrix("y", y, dt, T_, d, dev),
+                   _opt("w_post", w_post, dt, d, dev), _opt("gate", gate, dt, gates, dev),
+                   _opt("w_pre", w_pre, dt, d, dev), *_matrix("r", r, dt, T_, d, dev),
+                   *_matrix("h", h, dt, T_, d, dev), _opt("q", q, torch.int8, T_ * d, dev),
+                   _opt("q_scale", q_scale, torch.float32, T_, dev))
+    _run("moe_norm_residual", dev, stream, ctypes.byref(s), ctypes.byref(io))
 
 
 def moe_norm_residual_backward_workspace_bytes(shape: MoeNormShape) -> int:
@@ -379,18 +364,15 @@ def moe_norm_residual_backward(shape: MoeNormShape, ws, *, r=None, y=None, w_pos
                                accumulate=False, stream=None):
     """Gradients of moe_norm_residual from dr and dh, the gradients at r and h;
     r, y and the vectors as the forward pass left and had them."""
-    s = shape
-    rows, dev = _norm_arrays(s, dict(r=r, y=y, dr=dr, dh=dh, dx=dx, dy=dy),
-                             dict(w_post=w_post, w_pre=w_pre, dw_post=dw_post, dw_pre=dw_pre),
-                             dict(gate=gate, dgate=dgate))
-    _apart([("dx", dx), ("dy", dy), ("dgate", dgate), ("dw_post", dw_post), ("dw_pre", dw_pre)],
-           [("r", r), ("y", y), ("w_post", w_post), ("gate", gate), ("w_pre", w_pre), ("dr", dr), ("dh", dh)],
-           {(o, i) for o in ("dx", "dy") for i in ("r", "y", "dr", "dh")})
-    io = MoeNormGradIO(rows["r"], rows["y"], B._p(w_post), B._p(gate), B._p(w_pre), rows["dr"], rows["dh"],
-                       rows["dx"], rows["dy"], B._p(dgate), B._p(dw_post), B._p(dw_pre), int(bool(accumulate)), 0)
-
-    def call(st):
-        _workspace(ws, moe_norm_residual_backward_workspace_bytes(s), dev)
-        return lib().moe_norm_residual_backward(ctypes.byref(s), ctypes.byref(io), B._p(ws), st)
-
-    B._check("moe_norm_residual_backward", _on(dev, call, stream))
+    s, dev = shape, _device("ws", ws)
+    T_, d, dt = s.T, s.d_model, _DTYPE.get(s.dtype)
+    gates = -(-T_ // s.rows_per_gate) * d if gate is not None else 0
+    io = MoeNormGradIO(*_matrix("r", r, dt, T_, d, dev), *_matrix("y", y, dt, T_, d, dev),
+                       _opt("w_post", w_post, dt, d, dev), _opt("gate", gate, dt, gates, dev),
+                       _opt("w_pre", w_pre, dt, d, dev), *_matrix("dr", dr, dt, T_, d, dev),
+                       *_matrix("dh", dh, dt, T_, d, dev), *_matrix("dx", dx, dt, T_, d, dev),
+                       *_matrix("dy", dy, dt, T_, d, dev), _opt("dgate", dgate, dt, gates, dev),
+                       _opt("dw_post", dw_post, dt, d, dev), _opt("dw_pre", dw_pre, dt, d, dev),
+                       int(bool(accumulate)), 0)
+    _run("moe_norm_residual_backward", dev, stream, ctypes.byref(s), ctypes.byref(io),
+         _scratch(ws, _on(dev, moe_norm_residual_backward_workspace_bytes, s), dev))

@@ -77,6 +77,7 @@ struct I8Args {
   const int32_t* offsets;  // may be null with one group
   int64_t lda, ldo;
   int ngroups, M, N, K;
+  int rows;                // about as many of the M are in use
   int nsplit;              // ranges of the reduction, their sums in `part`
   int32_t* part;           // [nsplit, M, N]
 };

@@ -18,6 +18,39 @@ static bool al4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 static size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 static int elem_size(int dtype) { return dtype == MOE_BF16 ? 2 : 4; }
 
+// The arrays of a call.  A written one must not overlap any other, but for
+// pairs that may be one and the same memory: rows of the same kind at the same
+// start and stride, each element read before it is written, by one thread.
+struct Arrays {
+  struct Span {
+    uintptr_t from, to;
+    int64_t ld;
+    bool written, may_alias;
+  };
+  Span s[16];
+  int n = 0;
+  void add(const void* p, size_t bytes, bool written, int64_t ld = 0, bool may_alias = false) {
+    if (p == nullptr || bytes == 0) return;
+    s[n++] = Span{(uintptr_t)p, (uintptr_t)p + bytes, ld, written, may_alias};
+  }
+  void rows(const moe_rows& r, int M, int width, int size, bool written, bool may_alias) {
+    if (M > 0) add(r.p, ((size_t)(M - 1) * r.ld + width) * size, written, r.ld, may_alias);
+  }
+  int check() const {
+    for (int i = 0; i < n; ++i)
+      for (int j = 0; j < i; ++j) {
+        if (!s[i].written && !s[j].written) continue;
+        if (s[i].from >= s[j].to || s[j].from >= s[i].to) continue;
+        // an output in an input's place
+        if (s[i].written != s[j].written && s[i].may_alias && s[j].may_alias &&
+            s[i].from == s[j].from && s[i].ld == s[j].ld)
+          continue;
+        return MOE_EINVAL;
+      }
+    return MOE_OK;
+  }
+};
+
 static int check_select(const moe_shape* s, const moe_select_params* p) {
   const int rc = check_shape(s);
   if (rc) return rc;
@@ -166,6 +199,13 @@ int moe_select(const moe_shape* s, const moe_select_params* p, const float* logi
   if (rc) return rc;
   if (!logits || !topk_idx || !topk_gate || ld_logits < s->n_ffn + s->n_zero) return MOE_EINVAL;
   if (!al4(logits) || !al4(bias) || !al4(topk_idx) || !al4(topk_gate)) return MOE_EALIGN;
+  const size_t T = s->T, E = (size_t)s->n_ffn + s->n_zero;
+  Arrays v;
+  v.add(logits, ((T - 1) * ld_logits + E) * 4, false);
+  v.add(bias, E * 4, false);
+  v.add(topk_idx, T * s->top_k * 4, true);
+  v.add(topk_gate, T * s->top_k * 4, true);
+  if (const int bad = v.check()) return bad;
   return run_select(s, p, logits, ld_logits, bias, topk_idx, topk_gate, (hipStream_t)stream);
 }
 
@@ -179,6 +219,17 @@ int moe_route_select(const moe_shape* s, const moe_select_params* p, const void*
   if (!al16(x) || !al16(w_router) || !al16(ws) || !al4(logit_bias) || !al4(bias) ||
       !al4(topk_idx) || !al4(topk_gate) || !al4(logits_out))
     return MOE_EALIGN;
+  const size_t T = s->T, E = (size_t)s->n_ffn + s->n_zero, d = s->d_model, es = elem_size(s->dtype);
+  Arrays v;
+  v.add(x, T * d * es, false);
+  v.add(w_router, E * d * es, false);
+  v.add(logit_bias, E * 4, false);
+  v.add(bias, E * 4, false);
+  v.add(topk_idx, T * s->top_k * 4, true);
+  v.add(topk_gate, T * s->top_k * 4, true);
+  v.add(logits_out, T * E * 4, true);
+  v.add(ws, moe_workspace_bytes(s), true);
+  if ((rc = v.check())) return rc;
   if ((rc = run_router_logits(s, x, w_router, logit_bias, logits_out, ws, (hipStream_t)stream)))
     return rc;
   return run_select(s, p, logits_out, s->n_ffn + s->n_zero, bias, topk_idx, topk_gate,
@@ -193,6 +244,13 @@ int moe_select_backward(const moe_shape* s, const moe_select_params* p, const fl
   if (!logits || !topk_idx || !dgate || !dlogits || ld_logits < s->n_ffn + s->n_zero)
     return MOE_EINVAL;
   if (!al4(logits) || !al4(topk_idx) || !al4(dgate) || !al4(dlogits)) return MOE_EALIGN;
+  const size_t T = s->T, E = (size_t)s->n_ffn + s->n_zero;
+  Arrays v;
+  v.add(logits, ((T - 1) * ld_logits + E) * 4, false);
+  v.add(topk_idx, T * s->top_k * 4, false);
+  v.add(dgate, T * s->top_k * 4, false);
+  v.add(dlogits, T * E * 4, true);
+  if (const int bad = v.check()) return bad;
   SelectBwdArgs a{};
   a.logits = logits;
   a.ld = ld_logits;
@@ -223,6 +281,11 @@ int moe_quantize_rows(const moe_quant_shape* s, const void* x, int8_t* q, float*
   if (rc) return rc;
   if (s->M > 0 && (!x || !q || !scale)) return MOE_EINVAL;
   if (!al16(x) || !al16(q) || !al4(scale)) return MOE_EALIGN;
+  Arrays v;
+  v.rows(moe_rows{(void*)x, s->ldx}, s->M, s->K, elem_size(s->dtype), false, false);
+  v.rows(moe_rows{(void*)q, s->ldq}, s->M, s->K, 1, true, false);
+  v.add(scale, (size_t)s->M * 4, true);
+  if (const int bad = v.check()) return bad;
   return launch_quantize(s->dtype, x, s->ldx, s->M, s->K, q, s->ldq, scale, nullptr,
                          (hipStream_t)stream);
 }
@@ -249,6 +312,15 @@ int moe_matmul_i8(const moe_i8_shape* s, const int32_t* offsets, const int8_t* a
   g.nsplit = i8_nsplit(s, cus);
   if (g.nsplit > 1 && !ws) return MOE_EINVAL;
   if (none) return MOE_OK;
+  Arrays v;
+  v.rows(moe_rows{(void*)a, s->lda}, s->M, s->K, 1, false, false);
+  v.add(a_scale, (size_t)s->M * 4, false);
+  v.add(w, (size_t)s->n_groups * s->N * s->K, false);
+  v.add(w_scale, (size_t)s->n_groups * s->N * 4, false);
+  v.add(offsets, ((size_t)s->n_groups + 1) * 4, false);
+  v.rows(moe_rows{c, s->ldc}, s->M, s->N, elem_size(s->out_dtype), true, false);
+  v.add(ws, i8_part_bytes(s, g.nsplit), true);
+  if (const int bad = v.check()) return bad;
   g.a = a;
   g.sa = a_scale;
   g.b = w;
@@ -258,7 +330,7 @@ int moe_matmul_i8(const moe_i8_shape* s, const int32_t* offsets, const int8_t* a
   g.lda = s->lda;
   g.ldo = s->ldc;
   g.ngroups = s->n_groups;
-  g.M = s->M;
+  g.M = g.rows = s->M;
   g.N = s->N;
   g.K = s->K;
   g.part = (int32_t*)ws;
@@ -282,6 +354,25 @@ int moe_expert_ffn_i8(const moe_shape* s, const moe_ffn_i8_io* io, void* ws, voi
     return MOE_EALIGN;
   hipStream_t st = (hipStream_t)stream;
   const FfnLayout w = ffn_layout(s);
+  {
+    const size_t T = s->T, rows = T * s->top_k, dd = s->d_model, es = elem_size(s->dtype);
+    const size_t up = (size_t)s->n_ffn * s->d_ff * dd, E = (size_t)s->n_ffn + s->n_zero;
+    Arrays v;
+    v.add(io->x, T * dd * es, false);
+    v.add(io->xq, T * dd, false);
+    v.add(io->x_scale, T * 4, false);
+    v.add(io->perm, rows * 4, false);
+    v.add(io->offsets, (E + 1) * 4, false);
+    v.add(io->w_gate, up, false);
+    v.add(io->w_up, up, false);
+    v.add(io->w_down, up, false);
+    v.add(io->s_gate, (size_t)s->n_ffn * s->d_ff * 4, false);
+    v.add(io->s_up, (size_t)s->n_ffn * s->d_ff * 4, false);
+    v.add(io->s_down, (size_t)s->n_ffn * dd * 4, false);
+    v.add(io->y_perm, rows * dd * es, true);
+    v.add(ws, w.total, true);
+    if ((rc = v.check())) return rc;
+  }
   char* base = (char*)ws;
   const int Tk = s->T * s->top_k, d = s->d_model, f = s->d_ff;
   const int8_t* xq = io->xq;
@@ -310,6 +401,8 @@ int moe_expert_ffn_i8(const moe_shape* s, const moe_ffn_i8_io* io, void* ws, voi
   g.ldo = f;
   g.ngroups = s->n_ffn;
   g.M = Tk;
+  // (as many fall on FFN experts where all are chosen alike)
+  g.rows = std::max(1, (int)((long)Tk * s->n_ffn / (s->n_ffn + s->n_zero)));
   g.N = f;
   g.K = d;
   g.nsplit = 1;
@@ -345,6 +438,19 @@ int moe_norm_residual(const moe_norm_shape* s, const moe_norm_io* io, void* stre
     return rc;
   if (!al16(io->w_post) || !al16(io->gate) || !al16(io->w_pre) || !al16(io->q) || !al4(io->q_scale))
     return MOE_EALIGN;
+  const int T = s->T, d = s->d_model, es = elem_size(s->dtype);
+  const size_t vec = (size_t)d * es, gates = ((size_t)T + s->rows_per_gate - 1) / s->rows_per_gate;
+  Arrays v;
+  v.rows(io->x, T, d, es, false, true);
+  v.rows(io->r, T, d, es, true, true);
+  v.rows(io->y, T, d, es, false, false);
+  v.rows(io->h, T, d, es, true, false);
+  v.add(io->w_post, vec, false);
+  v.add(io->gate, gates * vec, false);
+  v.add(io->w_pre, vec, false);
+  v.add(io->q, (size_t)T * d, true);
+  v.add(io->q_scale, (size_t)T * 4, true);
+  if ((rc = v.check())) return rc;
   return launch_norm(*s, *io, (hipStream_t)stream);
 }
 
@@ -376,6 +482,23 @@ int moe_norm_residual_backward(const moe_norm_shape* s, const moe_norm_grad_io* 
     return MOE_EALIGN;
   const int cus = device_cu_count();
   if (cus <= 0) return MOE_EHIP;
+  const int T = s->T, d = s->d_model, es = elem_size(s->dtype);
+  const size_t vec = (size_t)d * es, gates = ((size_t)T + s->rows_per_gate - 1) / s->rows_per_gate;
+  Arrays v;
+  v.rows(io->r, T, d, es, false, true);
+  v.rows(io->y, T, d, es, false, true);
+  v.rows(io->dr, T, d, es, false, true);
+  v.rows(io->dh, T, d, es, false, true);
+  v.rows(io->dx, T, d, es, true, true);
+  v.rows(io->dy, T, d, es, true, true);
+  v.add(io->w_post, vec, false);
+  v.add(io->gate, gates * vec, false);
+  v.add(io->w_pre, vec, false);
+  v.add(io->dgate, gates * vec, true);
+  v.add(io->dw_post, vec, true);
+  v.add(io->dw_pre, vec, true);
+  v.add(ws, norm_bwd_ws_bytes(*s, cus), true);
+  if ((rc = v.check())) return rc;
   return launch_norm_bwd(*s, *io, ws, cus, (hipStream_t)stream);
 }
 

@@ -4,11 +4,20 @@
 //
 // The 16x16x64 int8 MFMA takes 16 bytes a lane and operand and as many cycles as
 // the bf16 one over half the depth: a tile has the bytes of a bf16 tile and
-// twice its products, so geometry and pipeline are those of the bf16 products'
-// forward form (direct-to-LDS loads, swizzled slots, rings of stages with one
-// barrier a step, a persistent grid that works out the next tile and asks for
-// its first stages before this tile's stores).  Sums are whole numbers, exact
-// in 32 bits, and so do not depend on the split of a long reduction.
+// twice its products, so its geometry is that of the bf16 products' forward form
+// (direct-to-LDS loads, swizzled slots, rings of stages with one barrier a
+// step, a persistent grid that works out the next tile and asks for its first
+// stages before this tile's stores).  Sums are whole numbers, exact in 32 bits,
+// and so do not depend on the split of a long reduction.
+//
+// With half the bytes a weight and twice the rate, loads bound it up to some 250
+// rows a group, so every step issues the same number of loads and waits for
+// those that it needs only (load_a below).
+//
+// Measured for 16384 tokens, 12 of 512 + 256 experts, d_model 6144, d_ff 2048:
+// gate and up 3.7 ms (1.8 PFLOP/s), down 2.1 ms; 65536 tokens 10.9 and 6.6 ms
+// (2.4 and 2.0; a library product of 8192^3 2.1); 128 tokens 1.62 and 0.81 ms
+// (6.9 TB/s).
 
 #include <algorithm>
 #include <type_traits>
@@ -20,6 +29,7 @@
 namespace moe {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef f32x4_t f32x4_any_t __attribute__((aligned(4)));
 
 // silu(z) u; in 64 bits for an fp32 H.
 __device__ __forceinline__ float swiglu(float z, float u) {
@@ -38,11 +48,11 @@ __device__ __forceinline__ void i8_rows(const int32_t* offsets, int e, int M, in
 }
 
 // SW: with b2, the tile's first half of columns are gate's, the second up's.
-template <bool SW, typename TO, int BM, int BN, int WM, int WN, int SA, int SB>
+template <bool SW, typename TO, int BM, int BN, int WM, int WN, int SA, int SB, bool NT>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
 gmm_i8_kernel(I8Args g) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int NW = WM * WN, NT = 64 * NW, KS = 128;  // bytes a step
+  constexpr int NW = WM * WN, THREADS = 64 * NW, KS = 128;  // bytes a step
   using TA = Tile<false, BM, NW, KS / 2>;
   using TB = Tile<false, BN, NW, KS / 2>;
   constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
@@ -50,19 +60,18 @@ gmm_i8_kernel(I8Args g) {
   constexpr int HN = SW ? BN / 2 : BN;  // output columns per tile
   constexpr int MG = 4;
   constexpr int DA = SA - 1, DB = SB - 1;
-  static_assert(!SW || (NB % 2 == 0 && B_PW % 2 == 0), "tile");
+  static_assert(TA::NP == 1 && TB::NP == 1 && (!SW || (NB % 2 == 0 && BN % 32 == 0)), "tile");
   static_assert(TB::BYTES > kMfmaMaxGroups * 4, "the groups' prefix fits a stage");
-  static_assert(DA >= 1 && DB >= DA && SB <= 5 && SA * TA::BYTES + SB * TB::BYTES <= 160 * 1024, "LDS");
+  static_assert(DA >= 1 && DB >= DA && SA <= 4 && SB <= 4 && SA * TA::BYTES + SB * TB::BYTES <= 160 * 1024,
+                "LDS");
   __shared__ __attribute__((aligned(1024))) char s_a0[TA::BYTES];
   __shared__ __attribute__((aligned(1024))) char s_a1[TA::BYTES];
   __shared__ __attribute__((aligned(1024))) char s_a2[SA > 2 ? TA::BYTES : 16];
   __shared__ __attribute__((aligned(1024))) char s_a3[SA > 3 ? TA::BYTES : 16];
-  __shared__ __attribute__((aligned(1024))) char s_a4[SA > 4 ? TA::BYTES : 16];
   __shared__ __attribute__((aligned(1024))) char s_b0[TB::BYTES];
   __shared__ __attribute__((aligned(1024))) char s_b1[TB::BYTES];
   __shared__ __attribute__((aligned(1024))) char s_b2[SB > 2 ? TB::BYTES : 16];
   __shared__ __attribute__((aligned(1024))) char s_b3[SB > 3 ? TB::BYTES : 16];
-  __shared__ __attribute__((aligned(1024))) char s_b4[SB > 4 ? TB::BYTES : 16];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = uni(tid >> 6);
@@ -85,7 +94,7 @@ gmm_i8_kernel(I8Args g) {
   auto describe = [&](int k0) {
     int* s_pref = reinterpret_cast<int*>(s_b0);
     int* s_scan = reinterpret_cast<int*>(s_b1);
-    constexpr int PER = (kMfmaMaxGroups + NT - 1) / NT;
+    constexpr int PER = (kMfmaMaxGroups + THREADS - 1) / THREADS;
     // ascending offsets give at most this many row tiles; more are cut off
     // here and computed nowhere
     const int most = g.M / BM + g.ngroups;
@@ -100,7 +109,7 @@ gmm_i8_kernel(I8Args g) {
       }
       loc[k] = run;
     }
-    const int base = block_inclusive_scan<NT>(run, s_scan) - run;
+    const int base = block_inclusive_scan<THREADS>(run, s_scan) - run;
     if (tid == 0) s_pref[0] = 0;
 #pragma unroll
     for (int k = 0; k < PER; ++k)
@@ -128,17 +137,14 @@ gmm_i8_kernel(I8Args g) {
     int k_lo, k_hi, r_end;  // its steps, and the end of its reduction
     const char *a_base, *b_base, *b_base2;
     uint32_t a_bytes, b_bytes;
-    bool once;              // no other tile reads this tile's part of b
+    int once;               // no other tile reads this tile's part of b
   };
   const uint32_t lda = (uint32_t)g.lda, ldb = (uint32_t)g.K;
-  // lane offsets of the first load instructions of each kind
-  uint32_t a_off[TA::NP], b_off[TB::NP];
-#pragma unroll
-  for (int q = 0; q < TA::NP; ++q)
-    a_off[q] = (uint32_t)TA::row(q, wave, lane) * lda + TA::chunk(q, wave, lane) * 16;
-#pragma unroll
-  for (int q = 0; q < TB::NP; ++q)
-    b_off[q] = (uint32_t)TB::row(q, wave, lane) * ldb + TB::chunk(q, wave, lane) * 16;
+  // A load instruction brings RPI rows; a lane's place in them, and what chunk of
+  // its row it fetches, are the same for all of a wave's instructions.
+  const uint32_t chunk = (uint32_t)TA::chunk(0, wave, lane) * 16;
+  const uint32_t a_off = (uint32_t)(lane / (KS / 16)) * lda + chunk;
+  const uint32_t b_off = (uint32_t)(lane / (KS / 16)) * ldb + chunk;
 
   // Tile number k of this workgroup; false behind the last one.
   auto setup = [&](int k, Place& t) -> bool {
@@ -164,9 +170,9 @@ gmm_i8_kernel(I8Args g) {
     const int mg = max(1, min(MG, mt - m0));
     const int in = local - m0 * jt;
     t.j0 = uni((in / mg) * HN);
+    t.once = uni(mt == 1);
     const int h = ((t.rows + mt - 1) / mt + 15) & ~15;  // balanced height
     t.i0 = uni((m0 + in % mg) * h);
-    t.once = mt == 1;
     t.i_end = uni(min(t.rows, t.i0 + h));
     t.split = uni(t.split);
     const int steps = (g.K + KS - 1) / KS;
@@ -184,39 +190,44 @@ gmm_i8_kernel(I8Args g) {
 
   auto stage_a = [&](auto sc) -> char* {
     constexpr int N = decltype(sc)::value % SA;
-    return N == 0 ? s_a0 : N == 1 ? s_a1 : N == 2 ? s_a2 : N == 3 ? s_a3 : s_a4;
+    return N == 0 ? s_a0 : N == 1 ? s_a1 : N == 2 ? s_a2 : s_a3;
   };
   auto stage_b = [&](auto sc) -> char* {
     constexpr int N = decltype(sc)::value % SB;
-    return N == 0 ? s_b0 : N == 1 ? s_b1 : N == 2 ? s_b2 : N == 3 ? s_b3 : s_b4;
+    return N == 0 ? s_b0 : N == 1 ? s_b1 : N == 2 ? s_b2 : s_b3;
   };
-  // Load instruction q of step ks into a stage.  What its wave-uniform part
-  // adds to the lane offset goes through the scalar offset.
+  // Load instruction q of step ks into a stage; what its wave-uniform part adds
+  // to the lane offset goes through the scalar offset.  Steps behind the tile's
+  // last one load zeros, with no memory access: so every step has the same
+  // number of loads outstanding, and the compiler, which follows them through
+  // the control flow, adds no waits of its own (with loads left out at the end
+  // it had waited for all of them in every fourth step and more).
   auto load_a = [&](const Place& t, auto sc, int ks, int q) {
-    char* dst = stage_a(sc) + (wave + q * NW) * 1024;
-    const int add = (int)((uint32_t)(q - q % TA::NP) * (NW * TA::RPI) * lda);
-    const auto rs = descriptor(t.a_base, t.a_bytes);
+    const int i = wave + q * NW;
     const int left = t.r_end - ks * KS;
-    uint32_t off = a_off[q % TA::NP];
-    if (left < KS) off = TA::chunk(q, wave, lane) * 16 < left ? off : kOutside;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)off, ks * KS + add, 0, 0);
+    const auto rs = descriptor(t.a_base, left > 0 ? t.a_bytes : 0u);
+    uint32_t off = a_off;
+    if (left < KS) off = (int)chunk < left ? off : kOutside;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(stage_a(sc) + i * 1024), 16, (int)off,
+                                             ks * KS + i * TA::RPI * (int)lda, 0, 0);
   };
   auto load_b1 = [&](const Place& t, auto sc, int ks, int q, auto cache) {
     constexpr int AUX = decltype(cache)::value;
-    char* dst = stage_b(sc) + (wave + q * NW) * 1024;
+    const int i = wave + q * NW;
     // SwiGLU: gate rows fill the first half of the tile, up rows the second
-    const bool second = SW && q >= B_PW / 2;
-    const int h = second ? q - B_PW / 2 : q;
-    const int add = (int)((uint32_t)(h - h % TB::NP) * (NW * TB::RPI) * ldb);
-    const auto rs = descriptor(second ? t.b_base2 : t.b_base, t.b_bytes);
+    const bool second = SW && i * TB::RPI >= BN / 2;
+    const int r = i * TB::RPI - (second ? BN / 2 : 0);
     const int left = t.r_end - ks * KS;
-    uint32_t off = b_off[h % TB::NP];
-    if (left < KS) off = TB::chunk(q, wave, lane) * 16 < left ? off : kOutside;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, (int)off, ks * KS + add, 0, AUX);
+    const auto rs = descriptor(second ? t.b_base2 : t.b_base, left > 0 ? t.b_bytes : 0u);
+    uint32_t off = b_off;
+    if (left < KS) off = (int)chunk < left ? off : kOutside;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(stage_b(sc) + i * 1024), 16, (int)off,
+                                             ks * KS + r * (int)ldb, 0, AUX);
   };
-  // The step's b loads; weights that one tile reads are loaded non-temporally.
+  // The step's b loads.  NT: tiles for few rows load weights that no other tile
+  // reads non-temporally.
   auto load_b = [&](const Place& t, auto sc, int ks) {
-    if (t.once) {
+    if (NT && uni(t.once) != 0) {
 #pragma unroll
       for (int q = 0; q < B_PW; ++q) load_b1(t, sc, ks, q, std::integral_constant<int, kCpolNT>{});
     } else {
@@ -225,34 +236,34 @@ gmm_i8_kernel(I8Args g) {
     }
   };
 
-  constexpr int UNROLL = SA == SB ? SA : SA * SB;
+  constexpr int UNROLL = SB % SA == 0 ? SB : SA * SB;
+  static_assert(UNROLL <= 12, "code size");
   // A tile's first DA and DB steps, in the order in which the loop would
   // have asked for them.
   auto prologue = [&](const Place& t) {
     auto one = [&](auto vc) {  // what step V of -DB .. -1 would load
       constexpr int V = decltype(vc)::value - DB;
       if constexpr (V + DA >= 0) {
-        if (t.k_lo + V + DA < t.k_hi) {
 #pragma unroll
-          for (int q = 0; q < A_PW; ++q)
-            load_a(t, std::integral_constant<int, V + DA>{}, t.k_lo + V + DA, q);
-        }
+        for (int q = 0; q < A_PW; ++q)
+          load_a(t, std::integral_constant<int, V + DA>{}, t.k_lo + V + DA, q);
       }
-      if (t.k_lo + V + DB < t.k_hi)
-        load_b(t, std::integral_constant<int, V + DB>{}, t.k_lo + V + DB);
+      load_b(t, std::integral_constant<int, V + DB>{}, t.k_lo + V + DB);
     };
-    one(std::integral_constant<int, 0>{});
-    if constexpr (DB > 1) one(std::integral_constant<int, 1>{});
-    if constexpr (DB > 2) one(std::integral_constant<int, 2>{});
-    if constexpr (DB > 3) one(std::integral_constant<int, 3>{});
+    auto each = [&](auto self, auto vc) {
+      constexpr int V = decltype(vc)::value;
+      if constexpr (V < DB) {
+        one(vc);
+        self(self, std::integral_constant<int, V + 1>{});
+      }
+    };
+    each(each, std::integral_constant<int, 0>{});
   };
-  // Loads issued after the last one that a step with `behind` steps behind it
-  // needs.
-  auto later = [](int behind) constexpr {
-    const int na = behind < DA - 1 ? behind : DA - 1;
-    const int lo = DB == DA ? 1 : DB - DA, hi = behind < DB - 1 ? behind : DB - 1;
-    return na * A_PW + (hi >= lo ? hi - lo + 1 : 0) * B_PW;
-  };
+  // Loads issued after the last one that a step needs: a's of the next DA - 1
+  // steps, and b's from (DB - DA) steps ahead on (with equal leads, b's own is
+  // needed).
+  constexpr int LATER = (DA - 1) * A_PW + (DB == DA ? DB - 1 : DA) * B_PW;
+  static_assert(LATER < 64, "vmcnt");
 
   describe(0);
   Place t, next;
@@ -273,11 +284,7 @@ gmm_i8_kernel(I8Args g) {
       constexpr int MBA = decltype(mbac)::value, N = decltype(nc)::value;
       const char* sa = stage_a(nc);
       const char* sb = stage_b(nc);
-      const int behind = t.k_hi - 1 - ks;
-      if (DB == 1 || behind >= DB - 1) wait_vm<later(DB - 1)>();
-      else if (DB > 3 && behind == 2) wait_vm<later(DB > 3 ? 2 : 0)>();
-      else if (DB > 2 && behind == 1) wait_vm<later(DB > 2 ? 1 : 0)>();
-      else wait_vm<later(0)>();
+      wait_vm<LATER>();
       barrier_all();
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -291,11 +298,11 @@ gmm_i8_kernel(I8Args g) {
           fb[j] = __builtin_bit_cast(
               i32x4_t, TB::frag(sb, b_lane, SW && j >= NB / 2 ? BN / 32 + j - NB / 2 : j, kk));
         // into the stages that every wave has left at this step's barrier
-        if (kk == 0 && behind >= DA) {
+        if (kk == 0) {
 #pragma unroll
           for (int q = 0; q < A_PW; ++q) load_a(t, std::integral_constant<int, N + DA>{}, ks + DA, q);
         }
-        if (kk == 1 && behind >= DB) load_b(t, std::integral_constant<int, N + DB>{}, ks + DB);
+        if (kk == 1) load_b(t, std::integral_constant<int, N + DB>{}, ks + DB);
 #pragma unroll
         for (int i = 0; i < MBA; ++i)
 #pragma unroll
@@ -307,27 +314,15 @@ gmm_i8_kernel(I8Args g) {
     };
 
     auto loop = [&](auto mbac) {
-      for (int ks = t.k_lo; ks < t.k_hi; ks += UNROLL) {
-        step(mbac, std::integral_constant<int, 0>{}, ks);
-        if (ks + 1 >= t.k_hi) break;
-        step(mbac, std::integral_constant<int, 1>{}, ks + 1);
-        if constexpr (UNROLL > 2) {
-          if (ks + 2 >= t.k_hi) break;
-          step(mbac, std::integral_constant<int, 2>{}, ks + 2);
-        }
-        if constexpr (UNROLL > 3) {
-          if (ks + 3 >= t.k_hi) break;
-          step(mbac, std::integral_constant<int, 3>{}, ks + 3);
-        }
-        if constexpr (UNROLL > 4) {
-          if (ks + 4 >= t.k_hi) break;
-          step(mbac, std::integral_constant<int, 4>{}, ks + 4);
-        }
-        if constexpr (UNROLL > 5) {
-          if (ks + 5 >= t.k_hi) break;
-          step(mbac, std::integral_constant<int, 5>{}, ks + 5);
-        }
-      }
+      auto steps = [&](auto self, auto nc, int ks) -> bool {
+        constexpr int N = decltype(nc)::value;
+        step(mbac, nc, ks);
+        if (ks + 1 >= t.k_hi) return false;
+        if constexpr (N + 1 < UNROLL) return self(self, std::integral_constant<int, N + 1>{}, ks + 1);
+        else return true;
+      };
+      for (int ks = t.k_lo; ks < t.k_hi; ks += UNROLL)
+        if (!steps(steps, std::integral_constant<int, 0>{}, ks)) break;
     };
     if constexpr (MB == 1) {
       loop(std::integral_constant<int, MB>{});
@@ -335,11 +330,14 @@ gmm_i8_kernel(I8Args g) {
       // row blocks of this wave that hold rows (a wave without any still
       // loads and waits with the others, on one block that is not stored)
       const int nrb = (t.i_end - t.i0 + 15) / 16;
-      const int mba = min(MB, (nrb - wm + WM - 1) / WM);
-      if (mba >= 4 && MB >= 4) loop(std::integral_constant<int, MB >= 4 ? 4 : MB>{});
-      else if (mba == 3 && MB >= 3) loop(std::integral_constant<int, MB >= 3 ? 3 : MB>{});
-      else if (mba == 2) loop(std::integral_constant<int, 2>{});
-      else loop(std::integral_constant<int, 1>{});
+      const int mba = max(1, min(MB, (nrb - wm + WM - 1) / WM));
+      auto pick = [&](auto self, auto nc) {
+        constexpr int N = decltype(nc)::value;
+        if constexpr (N == 1) loop(nc);
+        else if (mba == N) loop(nc);
+        else self(self, std::integral_constant<int, N - 1>{});
+      };
+      pick(pick, std::integral_constant<int, MB>{});
     }
 
     // ---- out.  b was the MFMA's row operand: lane (l16, l4) holds columns
@@ -359,16 +357,14 @@ gmm_i8_kernel(I8Args g) {
       const float* col2 = SW ? g.sb2 + (int64_t)t.e * J : nullptr;
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
-        const int jj = jw + j * 16 + l4 * 4;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          sb[j][v] = col[min(jj + v, J - 1)];
-          if constexpr (SW) sb2[j][v] = col2[min(jj + v, J - 1)];
-        }
+        const int jj = min(jw + j * 16 + l4 * 4, J - 4);  // (J is a multiple of 4)
+        sb[j] = *reinterpret_cast<const f32x4_any_t*>(col + jj);
+        if constexpr (SW) sb2[j] = *reinterpret_cast<const f32x4_any_t*>(col2 + jj);
       }
     }
     // the next tile's first loads, before this one's stores: every wave is done
-    // with the stages, and no load of theirs is outstanding
+    // with the stages, and what they load has landed
+    wait_vm<0>();
     if (early) {
       barrier_all();
       if (have) prologue(next);
@@ -448,11 +444,11 @@ MOE_CHECK_ACCESSOR(check_word_gmm_i8)
 
 bool i8_mfma_ok(int N, int K, int64_t lda, int64_t ldo) {
   // 16-byte rows; a lane stores 4 neighbouring columns; a descriptor spans at
-  // most 256 rows
+  // most 320 rows
   return K % 16 == 0 && lda % 16 == 0 && lda <= (1 << 20) && N % 4 == 0 && ldo % 4 == 0 && ldo <= (1 << 20);
 }
 
-template <bool SW, typename TO, int BM, int BN, int WM, int WN, int SA, int SB>
+template <bool SW, typename TO, int BM, int BN, int WM, int WN, int SA, int SB, bool NT>
 static int launch_tile(const I8Args& g, hipStream_t st) {
   const int cus = stream_cu_count(st);
   if (cus <= 0) return MOE_EHIP;
@@ -463,20 +459,43 @@ static int launch_tile(const I8Args& g, hipStream_t st) {
   if (grid > most) grid = most;
   if (grid > 8) grid -= grid % 8;
   if (grid < 1) return MOE_OK;
-  hipLaunchKernelGGL((gmm_i8_kernel<SW, TO, BM, BN, WM, WN, SA, SB>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((gmm_i8_kernel<SW, TO, BM, BN, WM, WN, SA, SB, NT>), dim3((unsigned)grid),
                      dim3(64 * WM * WN), 0, st, g);
   return check_launch();
 }
 
+// Tile choice by the rows that a group has on average (`rows`; measured over 512
+// groups of W [2 x 2048, 6144] with SwiGLU, 12.9 GB of weights, ragged groups,
+// us):
+//   rows       8    32    64    96   128   192   224   256   288   512
+//   64x256  1915  2223  2723  3321  3696
+//   128x256 2123  2188  2391  2533  3034  3598
+//   256x256 2209  2247  2467  2563  2676  3013  3217  3840  4367  6433
+//   320x192             2666        3133  3317  3471  3718  3926  6494
+// Weights that come once from HBM bound all of them at first (1915: 6.7 TB/s),
+// so what counts is how far ahead they are asked for; a second row tile in a
+// group loads them again from L2, which 320 rows avoid for groups just over
+// 256.  Where a tile shape leaves CUs idle, smaller ones: the same products with
+// 128 x 128 and 64 x 128 tiles, two workgroups on a CU.
 template <bool SW, typename TO>
 static int launch_any(const I8Args& g, hipStream_t st) {
   const int cus = stream_cu_count(st);
   if (cus <= 0) return MOE_EHIP;
-  const long per = g.M / g.ngroups;
-  const long t256 = (long)(g.M / 256 + std::min(g.M, g.ngroups)) * ((g.N + (SW ? 127 : 255)) / (SW ? 128 : 256)) * g.nsplit;
-  if (per >= 128 && t256 >= cus) return launch_tile<SW, TO, 256, 256, 4, 2, 2, 3>(g, st);
-  if (per < 64) return launch_tile<SW, TO, 64, 128, 1, 4, 3, 3>(g, st);
-  return launch_tile<SW, TO, 128, 128, 2, 2, 2, 3>(g, st);
+  const long per = g.rows / g.ngroups;
+  auto tiles = [&](int bm, int bn) {
+    const int hn = SW ? bn / 2 : bn;
+    return (long)(g.rows / bm + std::min(g.rows, g.ngroups)) * ((g.N + hn - 1) / hn) * g.nsplit;
+  };
+  if (per >= 250 && per < 305 && tiles(320, 192) >= cus)
+    return launch_tile<SW, TO, 320, 192, 4, 2, 2, 3, false>(g, st);
+  if (per >= 112 && tiles(256, 256) >= cus) return launch_tile<SW, TO, 256, 256, 4, 2, 2, 3, false>(g, st);
+  if (per >= 24) {
+    if (tiles(128, 256) >= cus) return launch_tile<SW, TO, 128, 256, 2, 4, 3, 3, false>(g, st);
+    if (per >= 64) return launch_tile<SW, TO, 128, 128, 2, 2, 2, 3, false>(g, st);
+  } else if (tiles(64, 256) >= cus) {
+    return launch_tile<SW, TO, 64, 256, 1, 8, 4, 4, true>(g, st);
+  }
+  return launch_tile<SW, TO, 64, 128, 1, 4, 3, 3, true>(g, st);
 }
 
 int launch_i8_mfma(int out_dtype, const I8Args& g, hipStream_t st) {

@@ -34,12 +34,12 @@ struct NormArgs {
 };
 
 // N chunks a thread; ALONE: one wave per row.
-template <typename T, int N, bool ALONE>
-__global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
-  __shared__ uint32_t s[32];
+template <typename T, int N, bool ALONE, int NT, bool WHOLE>
+__global__ void __launch_bounds__(NT) norm_kernel(NormArgs a) {
+  __shared__ uint32_t s[96];
   int turn = 0;
-  const int tid = ALONE ? lane_id() : threadIdx.x, nt = ALONE ? kWave : blockDim.x;
-  const int per = ALONE ? blockDim.x >> 6 : 1;
+  const int tid = ALONE ? lane_id() : threadIdx.x, nt = ALONE ? kWave : NT;
+  const int per = ALONE ? NT / kWave : 1;
   const int step = gridDim.x * per;
   const int d = a.d;
   const float over = 1.f / (float)d;
@@ -50,25 +50,25 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
   auto load = [&](int row) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (y != nullptr) ry[i] = load_chunk(y + row * a.ldy, tid + i * nt, d);
-      if (x != nullptr) rx[i] = load_chunk(x + row * a.ldx, tid + i * nt, d);
+      if (y != nullptr) ry[i] = load_chunk<WHOLE>(y + row * a.ldy, tid + i * nt, d);
+      if (x != nullptr) rx[i] = load_chunk<WHOLE>(x + row * a.ldx, tid + i * nt, d);
     }
   };
   load(t);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    if (a.w_post != nullptr) wp[i] = load_chunk((const T*)a.w_post, tid + i * nt, d);
-    if (a.w_pre != nullptr) wn[i] = load_chunk((const T*)a.w_pre, tid + i * nt, d);
+    if (a.w_post != nullptr) wp[i] = load_chunk<WHOLE>((const T*)a.w_post, tid + i * nt, d);
+    if (a.w_pre != nullptr) wn[i] = load_chunk<WHOLE>((const T*)a.w_pre, tid + i * nt, d);
   }
   for (; t < a.T; t += step) {
     Raw<T> rg[N], out[N];
     if (gate != nullptr) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        rg[i] = load_chunk(gate + (size_t)(t / a.per_gate) * d, tid + i * nt, d);
+        rg[i] = load_chunk<WHOLE>(gate + (size_t)(t / a.per_gate) * d, tid + i * nt, d);
     }
     float inv = 1.f;
-    if (y != nullptr && a.w_post != nullptr) {
+    if (a.w_post != nullptr) {
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) sum += f[k] * f[k];
       }
-      sum = row_sum(sum, ALONE, s, turn);
+      sum = row_sum<ALONE, NT>(sum, s, turn);
       inv = 1.f / sqrtf(sum * over + a.eps);
     }
     float sum = 0.f;
@@ -115,10 +115,10 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
     if (a.r != nullptr) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if ((tid + i * nt) * kChunk < d) store_chunk((T*)a.r + t * a.ldr, tid + i * nt, d, out[i]);
+        if ((tid + i * nt) * kChunk < d) store_chunk<WHOLE>((T*)a.r + t * a.ldr, tid + i * nt, d, out[i]);
     }
     if (a.w_pre != nullptr) {
-      sum = row_sum(sum, ALONE, s, turn);
+      sum = row_sum<ALONE, NT>(sum, s, turn);
       inv = 1.f / sqrtf(sum * over + a.eps);
       uint32_t top = 0;
 #pragma unroll
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
         for (int k = 0; k < 8; ++k) v[k] = v[k] * inv * f[k];
         out[i] = raw_of(v, (T*)nullptr);
         if (a.h != nullptr && (tid + i * nt) * kChunk < d)
-          store_chunk((T*)a.h + t * a.ldh, tid + i * nt, d, out[i]);
+          store_chunk<WHOLE>((T*)a.h + t * a.ldh, tid + i * nt, d, out[i]);
         if (a.q != nullptr) {
           floats(out[i], v);
 #pragma unroll
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
         }
       }
       if (a.q != nullptr) {
-        top = row_max(top, ALONE, s, turn);
+        top = row_max<ALONE, NT>(top, s, turn);
         const float scale = code_scale(top);
         if (tid == 0) a.q_scale[t] = scale;
 #pragma unroll
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
   }
 }
 
-template <typename T>
+template <typename T, bool WHOLE>
 static int launch_norm_t(const NormArgs& a, hipStream_t st) {
   const int cus = stream_cu_count(st);
   if (cus <= 0) return MOE_EHIP;
@@ -162,7 +162,7 @@ static int launch_norm_t(const NormArgs& a, hipStream_t st) {
   do {                                                                                          \
     const int per = ALONE ? NT / 64 : 1;                                                        \
     const long blocks = std::min<long>(((long)a.T + per - 1) / per, (long)cus * (2048 / NT));   \
-    hipLaunchKernelGGL((norm_kernel<T, N, ALONE>), dim3((unsigned)blocks), dim3(NT), 0, st, a); \
+    hipLaunchKernelGGL((norm_kernel<T, N, ALONE, NT, WHOLE>), dim3((unsigned)blocks), dim3(NT), 0, st, a); \
   } while (0)
   if (chunks <= 64) MOE_NORM(1, true, 256);
   else if (chunks <= 128) MOE_NORM(2, true, 256);
@@ -197,7 +197,10 @@ int launch_norm(const moe_norm_shape& s, const moe_norm_io& io, hipStream_t st) 
   a.T = s.T;
   a.d = s.d_model;
   a.per_gate = s.rows_per_gate;
-  return s.dtype == MOE_BF16 ? launch_norm_t<__bf16>(a, st) : launch_norm_t<float>(a, st);
+  const bool whole = s.d_model % kChunk == 0;
+  if (s.dtype == MOE_BF16)
+    return whole ? launch_norm_t<__bf16, true>(a, st) : launch_norm_t<__bf16, false>(a, st);
+  return whole ? launch_norm_t<float, true>(a, st) : launch_norm_t<float, false>(a, st);
 }
 
 // ---- backward
@@ -212,12 +215,12 @@ struct NormBwdArgs {
   int accumulate;
 };
 
-template <typename T, int N, bool ALONE>
-__global__ void __launch_bounds__(1024) norm_bwd_kernel(NormBwdArgs a) {
-  __shared__ uint32_t s[32];
+template <typename T, int N, bool ALONE, int NT, bool WHOLE>
+__global__ void __launch_bounds__(NT, N == 1 && NT <= 512 ? 4 : 1) norm_bwd_kernel(NormBwdArgs a) {
+  __shared__ uint32_t s[96];
   int turn = 0;
-  const int tid = ALONE ? lane_id() : threadIdx.x, nt = ALONE ? kWave : blockDim.x;
-  const int group = ALONE ? (int)(blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6)) : (int)blockIdx.x;
+  const int tid = ALONE ? lane_id() : threadIdx.x, nt = ALONE ? kWave : NT;
+  const int group = ALONE ? (int)(blockIdx.x * (NT / kWave) + (threadIdx.x >> 6)) : (int)blockIdx.x;
   if (group >= a.groups) return;
   const int lo = group * a.rows, hi = min(a.T, lo + a.rows);
   const int d = a.d;
@@ -238,25 +241,25 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(NormBwdArgs a) {
     for (int i = 0; i < N; ++i) {
       const int c = tid + i * nt;
       if (pre) {
-        rr[i] = load_chunk((const T*)a.r + row * a.ldr, c, d);
-        rdh[i] = load_chunk((const T*)a.dh + row * a.lddh, c, d);
+        rr[i] = load_chunk<WHOLE>((const T*)a.r + row * a.ldr, c, d);
+        rdh[i] = load_chunk<WHOLE>((const T*)a.dh + row * a.lddh, c, d);
       }
-      if (y != nullptr) ry[i] = load_chunk(y + row * a.ldy, c, d);
-      if (a.dr != nullptr) rdr[i] = load_chunk((const T*)a.dr + row * a.lddr, c, d);
+      if (y != nullptr) ry[i] = load_chunk<WHOLE>(y + row * a.ldy, c, d);
+      if (a.dr != nullptr) rdr[i] = load_chunk<WHOLE>((const T*)a.dr + row * a.lddr, c, d);
     }
   };
   if (lo < hi) load(lo);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    if (post) wp[i] = load_chunk((const T*)a.w_post, tid + i * nt, d);
-    if (pre) wn[i] = load_chunk((const T*)a.w_pre, tid + i * nt, d);
+    if (post) wp[i] = load_chunk<WHOLE>((const T*)a.w_post, tid + i * nt, d);
+    if (pre) wn[i] = load_chunk<WHOLE>((const T*)a.w_pre, tid + i * nt, d);
   }
   for (int t = lo; t < hi; ++t) {
     Raw<T> rg[N];
     if (gate != nullptr) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        rg[i] = load_chunk(gate + (size_t)(t / a.per_gate) * d, tid + i * nt, d);
+        rg[i] = load_chunk<WHOLE>(gate + (size_t)(t / a.per_gate) * d, tid + i * nt, d);
     }
     // g, the gradient at r
     float g[N][8];
@@ -275,22 +278,21 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(NormBwdArgs a) {
           dot += h[k] * w[k] * r[k];
         }
       }
-      if (y != nullptr && post) {
+      if (post) {
         float v[8];
         floats(ry[i], v);
 #pragma unroll
         for (int k = 0; k < 8; ++k) sy += v[k] * v[k];
       }
     }
-    if (pre) {
-      sq = row_sum(sq, ALONE, s, turn);
-      dot = row_sum(dot, ALONE, s, turn);
-      inv_r = 1.f / sqrtf(sq * over + a.eps);
-      mean_r = dot * over * inv_r * inv_r;
-    }
-    if (y != nullptr && post) {
-      sy = row_sum(sy, ALONE, s, turn);
-      inv_y = 1.f / sqrtf(sy * over + a.eps);
+    if (pre || post) {
+      float three[3] = {sq, dot, sy};
+      row_sums<ALONE, NT, 3>(three, s, turn);
+      if (pre) {
+        inv_r = 1.f / sqrtf(three[0] * over + a.eps);
+        mean_r = three[1] * over * inv_r * inv_r;
+      }
+      if (post) inv_y = 1.f / sqrtf(three[2] * over + a.eps);
     }
     float cn = 0.f;
 #pragma unroll
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(NormBwdArgs a) {
         float v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = a.res_scale * g[i][k];
-        store_chunk((T*)a.dx + t * a.lddx, tid + i * nt, d, raw_of(v, (T*)nullptr));
+        store_chunk<WHOLE>((T*)a.dx + t * a.lddx, tid + i * nt, d, raw_of(v, (T*)nullptr));
       }
       if (y != nullptr) {
         float v[8], w[8], q[8];
@@ -342,7 +344,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(NormBwdArgs a) {
     }
     if (y != nullptr) {
       float mean = 0.f;
-      if (post) mean = row_sum(cn, ALONE, s, turn) * over;
+      if (post) mean = row_sum<ALONE, NT>(cn, s, turn) * over;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         float v[8];
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(NormBwdArgs a) {
           for (int k = 0; k < 8; ++k) v[k] = g[i][k];
         }
         if ((tid + i * nt) * kChunk < d)
-          store_chunk((T*)a.dy + t * a.lddy, tid + i * nt, d, raw_of(v, (T*)nullptr));
+          store_chunk<WHOLE>((T*)a.dy + t * a.lddy, tid + i * nt, d, raw_of(v, (T*)nullptr));
       }
     }
     if (t + 1 < hi) load(t + 1);
@@ -373,12 +375,12 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(NormBwdArgs a) {
           if (c * kChunk >= d) continue;
           if (whole) {
             float v[8], old[8];
-            if (a.accumulate) floats(load_chunk((const T*)out, c, d), old);
+            if (a.accumulate) floats(load_chunk<WHOLE>((const T*)out, c, d), old);
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = a.accumulate ? old[k] + s_gate[i][k] : s_gate[i][k];
-            store_chunk(out, c, d, raw_of(v, (T*)nullptr));
+            store_chunk<WHOLE>(out, c, d, raw_of(v, (T*)nullptr));
           } else {
-            store_chunk(part, c, d, raw_of(s_gate[i], (float*)nullptr));
+            store_chunk<WHOLE>(part, c, d, raw_of(s_gate[i], (float*)nullptr));
           }
         }
         clear(s_gate);
@@ -390,13 +392,13 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(NormBwdArgs a) {
     const int c = tid + i * nt;
     if (c * kChunk >= d) continue;
     if (a.p_pre != nullptr)
-      store_chunk(a.p_pre + (size_t)group * d, c, d, raw_of(s_pre[i], (float*)nullptr));
+      store_chunk<WHOLE>(a.p_pre + (size_t)group * d, c, d, raw_of(s_pre[i], (float*)nullptr));
     if (a.p_post != nullptr)
-      store_chunk(a.p_post + (size_t)group * d, c, d, raw_of(s_post[i], (float*)nullptr));
+      store_chunk<WHOLE>(a.p_post + (size_t)group * d, c, d, raw_of(s_post[i], (float*)nullptr));
   }
 }
 
-// The groups' sums added up.  Workgroups of 64 columns by 4 ranges of the
+// The groups' sums added up.  Workgroups of 64 columns by 16 ranges of the
 // groups.  blockIdx.y: dw_pre, dw_post, then the gate rows that several groups
 // touch: gate row y, or, where there are more of them than groups, the one at
 // the end of group y.
@@ -408,8 +410,8 @@ struct NormSumArgs {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(256) norm_sum_kernel(NormSumArgs a) {
-  __shared__ float s[4][64];
+__global__ void __launch_bounds__(1024) norm_sum_kernel(NormSumArgs a) {
+  __shared__ float s[16][64];
   const int col = blockIdx.x * 64 + (threadIdx.x & 63), part = threadIdx.x >> 6;
   const float* from;
   T* out;
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(256) norm_sum_kernel(NormSumArgs a) {
   }
   if (out == nullptr) return;
   float sum = 0.f;
-  const int n = q1 - q0, each = (n + 3) / 4;
+  const int n = q1 - q0, each = (n + 15) / 16;
   const int lo = q0 + part * each, hi = std::min(q1, lo + each);
   if (col < a.d) {
     constexpr int U = 8;
@@ -463,18 +465,20 @@ __global__ void __launch_bounds__(256) norm_sum_kernel(NormSumArgs a) {
   s[part][threadIdx.x & 63] = sum;
   __syncthreads();
   if (part == 0 && col < a.d) {
-    sum = (s[0][threadIdx.x] + s[1][threadIdx.x]) + (s[2][threadIdx.x] + s[3][threadIdx.x]);
+    sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) sum += s[q][threadIdx.x];
     if (a.accumulate) sum += ElemOps<T>::to_f(out[col]);
     out[col] = ElemOps<T>::from_f(sum);
   }
 }
 
-// Row groups: as many as keep the chip busy, each of at least 8 rows, so that
-// the sums (8 bytes a column and vector, written and read) stay few beside the
-// rows (12 bytes a column in bf16).
+// Row groups: as many as keep the chip busy.  Their sums (8 bytes a column,
+// vector and group, written and read) are few beside the rows (12 bytes a
+// column in bf16) where there are many rows, and small where there are not.
 int norm_bwd_groups(int T, int d, int cus) {
-  const int most = d <= 1024 ? 16 * cus : d <= 4096 ? 2 * cus : cus;
-  return std::max(1, std::min(most, (T + 7) / 8));
+  const int most = d <= 512 ? 16 * cus : d <= 2048 ? 4 * cus : d <= 4096 ? 2 * cus : cus;
+  return std::max(1, std::min(most, T));
 }
 
 static size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -483,19 +487,21 @@ size_t norm_bwd_ws_bytes(const moe_norm_shape& s, int cus) {
   return 256 + 4 * up256((size_t)norm_bwd_groups(s.T, s.d_model, cus) * s.d_model * 4);
 }
 
-template <typename T>
+template <typename T, bool WHOLE>
 static int launch_norm_bwd_t(const NormBwdArgs& a, hipStream_t st) {
   const int chunks = (a.d + kChunk - 1) / kChunk;
 #define MOE_NORM_BWD(N, ALONE, NT)                                                                 \
   do {                                                                                             \
     const int per = ALONE ? NT / 64 : 1;                                                           \
-    hipLaunchKernelGGL((norm_bwd_kernel<T, N, ALONE>), dim3((unsigned)((a.groups + per - 1) / per)), \
-                       dim3(NT), 0, st, a);                                                        \
+    hipLaunchKernelGGL((norm_bwd_kernel<T, N, ALONE, NT, WHOLE>),                                        \
+                       dim3((unsigned)((a.groups + per - 1) / per)), dim3(NT), 0, st, a);                                                        \
   } while (0)
   if (chunks <= 64) MOE_NORM_BWD(1, true, 256);
-  else if (chunks <= 128) MOE_NORM_BWD(2, true, 256);
+  else if (chunks <= 128) MOE_NORM_BWD(1, false, 128);
   else if (chunks <= 256) MOE_NORM_BWD(1, false, 256);
-  else if (chunks <= 1024) MOE_NORM_BWD(1, false, (chunks + 63) / 64 * 64);
+  else if (chunks <= 512) MOE_NORM_BWD(1, false, 512);
+  else if (chunks <= 768) MOE_NORM_BWD(1, false, 768);
+  else if (chunks <= 1024) MOE_NORM_BWD(1, false, 1024);
   else if (chunks <= 2048) MOE_NORM_BWD(2, false, 1024);
   else MOE_NORM_BWD(4, false, 1024);
 #undef MOE_NORM_BWD
@@ -535,10 +541,15 @@ int launch_norm_bwd(const moe_norm_shape& s, const moe_norm_grad_io& io, void* w
   a.p_pre = io.dw_pre ? base : nullptr;
   a.p_post = io.dw_post ? base + each / 4 : nullptr;
   a.p_gate = base + each / 2;
-  int rc = MOE_OK;
-  if (s.T > 0 && (rc = s.dtype == MOE_BF16 ? launch_norm_bwd_t<__bf16>(a, st)
-                                           : launch_norm_bwd_t<float>(a, st)))
-    return rc;
+  if (s.T > 0) {
+    const bool whole = s.d_model % kChunk == 0;
+    int rc;
+    if (s.dtype == MOE_BF16)
+      rc = whole ? launch_norm_bwd_t<__bf16, true>(a, st) : launch_norm_bwd_t<__bf16, false>(a, st);
+    else
+      rc = whole ? launch_norm_bwd_t<float, true>(a, st) : launch_norm_bwd_t<float, false>(a, st);
+    if (rc) return rc;
+  }
   NormSumArgs b{};
   b.p_pre = a.p_pre;
   b.p_post = a.p_post;
@@ -559,9 +570,9 @@ int launch_norm_bwd(const moe_norm_shape& s, const moe_norm_grad_io& io, void* w
   if (!io.dw_pre && !io.dw_post && gates == 0) return MOE_OK;
   const dim3 grid((unsigned)((s.d_model + 63) / 64), (unsigned)(2 + gates));
   if (s.dtype == MOE_BF16)
-    hipLaunchKernelGGL(norm_sum_kernel<__bf16>, grid, dim3(256), 0, st, b);
+    hipLaunchKernelGGL(norm_sum_kernel<__bf16>, grid, dim3(1024), 0, st, b);
   else
-    hipLaunchKernelGGL(norm_sum_kernel<float>, grid, dim3(256), 0, st, b);
+    hipLaunchKernelGGL(norm_sum_kernel<float>, grid, dim3(1024), 0, st, b);
   return check_launch();
 }
 

@@ -15,14 +15,14 @@ namespace moe {
 
 // N chunks a thread, threads of one wave (ALONE) or of the workgroup; N = 0:
 // any number, read twice.
-template <typename T, int N, bool ALONE>
-__global__ void __launch_bounds__(1024)
+template <typename T, int N, bool ALONE, int NT>
+__global__ void __launch_bounds__(NT)
 quantize_kernel(const T* __restrict__ x, int64_t ldx, int M, int K, int8_t* __restrict__ q,
                 int64_t ldq, float* __restrict__ scale, const int32_t* __restrict__ used) {
-  __shared__ uint32_t s[32];
+  __shared__ uint32_t s[96];
   int turn = 0;
-  const int tid = ALONE ? lane_id() : threadIdx.x, nt = ALONE ? kWave : blockDim.x;
-  const int per = ALONE ? blockDim.x >> 6 : 1;
+  const int tid = ALONE ? lane_id() : threadIdx.x, nt = ALONE ? kWave : NT;
+  const int per = ALONE ? NT / kWave : 1;
   const int rows = used != nullptr ? min(max(used[0], 0), M) : M;
   for (int m = blockIdx.x * per + (ALONE ? (int)(threadIdx.x >> 6) : 0); m < rows; m += gridDim.x * per) {
     const T* row = x + m * ldx;
@@ -39,7 +39,7 @@ quantize_kernel(const T* __restrict__ x, int64_t ldx, int M, int K, int8_t* __re
 #pragma unroll
         for (int k = 0; k < 8; ++k) top = max(top, magnitude(f[k]));
       }
-      top = row_max(top, ALONE, s, turn);
+      top = row_max<ALONE, NT>(top, s, turn);
       const float sc = code_scale(top);
       if (tid == 0) scale[m] = sc;
 #pragma unroll
@@ -58,7 +58,7 @@ quantize_kernel(const T* __restrict__ x, int64_t ldx, int M, int K, int8_t* __re
 #pragma unroll
         for (int k = 0; k < 8; ++k) top = max(top, magnitude(f[k]));
       }
-      top = row_max(top, ALONE, s, turn);
+      top = row_max<ALONE, NT>(top, s, turn);
       const float sc = code_scale(top);
       if (tid == 0) scale[m] = sc;
       for (int c = tid; c * kChunk < K; c += nt) {
@@ -80,7 +80,7 @@ static int launch_quantize_t(const T* x, int64_t ldx, int M, int K, int8_t* q, i
   do {                                                                                            \
     const int per = ALONE ? NT / 64 : 1;                                                          \
     const long blocks = std::min<long>(((long)M + per - 1) / per, (long)cus * (8192 / NT));       \
-    hipLaunchKernelGGL((quantize_kernel<T, N, ALONE>), dim3((unsigned)blocks), dim3(NT), 0, st, x, \
+    hipLaunchKernelGGL((quantize_kernel<T, N, ALONE, NT>), dim3((unsigned)blocks), dim3(NT), 0, st, x, \
                        ldx, M, K, q, ldq, scale, used);                                           \
   } while (0)
   if (chunks <= 64) MOE_QUANT(1, true, 256);

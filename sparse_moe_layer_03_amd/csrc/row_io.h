@@ -5,6 +5,7 @@
 
 #include "../../include/moe.h"
 #include "common.h"
+#include "wave.h"
 
 namespace moe {
 
@@ -76,9 +77,11 @@ __device__ __forceinline__ Raw<T> load_raw(const T* p) {
 
 // Chunk c of a row of n values, zeros behind its end: the row's last chunk is
 // loaded from its last 8 values, and what it has too much in front dropped.
-template <typename T>
+// WHOLE: rows of whole chunks.
+template <bool WHOLE = false, typename T>
 __device__ __forceinline__ Raw<T> load_chunk(const T* row, int c, int n) {
   const int at = c * kChunk;
+  if (WHOLE) return at < n ? load_raw(row + at) : zero_raw<T>();
   if (at + kChunk <= n) return load_raw(row + at);
   if (at >= n) return zero_raw<T>();
   if (n >= kChunk) return drop(load_raw(row + n - kChunk), at + kChunk - n);
@@ -107,10 +110,11 @@ __device__ __forceinline__ Raw<float> raw_of(const float* f, float*) {
   return r;
 }
 
-template <typename T>
+// (c begins inside the row)
+template <bool WHOLE = false, typename T>
 __device__ __forceinline__ void store_chunk(T* row, int c, int n, const Raw<T>& r) {
   const int at = c * kChunk;
-  if (at + kChunk <= n) {
+  if (WHOLE || at + kChunk <= n) {
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T) / 2; ++i)
       *reinterpret_cast<u32x4_any_t*>((char*)(row + at) + 16 * i) = r.v[i];
@@ -168,29 +172,52 @@ __device__ __forceinline__ void store_codes(int8_t* row, int c, int n, u32x2_t v
 
 __device__ __forceinline__ uint32_t magnitude(float f) { return __float_as_uint(f) & 0x7fffffffu; }
 
-// ---- reductions over a row's threads: one wave, or the whole workgroup through
-// `s` (2 * 16 words, used alternately: a slot is written again only behind the
-// barrier of the other one)
+// ---- reductions over a row's threads: one wave (ALONE), or the NT threads of the
+// workgroup through `s` (2 * 3 * 16 words, its halves used in turn: a half is
+// written again only behind the barrier of the other one)
 
-template <typename V, typename OP>
-__device__ __forceinline__ V row_reduce(V v, bool alone, uint32_t* s, int& turn, OP op) {
+template <bool ALONE, int NT, int N, typename OP>
+__device__ __forceinline__ void row_reduce(uint32_t (&v)[N], uint32_t* s, int& turn, OP op) {
+  if constexpr (!ALONE) {
+    constexpr int W = NT / kWave;
+    uint32_t* at = s + (turn & 1) * 48;
+    ++turn;
+    if (lane_id() == 0) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = op(v, __shfl_xor(v, o, kWave));
-  if (alone) return v;
-  V* at = reinterpret_cast<V*>(s) + (turn & 1) * 16;
-  ++turn;
-  if (lane_id() == 0) at[threadIdx.x >> 6] = v;
-  __syncthreads();
-  const int waves = blockDim.x >> 6;
-  v = at[0];
-  for (int q = 1; q < waves; ++q) v = op(v, at[q]);
-  return v;
+      for (int k = 0; k < N; ++k) at[k * 16 + (threadIdx.x >> 6)] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      uint32_t r = at[k * 16];
+#pragma unroll
+      for (int q = 1; q < W; ++q) r = op(r, at[k * 16 + q]);
+      v[k] = r;
+    }
+  }
 }
-__device__ __forceinline__ float row_sum(float v, bool alone, uint32_t* s, int& turn) {
-  return row_reduce(v, alone, s, turn, [](float a, float b) { return a + b; });
+template <bool ALONE, int NT, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], uint32_t* s, int& turn) {
+  uint32_t u[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) u[k] = __float_as_uint(wave_sum_f(v[k]));
+  row_reduce<ALONE, NT, N>(u, s, turn, [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  });
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = __uint_as_float(u[k]);
 }
-__device__ __forceinline__ uint32_t row_max(uint32_t v, bool alone, uint32_t* s, int& turn) {
-  return row_reduce(v, alone, s, turn, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+template <bool ALONE, int NT>
+__device__ __forceinline__ float row_sum(float v, uint32_t* s, int& turn) {
+  float a[1] = {v};
+  row_sums<ALONE, NT, 1>(a, s, turn);
+  return a[0];
+}
+template <bool ALONE, int NT>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* s, int& turn) {
+  uint32_t a[1] = {wave_max_u(v)};
+  row_reduce<ALONE, NT, 1>(a, s, turn, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
+  return a[0];
 }
 
 }  // namespace moe

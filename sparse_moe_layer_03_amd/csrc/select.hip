@@ -6,21 +6,18 @@
 // groups: with G groups (rounded up to a power of two) lane l serves group
 // l / L, L = 64 / G, and holds its experts l % L, l % L + L, ... in registers.
 //
-// The top k.  Keys are mapped to integers of the same order.  The k-th largest
-// of the 64 lane maxima bounds the threshold from below (k keys reach it), so
-// few keys beyond the k wanted are left; the surplus is taken off from below,
-// one value a step.  (Building the threshold bit by bit from all keys takes 32
-// ballots for each of a lane's keys.)  It is the way left where the surplus is
-// large: few lanes in the kept groups, or keys in equal runs.
+// The top k.  Keys are mapped to integers of the same order, and a threshold is
+// built bit by bit until it parts k of them from the rest; of a lane's keys only
+// the best two take part, which is nearly always enough (one pass over all
+// keys shows it) and takes 2 ballots a bit instead of one for every slot.
 //
-// Keys that fp32 cannot tell apart.  The fp32 key differs from the 64-bit one
-// by less than half of `margin`; where another key lies within the margin of
-// the threshold (of keys, or of group scores) the wave selects again with keys
-// in 64 bits, in LDS.  That is rare: with random logits over 768 experts about
-// 1 token of 1000 (softmax), 1 of 2000 (sigmoid).
+// Keys that fp32 cannot tell apart.  Keys that lie closer to the last one chosen
+// than fp32's error of both are computed in 64 bits and chosen from by those, and
+// so are group scores.  With random logits over 768 experts that happens to about
+// 1 token in some thousand.
 //
-// The kernel reads 4 bytes and spends some 10 instructions an expert; the
-// gradient reads and writes 8.
+// The kernel reads 4 bytes and spends some 50 instructions an expert and lane;
+// the gradient reads and writes 8 bytes.
 
 #include <math.h>
 
@@ -28,67 +25,36 @@
 
 #include "block.h"
 #include "common.h"
+#include "wave.h"
 
 namespace moe {
 
 constexpr int kMaxK = 16;
-
-// ---- reductions over a wave without LDS: rows of 16 lanes by row_shr, then
-// rows to rows; the result of lane 63, the same in every lane
-
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint32_t dpp(uint32_t old, uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)v, CTRL, ROWS, 0xf, false);
-}
-template <typename OP>
-__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, uint32_t neutral, OP op) {
-  v = op(v, dpp<0x111, 0xf>(neutral, v));  // row_shr 1
-  v = op(v, dpp<0x112, 0xf>(neutral, v));
-  v = op(v, dpp<0x114, 0xf>(neutral, v));
-  v = op(v, dpp<0x118, 0xf>(neutral, v));
-  v = op(v, dpp<0x142, 0xa>(neutral, v));  // lane 15 of rows 0, 2 to rows 1, 3
-  v = op(v, dpp<0x143, 0xc>(neutral, v));  // lane 31 to rows 2, 3
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
-__device__ __forceinline__ uint32_t wave_min_u(uint32_t v) {
-  return wave_reduce(v, ~0u, [](uint32_t a, uint32_t b) { return min(a, b); });
-}
-__device__ __forceinline__ float wave_max_f(float v) {
-  return __uint_as_float(wave_reduce(__float_as_uint(v), 0xff800000u, [](uint32_t a, uint32_t b) {
-    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
-  }));
-}
-__device__ __forceinline__ float wave_sum_f(float v) {
-  return __uint_as_float(wave_reduce(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) {
-    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-  }));
-}
 
 // exp(x): 2^(x log2 e) with the product's rounding error put back, off by
 // about 2 steps.
 __device__ __forceinline__ float exp_fast(float x) {
   constexpr float kL = 1.44269502162933349609f, kLo = 1.92596299e-8f;  // log2 e in two parts
   const float t = x * kL;
+  // (at most 2^-17 where 2^t is finite; NaN for an infinite t, which the median
+  // makes finite: infinities, 0 and NaN of 2^t stay what they are)
   const float rest = fmaf(x, kLo, fmaf(x, kL, -t));
-  const float y = __builtin_amdgcn_exp2f(t);
-  // (outside, y is 0, infinite or next to it, or NaN, and the rest may be NaN)
-  return fabsf(t) < 126.f ? fmaf(y, rest * 0.693147182464599609375f, y) : y;
+  const float some = __builtin_amdgcn_fmed3f(rest, -0x1p-16f, 0x1p-16f);
+  return __builtin_amdgcn_exp2f(t) * fmaf(some, 0.693147182464599609375f, 1.f);
 }
 
-// A key mapped to an integer of the same order: NaN ranks as -inf, -0 as +0;
-// above 0, which stands for "no key".
+// A key mapped to an integer of the same order, above 0, which stands for "no
+// key".  (A key is a score of 0 or more plus a bias: never -0.)
 __device__ __forceinline__ uint32_t ordered(float key) {
-  if (key != key) key = -INFINITY;
-  const uint32_t b = __float_as_uint(key + 0.0f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  const uint32_t b = __float_as_uint(key);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float unordered(uint32_t u) {
   return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
 }
 __device__ __forceinline__ uint64_t ordered(double key) {
-  if (key != key) key = -INFINITY;
-  const uint64_t b = __double_as_longlong(key + 0.0);
-  return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
+  const uint64_t b = __double_as_longlong(key);
+  return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
 }
 
 // A group's score from its two best keys: a second one of -inf (switched off, or
@@ -98,75 +64,124 @@ __device__ __forceinline__ F group_score(F best, F best2, bool two) {
   return two && best != (F)INFINITY && best2 != -(F)INFINITY ? best + best2 : best;
 }
 
-__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) {
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
-}
-
-// Everything that a token's lanes know about their place.
+// What a lane knows about its place.
 struct Lanes {
-  int g, j, L, each, G;     // group, place in it, lanes and experts a group, groups
-  uint64_t group, below;    // lanes of this group, lanes of the groups below
+  int g, j, L, each, G;   // group, place in it, lanes and experts a group, groups
+  int slots;              // experts that it holds
   __device__ __forceinline__ int expert(int i) const { return g * each + j + L * i; }
-  __device__ __forceinline__ bool valid(int i) const { return g < G && j + L * i < each; }
 };
 
-// The same selection with keys in 64 bits; returns this lane's chosen slots.
-// s_key: 64 keys a slot, this wave's own.
-__device__ __forceinline__ uint32_t select64(const SelectArgs& a, const float* __restrict__ row,
-                                          const float* s_bias, const Lanes& w, int slots,
-                                          uint64_t* s_key) {
-  const int lane = lane_id();
-  double m = -INFINITY, inv = 0.0;
-  if (a.score == MOE_SCORE_SOFTMAX) {
-    for (int i = 0; i < slots; ++i)
-      if (w.valid(i)) m = fmax(m, (double)row[w.expert(i)]);
-    for (int o = 32; o > 0; o >>= 1) m = fmax(m, __shfl_xor(m, o, kWave));
-    if (m == -INFINITY) m = 0.0;
+// The best two keys of a group, in each of its lanes, from each lane's own.
+template <int O>
+__device__ __forceinline__ void group_best(float& b1, float& b2, int L) {
+  if (O < L) {
+    const float c1 = partner<O>(b1), c2 = partner<O>(b2);
+    b2 = fmaxf(fmaxf(b2, c2), fminf(b1, c1));
+    b1 = fmaxf(b1, c1);
+  }
+  if constexpr (O < 32) group_best<2 * O>(b1, b2, L);
+}
+
+// Scores in 64 bits.
+struct Exact {
+  const float* row;
+  double m, sum;
+  bool softmax;
+  __device__ __forceinline__ double score(int e) const {
+    const double l = (double)row[e];
+    return softmax ? exp(l - m) / sum : 1.0 / (1.0 + exp(-l));
+  }
+  __device__ __forceinline__ double key(int e, float bias) const {
+    const double k = score(e) + (double)bias;
+    return k != k ? -INFINITY : k;
+  }
+};
+__device__ __forceinline__ Exact exact_scores(const float* row, float m, bool softmax, const Lanes& w) {
+  Exact x{row, (double)m, 1.0, softmax};
+  if (softmax) {
     double sum = 0.0;
-    for (int i = 0; i < slots; ++i)
-      if (w.valid(i)) sum += exp((double)row[w.expert(i)] - m);
+    for (int i = 0; i < w.slots; ++i) sum += exp((double)row[w.expert(i)] - x.m);
     for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
-    inv = sum == 0.0 ? 1.0 : sum;
+    x.sum = sum == 0.0 ? 1.0 : sum;
   }
+  return x;
+}
+
+// Whether the lane's group stays, by scores in 64 bits.
+__device__ __forceinline__ bool kept64(const SelectArgs& a, const Exact& x, const float* s_bias,
+                                       const Lanes& w) {
   double b1 = -INFINITY, b2 = -INFINITY;
-  for (int i = 0; i < slots; ++i) {
-    uint64_t u = 0;
-    if (w.valid(i)) {
-      const double l = (double)row[w.expert(i)];
-      const double p = a.score == MOE_SCORE_SOFTMAX ? exp(l - m) / inv : 1.0 / (1.0 + exp(-l));
-      double key = p + (double)s_bias[64 * i + lane];
-      if (key != key) key = -INFINITY;
-      u = ordered(key);
-      b2 = fmax(b2, fmin(b1, key));
-      b1 = fmax(b1, key);
-    }
-    s_key[64 * i + lane] = u;
+  for (int i = 0; i < w.slots; ++i) {
+    const double k = x.key(w.expert(i), s_bias[64 * i + lane_id()]);
+    b2 = fmax(b2, fmin(b1, k));
+    b1 = fmax(b1, k);
   }
-  if (w.G > 1) {
-    for (int o = 1; o < w.L; o <<= 1) {
-      const double c1 = __shfl_xor(b1, o, kWave), c2 = __shfl_xor(b2, o, kWave);
-      b2 = fmax(fmax(b2, c2), fmin(b1, c1));
-      b1 = fmax(b1, c1);
-    }
-    const double s = group_score(b1, b2, a.group_best == 2);
-    int rank = 0;
-    for (int g = 0; g < w.G; ++g) {
-      const double o = __shfl(s, g * w.L, kWave);
-      rank += o > s || (o == s && g < w.g);
-    }
-    if (rank >= a.top_groups)
-      for (int i = 0; i < slots; ++i) s_key[64 * i + lane] = 0;
+  for (int o = 1; o < w.L; o <<= 1) {
+    const double c1 = __shfl_xor(b1, o, kWave), c2 = __shfl_xor(b2, o, kWave);
+    b2 = fmax(fmax(b2, c2), fmin(b1, c1));
+    b1 = fmax(b1, c1);
+  }
+  const double s = group_score(b1, b2, a.group_best == 2);
+  int rank = 0;
+  for (int g = 0; g < w.G; ++g) {
+    const double o = __shfl(s, g * w.L, kWave);
+    rank += o > s || (o == s && g < w.g);
+  }
+  return w.g < w.G && rank < a.top_groups;
+}
+
+// The `need` best, by keys in 64 bits, of the slots in the lanes' masks; returns
+// the lane's.  key, id: 64 keys a slot and 64 numbers, this wave's own.
+__device__ __forceinline__ uint32_t best64(uint32_t mask, int need, const Exact& x,
+                                           const float* s_bias, const Lanes& w, uint64_t* key,
+                                           int* ids) {
+  const int lane = lane_id();
+  int before = 0, all = 0;  // of lower lanes, of the wave
+#pragma unroll
+  for (int b = 0; b < 6; ++b) {
+    const uint64_t with = __ballot(__popc(mask) >> b & 1);
+    before += __popcll(with & lanemask_lt()) << b;
+    all += __popcll(with) << b;
   }
   uint32_t chosen = 0;
-  for (int r = 0; r < a.k; ++r) {
+  if (all <= 64) {
+    // a lane for each: it counts those before it
+    int pos = before;
+    for (uint32_t v = mask; v != 0; v &= v - 1) {
+      const int i = __ffs(v) - 1;
+      key[pos] = ordered(x.key(w.expert(i), s_bias[64 * i + lane]));
+      ids[pos++] = w.expert(i);
+    }
+    __builtin_amdgcn_wave_barrier();
+    const uint64_t u = lane < all ? key[lane] : 0;
+    const int id = lane < all ? ids[lane] : 0x7fffffff;
+    int rank = 0;
+    for (int q = 0; q < all; ++q) {
+      const uint64_t o = (uint64_t)lane_value((uint32_t)(u >> 32), q) << 32 | lane_value((uint32_t)u, q);
+      rank += o > u || (o == u && (int)lane_value((uint32_t)id, q) < id);
+    }
+    const uint64_t taken = __ballot(lane < all && rank < need);
+    pos = before;
+    for (uint32_t v = mask; v != 0; v &= v - 1)
+      chosen |= taken >> pos++ & 1 ? v & -v : 0u;
+    __builtin_amdgcn_wave_barrier();
+    return chosen;
+  }
+  for (uint32_t v = mask; v != 0; v &= v - 1) {
+    const int i = __ffs(v) - 1;
+    key[64 * i + lane] = ordered(x.key(w.expert(i), s_bias[64 * i + lane]));
+  }
+  for (int r = 0; r < need; ++r) {
     uint64_t best = 0;
-    int id = 0x7fffffff, at = 0;
-    for (int i = 0; i < slots; ++i) {
-      const uint64_t u = s_key[64 * i + lane];
+    int id = 0x7fffffff;
+    uint32_t bit = 0;
+    for (uint32_t v = mask & ~chosen; v != 0; v &= v - 1) {
+      const int i = __ffs(v) - 1;
+      const uint64_t u = key[64 * i + lane];
       if (u > best) {
         best = u;
         id = w.expert(i);
-        at = i;
+        bit = v & -v;
       }
     }
     const int mine = id;
@@ -178,20 +193,18 @@ __device__ __forceinline__ uint32_t select64(const SelectArgs& a, const float* _
         id = oi;
       }
     }
-    if (best != 0 && id == mine) {
-      chosen |= 1u << at;
-      s_key[64 * at + lane] = 0;
-    }
+    if (best != 0 && id == mine) chosen |= bit;
   }
   return chosen;
 }
 
 // PL: most experts that a lane holds.
 template <int PL>
-__global__ void __launch_bounds__(256) select_kernel(SelectArgs a) {
+__global__ void __launch_bounds__(256, PL <= 12 ? 4 : 2) select_kernel(SelectArgs a) {
   __shared__ float s_bias[64 * PL];
   __shared__ float s_max[4];
   __shared__ uint64_t s_key[4][64 * PL];
+  __shared__ int s_id[4][64];
   const int lane = lane_id(), wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   Lanes w;
   w.G = a.n_groups;
@@ -199,15 +212,26 @@ __global__ void __launch_bounds__(256) select_kernel(SelectArgs a) {
   w.L = 64 >> (32 - __clz(a.n_groups - 1));  // (n_groups 1: 64)
   w.g = lane / w.L;
   w.j = lane & (w.L - 1);
-  const uint64_t some = w.L == 64 ? ~0ull : (1ull << w.L) - 1;
-  w.group = some << (w.g * w.L);
-  w.below = (1ull << (w.g * w.L)) - 1;
-  const int slots = (w.each + w.L - 1) / w.L;
+  w.slots = w.g < w.G && w.j < w.each ? (w.each - w.j + w.L - 1) / w.L : 0;
+
+  // A token's logits, asked for while the one before is worked on.  Slots without
+  // an expert read another's, or 0 behind the row's end.
+  int t = blockIdx.x * waves + wave;
+  const int step = gridDim.x * waves;
+  float next[PL];
+  auto load = [&](int t) {
+    const auto rs = __builtin_amdgcn_make_buffer_rsrc((void*)(a.logits + (size_t)t * a.ld), 0, a.E * 4,
+                                                      0x00020000);
+#pragma unroll
+    for (int i = 0; i < PL; ++i)
+      next[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, w.expert(0) * 4, i * w.L * 4, 0));
+  };
+  if (t < a.T) load(t);
 
   // the bias by slot and lane, and its largest finite magnitude
   float top = 0.f;
   for (int i = wave; i < PL; i += waves) {
-    const float b = a.bias != nullptr && w.valid(i) ? a.bias[w.expert(i)] : 0.f;
+    const float b = a.bias != nullptr && i < w.slots ? a.bias[w.expert(i)] : 0.f;
     s_bias[64 * i + lane] = b;
     if (fabsf(b) < INFINITY) top = fmaxf(top, fabsf(b));
   }
@@ -215,22 +239,32 @@ __global__ void __launch_bounds__(256) select_kernel(SelectArgs a) {
   if (lane == 0) s_max[wave] = top;
   __syncthreads();
   for (int q = 0; q < waves; ++q) top = fmaxf(top, s_max[q]);
-  // Twice the error of an fp32 key, relative to key and bias: sigmoid, some 3
-  // steps of p and one of the sum; softmax, exp's argument (l - m, at most 88
-  // where p counts, off by 2^-24 of it), the sum's 40 additions and the rest.
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
-  const float margin = softmax ? 2e-5f : 1.5e-6f;
-  const float least = 1e-36f;  // scores below fp32's normal numbers
+  // Twice the error of the fp32 score next to the key `cut` (whose scores are
+  // at most P = |cut| + top), and of the key's sum.  Sigmoid: some 6 steps of p.
+  // Softmax: exp's argument l - m is off by 2^-24 of it, so p by p |l - m| 2^-24,
+  // which grows with p up to p = P, where |l - m| <= -log P (or 1); the sum's
+  // PL + 6 additions and a few steps more.
+  auto margin = [&](float cut) {
+    const float P = fabsf(cut) + top;
+    const float steps = softmax ? fmaxf(1.f, -0.6931472f * __builtin_amdgcn_logf(P)) + (PL + 14) : 8.f;
+    return steps * 0x1p-23f * P + 1e-36f;  // (scores below fp32's normal numbers)
+  };
 
-  for (int t = blockIdx.x * waves + wave; t < a.T; t += gridDim.x * waves) {
+  for (; t < a.T; t += step) {
     const float* row = a.logits + (size_t)t * a.ld;
     float p[PL];
 #pragma unroll
-    for (int i = 0; i < PL; ++i) p[i] = w.valid(i) ? row[w.expert(i)] : -INFINITY;
+    for (int i = 0; i < PL; ++i) p[i] = next[i];
+    if (t + step < a.T) load(t + step);
+    float m = 0.f, inv = 1.f;
     if (softmax) {
-      float m = p[0];
+      m = -INFINITY;
 #pragma unroll
-      for (int i = 1; i < PL; ++i) m = fmaxf(m, p[i]);
+      for (int i = 0; i < PL; ++i) {
+        p[i] = i < w.slots ? p[i] : -INFINITY;
+        m = fmaxf(m, p[i]);
+      }
       m = wave_max_f(m);
       if (m == -INFINITY) m = 0.f;
       float sum = 0.f;
@@ -240,148 +274,131 @@ __global__ void __launch_bounds__(256) select_kernel(SelectArgs a) {
         sum += p[i];
       }
       sum = wave_sum_f(sum);
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
       for (int i = 0; i < PL; ++i) p[i] *= inv;
     } else {
 #pragma unroll
       for (int i = 0; i < PL; ++i) p[i] = __builtin_amdgcn_rcpf(1.f + exp_fast(-p[i]));
     }
-    uint32_t u[PL];
-    float b1 = -INFINITY, b2 = -INFINITY;
+    // keys, and the lane's best two
+    uint32_t u[PL], u1 = 0u, u2 = 0u;
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-      float key = p[i] + s_bias[64 * i + lane];
-      if (!w.valid(i)) key = -INFINITY;
-      u[i] = w.valid(i) ? ordered(key) : 0u;
-      if (key != key) key = -INFINITY;
-      b2 = fmaxf(b2, fminf(b1, key));
-      b1 = fmaxf(b1, key);
+      const float key = fmaxf(p[i] + s_bias[64 * i + lane], -INFINITY);  // (NaN: -inf)
+      u[i] = i < w.slots ? ordered(key) : 0u;
+      u2 = max(u2, min(u1, u[i]));
+      u1 = max(u1, u[i]);
     }
-    bool close = false;
     if (w.G > 1) {
-      for (int o = 1; o < w.L; o <<= 1) {
-        const float c1 = __shfl_xor(b1, o, kWave), c2 = __shfl_xor(b2, o, kWave);
-        b2 = fmaxf(fmaxf(b2, c2), fminf(b1, c1));
-        b1 = fmaxf(b1, c1);
-      }
+      float b1 = u1 ? unordered(u1) : -INFINITY, b2 = u2 ? unordered(u2) : -INFINITY;
+      group_best<1>(b1, b2, w.L);
       const float s = group_score(b1, b2, a.group_best == 2);
       int rank = 0;
       for (int g = 0; g < w.G; ++g) {
-        const float o = __uint_as_float(lane_value(__float_as_uint(s), g * w.L));
+        const float o = lane_value(s, g * w.L);
         rank += o > s || (o == s && g < w.g);
       }
-      const bool kept = w.g < w.G && rank < a.top_groups;
-#pragma unroll
-      for (int i = 0; i < PL; ++i)
-        if (!kept) u[i] = 0u;
-      // the last group that stays, and others within the margin below it
+      bool kept = w.g < w.G && rank < a.top_groups;
+      // Another group within the margin below the last one that stays: again in
+      // 64 bits.  (Each of the sum's two keys has a score of at most P.)
       const uint64_t last = __ballot(w.g < w.G && rank == a.top_groups - 1);
-      const float cut = __uint_as_float(lane_value(__float_as_uint(s), __ffsll((unsigned long long)last) - 1));
-      const float low = cut - (2.f * margin * (fabsf(cut) + 2.f * top) + least);
-      close = __ballot(w.g < w.G && !kept && s >= low && s > -INFINITY) != 0;
-    }
-    // the k-th largest lane maximum
-    uint32_t best = u[0];
+      const float cut = lane_value(s, __ffsll((unsigned long long)last) - 1);
+      const float low = cut - 2.f * margin(fabsf(cut) + top);
+      if (__ballot(w.g < w.G && !kept && s >= low && s > -INFINITY) != 0)
+        kept = kept64(a, exact_scores(row, m, softmax, w), s_bias, w);
 #pragma unroll
-    for (int i = 1; i < PL; ++i) best = max(best, u[i]);
+      for (int i = 0; i < PL; ++i) u[i] = kept ? u[i] : 0u;
+      u1 = kept ? u1 : 0u;
+      u2 = kept ? u2 : 0u;
+    }
+    // A threshold that the lanes' best two keys reach k times: bit by bit, up to
+    // the first that parts k of them from the others.  It serves all keys unless
+    // a lane's third reaches it too.
     uint32_t thr = 0u;
     for (int b = 31; b >= 0; --b) {
       const uint32_t cand = thr | (1u << b);
-      if (__popcll(__ballot(best >= cand)) >= a.k) thr = cand;
+      const int n = __popcll(__ballot(u1 >= cand)) + __popcll(__ballot(u2 >= cand));
+      if (n >= a.k) thr = cand;
+      if (n == a.k) break;
     }
     thr = max(thr, 1u);
     int count = 0;
 #pragma unroll
     for (int i = 0; i < PL; ++i) count += __popcll(__ballot(u[i] >= thr));
-    if (count > a.k + 8) {
-      // a large surplus: the k-th largest of all keys bit by bit
+    if (count != a.k) {
+      // from all keys
       thr = 0u;
       for (int b = 31; b >= 0; --b) {
         const uint32_t cand = thr | (1u << b);
-        int cnt = 0;
+        int n = 0;
 #pragma unroll
-        for (int i = 0; i < PL; ++i) cnt += __popcll(__ballot(u[i] >= cand));
-        if (cnt >= a.k) {
+        for (int i = 0; i < PL; ++i) n += __popcll(__ballot(u[i] >= cand));
+        if (n >= a.k) {
           thr = cand;
-          count = cnt;
+          count = n;
         }
-      }
-    } else {
-      // take the smallest value off while enough are left
-      while (true) {
-        uint32_t low = ~0u;
-#pragma unroll
-        for (int i = 0; i < PL; ++i) low = min(low, u[i] >= thr ? u[i] : ~0u);
-        thr = wave_min_u(low);
-        if (count == a.k) break;
-        int same = 0;
-#pragma unroll
-        for (int i = 0; i < PL; ++i) same += __popcll(__ballot(u[i] == thr));
-        if (count - same < a.k) break;
-        count -= same;
-        ++thr;
+        if (n == a.k) break;
       }
     }
-    // keys within the margin of the threshold that are not above it
-    const float cut = unordered(thr);
-    const float low = cut - (margin * (fabsf(cut) + top) + least);
-    const uint32_t reach = low > -INFINITY ? ordered(low) : thr;
+    // the smallest key of those, the k-th largest
+    uint32_t least = ~0u;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) least = min(least, u[i] >= thr ? u[i] : ~0u);
+    least = wave_min_u(least);
+    // Keys so close to it that fp32 may have them on the wrong side.  (An infinite
+    // one has only equals, which go by their ids.)
+    const float cut = unordered(least);
+    uint32_t from = least, to = least;
+    if (cut > -INFINITY && cut < INFINITY) {
+      const float width = margin(cut);
+      from = ordered(cut - width);
+      to = ordered(cut + width);
+    }
+    uint32_t chosen = 0, open = 0;
     int near = 0;
 #pragma unroll
-    for (int i = 0; i < PL; ++i) near += __popcll(__ballot(u[i] >= reach));
-    close = close || (near > a.k && cut > -INFINITY && cut < INFINITY);
-
-    uint32_t chosen = 0;
-    if (close) {
-      chosen = select64(a, row, s_bias, w, slots, s_key[wave]);
-    } else {
-      // every key above the threshold, then those equal to it by ascending id
-      int above = 0;
-#pragma unroll
-      for (int i = 0; i < PL; ++i) above += __popcll(__ballot(u[i] > thr));
-      const int need = a.k - above;
-      if (count == a.k) {
-#pragma unroll
-        for (int i = 0; i < PL; ++i) chosen |= u[i] >= thr ? 1u << i : 0u;
-      } else {
-        int before = 0;  // equal keys with a lower id: lower groups, then slots
-#pragma unroll
-        for (int i = 0; i < PL; ++i) before += __popcll(__ballot(u[i] == thr) & w.below);
-#pragma unroll
-        for (int i = 0; i < PL; ++i) {
-          const uint64_t same = __ballot(u[i] == thr) & w.group;
-          const int at = before + __popcll(same & lanemask_lt());
-          chosen |= u[i] > thr || (u[i] == thr && at < need) ? 1u << i : 0u;
-          before += __popcll(same);
-        }
-      }
+    for (int i = 0; i < PL; ++i) {
+      const bool at = u[i] >= from;
+      near += __popcll(__ballot(at));
+      chosen |= at ? 1u << i : 0u;
+      open |= at && u[i] <= to ? 1u << i : 0u;
     }
-
-    float scale = a.scaling;
-    float whole = 1.f;
-    if (a.renorm) {
-      float s = 0.f;
+    if (near > a.k) {
+      int sure = 0;
+      chosen &= ~open;
 #pragma unroll
-      for (int i = 0; i < PL; ++i) s += chosen >> i & 1 ? p[i] : 0.f;
-      whole = wave_sum_f(s) + a.eps;
+      for (int b = 0; b < 6; ++b) sure += __popcll(__ballot(__popc(chosen) >> b & 1)) << b;
+      // (infinite keys: any finite score leaves them equal)
+      chosen |= best64(open, a.k - sure, exact_scores(row, m, softmax, w), s_bias, w, s_key[wave],
+                       s_id[wave]);
     }
+    // The ids into LDS, lane by lane; then a lane for each, which counts the
+    // lower ones to find its place.
     int pos = 0;
 #pragma unroll
-    for (int i = 0; i < PL; ++i) pos += __popcll(__ballot(chosen >> i & 1) & w.below);
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      const uint64_t sel = __ballot(chosen >> i & 1) & w.group;
-      if (chosen >> i & 1) {
-        const int o = pos + __popcll(sel & lanemask_lt());
-        MOE_CHECK(w.valid(i), MOE_CHECK_ROUTE_ID);
-        if (MOE_GUARD(o < a.k, MOE_CHECK_ROUTE_ID)) {
-          a.idx[(size_t)t * a.k + o] = w.expert(i);
-          const float f = a.renorm ? (whole == 0.f ? 0.f : p[i] / whole) : p[i];
-          a.gate[(size_t)t * a.k + o] = scale * f;
-        }
-      }
-      pos += __popcll(sel);
+    for (int b = 0; b < 5; ++b)  // (at most 16)
+      pos += __popcll(__ballot(__popc(chosen) >> b & 1) & lanemask_lt()) << b;
+    while (chosen != 0) {
+      if (MOE_GUARD(pos < a.k, MOE_CHECK_ROUTE_ID)) s_id[wave][pos] = w.expert(__ffs(chosen) - 1);
+      ++pos;
+      chosen &= chosen - 1;
+    }
+    __builtin_amdgcn_wave_barrier();
+    const int id = lane < a.k ? s_id[wave][lane] : 0;
+    __builtin_amdgcn_wave_barrier();
+    int at = 0;
+    for (int q = 0; q < a.k; ++q) at += (int)lane_value((uint32_t)id, q) < id;
+    MOE_CHECK(id < a.E, MOE_CHECK_ROUTE_ID);
+    const float l = row[id];
+    float f = softmax ? exp_fast(l - m) * inv : __builtin_amdgcn_rcpf(1.f + exp_fast(-l));
+    if (a.renorm) {
+      const float whole = wave_sum_f(lane < a.k ? f : 0.f) + a.eps;
+      f = whole == 0.f ? 0.f : f / whole;
+    }
+    if (lane < a.k) {
+      a.idx[(size_t)t * a.k + at] = id;
+      a.gate[(size_t)t * a.k + at] = a.scaling * f;
     }
   }
 }
@@ -395,7 +412,7 @@ int launch_select(const SelectArgs& a, hipStream_t st) {
   // few tokens: a wave per workgroup, over more CUs
   const int waves = a.T < 4 * cus ? 1 : 4;
   const dim3 block(64 * waves);
-  const dim3 grid((unsigned)std::min<long>(((long)a.T + waves - 1) / waves, (long)cus * 16));
+  const dim3 grid((unsigned)std::min<long>(((long)a.T + waves - 1) / waves, (long)cus * 4));
 #define MOE_SELECT(PL) hipLaunchKernelGGL(select_kernel<PL>, grid, block, 0, st, a)
   if (slots <= 1) MOE_SELECT(1);
   else if (slots <= 2) MOE_SELECT(2);
@@ -476,7 +493,7 @@ __global__ void __launch_bounds__(256) select_bwd_kernel(SelectBwdArgs a) {
     // an expert that several slots name: the sum over them, in each
     float both = 0.f;
     for (int q = 0; q < a.k; ++q) {
-      const float o = __uint_as_float(lane_value(__float_as_uint(d), q));
+      const float o = lane_value(d, q);
       both += (int)lane_value((uint32_t)e, q) == e ? o : 0.f;
     }
     if (e >= 0) dp[e] = softmax ? both : both * sel * (1.f - sel);

@@ -34,7 +34,7 @@ def test_library_exports_every_declared_symbol():
 
 def test_struct_sizes_match_the_header(tmp_path):
     src = tmp_path / "s.c"
-    names = ("moe_select_params", "moe_quant_shape", "moe_i8_shape", "moe_ffn_i8_io", "moe_norm_shape", "moe_rows",
+    names = ("moe_select_params", "moe_quant_shape", "moe_i8_shape", "moe_ffn_i8_io", "moe_norm_shape",
              "moe_norm_io", "moe_norm_grad_io")
     src.write_text('#include <stdio.h>\n#include "moe_block.h"\nint main(void) { printf("' + "%zu " * len(names) + '", ' +
                    ", ".join(f"sizeof({n})" for n in names) + "); return 0; }\n")
@@ -42,7 +42,7 @@ def test_struct_sizes_match_the_header(tmp_path):
     subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
     got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
     assert got == [ctypes.sizeof(c) for c in (K.MoeSelectParams, K.MoeQuantShape, K.MoeI8Shape, K.MoeFfnI8IO, K.MoeNormShape,
-                                              K.MoeRows, K.MoeNormIO, K.MoeNormGradIO)]
+                                              K.MoeNormIO, K.MoeNormGradIO)]
 
 
 # ---- selection
@@ -196,17 +196,28 @@ def test_ffn_refuses():
 # ---- norms
 
 
-def R(p=A, ld=64):
-    return K.MoeRows(p, ld)
+class R(tuple):
+    """A matrix argument: address and elements between rows."""
+
+    def __new__(cls, p=A, ld=64):
+        return super().__new__(cls, (p, ld))
+
+
+def given(io, kw):
+    for n, v in kw.items():
+        if isinstance(v, R):
+            setattr(io, n, v[0])
+            setattr(io, n + "_ld", v[1])
+        else:
+            setattr(io, n, v)
+    return io
 
 
 def norm(shape=None, **kw):
     s = K.make_norm_shape(16, 64, "bf16", 1e-6, 1.0, 4)
     for n, v in (shape or {}).items():
         setattr(s, n, v)
-    io = K.MoeNormIO(R(), R(), A, A, A, R(), R(), A, A)
-    for n, v in kw.items():
-        setattr(io, n, v)
+    io = given(K.MoeNormIO(*R(), *R(), A, A, A, *R(), *R(), A, A), kw)
     return K.lib().moe_norm_residual(ref(s), ref(io), None)
 
 
@@ -214,9 +225,7 @@ def norm_bwd(shape=None, ws=A, **kw):
     s = K.make_norm_shape(16, 64, "bf16", 1e-6, 1.0, 4)
     for n, v in (shape or {}).items():
         setattr(s, n, v)
-    io = K.MoeNormGradIO(R(), R(), A, A, A, R(), R(), R(), R(), A, A, A, 0, 0)
-    for n, v in kw.items():
-        setattr(io, n, v)
+    io = given(K.MoeNormGradIO(*R(), *R(), A, A, A, *R(), *R(), *R(), *R(), A, A, A, 0, 0), kw)
     return K.lib().moe_norm_residual_backward(ref(s), ref(io), P(ws), None)
 
 
@@ -279,14 +288,25 @@ def test_binding_refuses_tensors_off_the_gpu():
             call()
 
 
-def test_binding_refuses_overlaps():
-    t = torch.zeros(100)
-    a, b = t[:60].view(6, 10), t[50:].view(5, 10)
-    with pytest.raises(ValueError, match="overlap"):
-        K._apart([("a", a)], [("b", b)])
-    with pytest.raises(ValueError, match="overlap"):
-        K._apart([("a", a), ("b", b)])
-    K._apart([("a", a)], [("a2", a)], {("a", "a2")})
-    with pytest.raises(ValueError, match="overlap"):
-        K._apart([("a", a)], [("a2", a[:5])], {("a", "a2")})
-    K._apart([("a", a[:5]), ("b", b), ("c", None)], [("d", None)])
+@pytest.mark.parametrize("out,other", [("r", "y"), ("r", "w_post"), ("r", "gate"), ("h", "x"), ("h", "r"), ("q", "h"),
+                                       ("q_scale", "w_pre"), ("r", "q")])
+def test_norm_refuses_overlaps(out, other):
+    """Arrays a MiB apart, then one's last element over another's first."""
+    mib = 1 << 20
+    at = {n: (i + 1) * mib for i, n in enumerate(("x", "y", "w_post", "gate", "w_pre", "r", "h", "q", "q_scale"))}
+    size = {"w_post": 128, "w_pre": 128, "gate": 4 * 128, "q": 16 * 64, "q_scale": 64}
+    bytes_ = {n: size.get(n, 16 * 128) for n in at}
+    rows = ("x", "y", "r", "h")
+    at[out] = at[other] - bytes_[out] + 16
+    assert norm(**{n: R(v) if n in rows else v for n, v in at.items()}) == EINVAL
+    at[out] = at[other] + bytes_[other] - 16
+    assert norm(**{n: R(v) if n in rows else v for n, v in at.items()}) == EINVAL
+
+
+def test_products_and_selections_refuse_overlaps():
+    assert quant(x=A, q=A + 512, scale=A + 8192) == EINVAL                  # x has 768 bytes
+    assert quant(x=A, q=A + 768, scale=A + 768 + 380) == EINVAL             # q has 384
+    assert select(layer(), rule(), logits=A, idx=A + 64, gate=A + 65536, bias=0) == EINVAL
+    assert select(layer(), rule(), logits=A, idx=A + 65536, gate=A + 65536 + 508, bias=0) == EINVAL
+    assert select_bwd(layer(), rule(), logits=A, idx=A + 65536, dgate=A + 2 * 65536, dlogits=A + 96 * 64 - 4) == EINVAL
+    assert ffn(layer(), y_perm=A) == EINVAL
