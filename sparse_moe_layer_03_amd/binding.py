@@ -223,11 +223,18 @@ class LayerBuffers:
 
 
 def layer_forward(buf: LayerBuffers, x, w_router, bias, w_gate, w_up, w_down, logit_bias=None,
-                  logits_out=None, stream=None):
-    """route -> dispatch -> expert FFN -> combine; outputs land in ``buf``."""
+                  logits_out=None, stream=None, select=None):
+    """route -> dispatch -> expert FFN -> combine; outputs land in ``buf``.
+    select: another selection rule than moe_route's (``block.make_select``;
+    logits_out is needed then)."""
     s = buf.shape
-    moe_route(s, x, w_router, logit_bias, bias, buf.topk_idx, buf.topk_gate, logits_out, buf.ws,
-              stream)
+    if select is None:
+        moe_route(s, x, w_router, logit_bias, bias, buf.topk_idx, buf.topk_gate, logits_out, buf.ws,
+                  stream)
+    else:
+        from . import block
+        block.moe_route_select(s, select, x, w_router, logit_bias, bias, buf.topk_idx, buf.topk_gate,
+                               logits_out, buf.ws, stream)
     moe_dispatch(s, buf.topk_idx, x, buf.counts, buf.offsets, buf.perm, buf.inv_perm,
                  buf.x_perm, buf.ws, stream)
     moe_expert_ffn(s, x, buf.x_perm, buf.perm, buf.offsets, w_gate, w_up, w_down, buf.y_perm,

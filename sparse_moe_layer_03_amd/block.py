@@ -7,6 +7,8 @@ torch tensors.  As in ``train``, the library checks sizes, alignment and
 overlaps, the binding what only it can see: that every tensor lies on one GPU,
 is laid out as the call reads it, and is as large as the shape says.  Calls run
 on the tensors' device, on its current stream unless ``stream`` names another.
+``block_forward`` and ``block_backward`` put the operators together with the
+layer's own calls, as the blocks of a model use them.
 """
 
 from __future__ import annotations
@@ -376,3 +378,93 @@ def moe_norm_residual_backward(shape: MoeNormShape, ws, *, r=None, y=None, w_pos
                        int(bool(accumulate)), 0)
     _run("moe_norm_residual_backward", dev, stream, ctypes.byref(s), ctypes.byref(io),
          _scratch(ws, _on(dev, moe_norm_residual_backward_workspace_bytes, s), dev))
+
+
+# ---- a block: selection, experts and the residual step behind them
+
+
+class I8Experts:
+    """The experts' weights in 8 bits: codes and the scales of their output
+    channels, laid out once (moe_quantize_rows)."""
+
+    def __init__(self, w_gate, w_up, w_down, stream=None):
+        (self.w_gate, self.s_gate), (self.w_up, self.s_up), (self.w_down, self.s_down) = (
+            quantize_rows(w, stream) for w in (w_gate, w_up, w_down))
+
+
+class BlockBuffers:
+    """Device buffers of one block: the layer's (binding.LayerBuffers), its
+    logits, the new residual r and the next block's input h; with i8, the codes
+    of h and the experts' workspace."""
+
+    def __init__(self, shape: B.MoeShape, i8=False, device="cuda"):
+        self.shape, self.layer = shape, B.LayerBuffers(shape, device)
+        dt, rows = _DTYPE[shape.dtype], (shape.T, shape.d_model)
+        self.logits = torch.empty((shape.T, shape.n_ffn + shape.n_zero), dtype=torch.float32, device=device)
+        self.r, self.h = torch.empty(rows, dtype=dt, device=device), torch.empty(rows, dtype=dt, device=device)
+        self.q = self.q_scale = self.ws = None
+        if i8:
+            self.q = torch.empty(rows, dtype=torch.int8, device=device)
+            self.q_scale = torch.empty(shape.T, dtype=torch.float32, device=device)
+            self.ws = torch.empty(moe_expert_ffn_i8_workspace_bytes(shape), dtype=torch.uint8, device=device)
+
+
+def block_input(norm: MoeNormShape, buf: BlockBuffers, x, w_pre, stream=None):
+    """The first block's input, h = x rstd(x) w_pre (and its codes), in ``buf``,
+    which stands for the block before it; norm: res_scale 1."""
+    moe_norm_residual(norm, x=x, w_pre=w_pre, h=buf.h, q=buf.q, q_scale=buf.q_scale, stream=stream)
+    return buf.h
+
+
+def block_forward(buf: BlockBuffers, params: MoeSelectParams, norm: MoeNormShape, x, before: BlockBuffers, w_router,
+                  bias, experts, *, w_post=None, gate=None, w_pre=None, logit_bias=None, stream=None):
+    """One block on the residual x and its input before.h: selection, experts
+    (I8Experts, or w_gate, w_up, w_down) and combine, then r = res_scale x + gate
+    norm(y, w_post) and the next block's input h = norm(r, w_pre), in ``buf``."""
+    s, L, h = buf.shape, buf.layer, before.h
+    moe_route_select(s, params, h, w_router, logit_bias, bias, L.topk_idx, L.topk_gate, buf.logits, L.ws, stream)
+    B.moe_dispatch(s, L.topk_idx, h, L.counts, L.offsets, L.perm, L.inv_perm, L.x_perm, L.ws, stream)
+    if isinstance(experts, I8Experts):
+        tokens = dict(x=h) if before.q is None else dict(xq=before.q, x_scale=before.q_scale)
+        e = experts
+        moe_expert_ffn_i8(s, FfnI8IO(perm=L.perm, offsets=L.offsets, w_gate=e.w_gate, s_gate=e.s_gate, w_up=e.w_up,
+                                     s_up=e.s_up, w_down=e.w_down, s_down=e.s_down, y_perm=L.y_perm, **tokens),
+                          buf.ws, stream)
+    else:
+        B.moe_expert_ffn(s, h, L.x_perm, L.perm, L.offsets, *experts, L.y_perm, L.ws, stream)
+    B.moe_combine(s, h, L.y_perm, L.topk_idx, L.topk_gate, L.inv_perm, L.y, stream)
+    out = {} if w_pre is None else dict(h=buf.h, q=buf.q, q_scale=buf.q_scale)
+    moe_norm_residual(norm, x=x, y=L.y, w_post=w_post, gate=gate, w_pre=w_pre, r=buf.r, stream=stream, **out)
+    return buf.r
+
+
+class BlockGrads:
+    """What the backward pass of a block needs beside its BlockBuffers: the
+    layer's gradients (train.TrainBuffers; its dx is the gradient at the block's
+    input), those at x and y, of the norms' vectors and the gate, workspace."""
+
+    def __init__(self, shape: B.MoeShape, norm: MoeNormShape, w_post=None, gate=None, w_pre=None, device="cuda"):
+        self.layer = T.TrainBuffers(shape, device)
+        like = self.layer.dx
+        self.dx, self.dy = torch.empty_like(like), torch.empty_like(like)
+        self.dw_post, self.dgate, self.dw_pre = (None if t is None else torch.zeros_like(t)
+                                                 for t in (w_post, gate, w_pre))
+        self.ws = torch.empty(moe_norm_residual_backward_workspace_bytes(norm), dtype=torch.uint8, device=device)
+
+
+def block_backward(buf: BlockBuffers, g: BlockGrads, params: MoeSelectParams, norm: MoeNormShape, before: BlockBuffers,
+                   w_router, experts, dr, dh=None, *, w_post=None, gate=None, w_pre=None, accumulate=False,
+                   stream=None):
+    """Gradients of the last ``block_forward`` on ``buf`` (experts w_gate, w_up,
+    w_down) from those at r and h: at x in ``g.dx``, at the block's input in
+    ``g.layer.dx``, which are the block before's dr and dh."""
+    moe_norm_residual_backward(norm, g.ws, r=buf.r if w_pre is not None else None, y=buf.layer.y, w_post=w_post,
+                               gate=gate, w_pre=w_pre, dr=dr, dh=dh, dx=g.dx, dy=g.dy, dgate=g.dgate,
+                               dw_post=g.dw_post, dw_pre=g.dw_pre, accumulate=accumulate, stream=stream)
+    L, t = buf.layer, g.layer
+    io = T.BackwardIO(x=before.h, w_router=w_router, logits=buf.logits, topk_idx=L.topk_idx, topk_gate=L.topk_gate,
+                      offsets=L.offsets, perm=L.perm, inv_perm=L.inv_perm, w_gate=experts[0], w_up=experts[1],
+                      w_down=experts[2], dy=g.dy, dx=t.dx, dgate=t.dgate, dlogits=t.dlogits, dw_router=t.dw_router,
+                      dw_gate=t.dw_gate, dw_up=t.dw_up, dw_down=t.dw_down, accumulate=accumulate)
+    moe_layer_backward_select(buf.shape, params, io, t.ws, stream)
+    return g.dx, t.dx

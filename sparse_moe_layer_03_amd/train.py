@@ -329,27 +329,33 @@ class TrainBuffers:
 
 
 def layer_backward(buf: B.LayerBuffers, tb: TrainBuffers, x, w_router, w_gate, w_up, w_down, dy,
-                   accumulate=False, stream=None):
+                   accumulate=False, stream=None, select=None):
     """Gradients of the last ``binding.layer_forward`` on ``buf``, which was
-    given ``tb.logits`` as logits_out; they land in ``tb``."""
+    given ``tb.logits`` as logits_out; they land in ``tb``.  select: the rule
+    (``block.make_select``) that the experts were chosen by, if not moe_route's."""
     io = BackwardIO(x=x, w_router=w_router, logits=tb.logits, topk_idx=buf.topk_idx,
                     topk_gate=buf.topk_gate, offsets=buf.offsets, perm=buf.perm,
                     inv_perm=buf.inv_perm, w_gate=w_gate, w_up=w_up, w_down=w_down, dy=dy, dx=tb.dx,
                     dgate=tb.dgate, dlogits=tb.dlogits, dw_router=tb.dw_router, dw_gate=tb.dw_gate,
                     dw_up=tb.dw_up, dw_down=tb.dw_down, accumulate=accumulate)
-    moe_layer_backward(buf.shape, io, tb.ws, stream)
+    if select is None:
+        moe_layer_backward(buf.shape, io, tb.ws, stream)
+    else:
+        from . import block
+        block.moe_layer_backward_select(buf.shape, select, io, tb.ws, stream)
     return tb.dx
 
 
 def train_step(buf: B.LayerBuffers, tb: TrainBuffers, x, w_router, bias, w_gate, w_up, w_down,
                loss_grad, params: MoeAdamwParams, tensors: AdamwTensors, state, logit_bias=None,
-               grad_scale: Optional[torch.Tensor] = None):
+               grad_scale: Optional[torch.Tensor] = None, select=None):
     """Forward, backward and AdamW step of one layer: dy = loss_grad(y).  On
     the current stream, where loss_grad's own work runs too.  The step updates
     what ``tensors`` lists; a logit_bias that is trained has the gradient
-    ``tb.dlogits.sum(0)``, which the step does not form."""
+    ``tb.dlogits.sum(0)``, which the step does not form.  select: another
+    selection rule than moe_route's (``block.make_select``)."""
     y = B.layer_forward(buf, x, w_router, bias, w_gate, w_up, w_down, logit_bias=logit_bias,
-                        logits_out=tb.logits)
-    dx = layer_backward(buf, tb, x, w_router, w_gate, w_up, w_down, loss_grad(y))
+                        logits_out=tb.logits, select=select)
+    dx = layer_backward(buf, tb, x, w_router, w_gate, w_up, w_down, loss_grad(y), select=select)
     moe_adamw(params, tensors, state, grad_scale=grad_scale)
     return y, dx
