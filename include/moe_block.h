@@ -192,7 +192,7 @@ size_t moe_expert_ffn_i8_workspace_bytes(const moe_shape* shape);
  *   y_perm[p] = (hq Wd^T) sh sd     rounded to dtype
  * sums exact; z, u and silu in fp32 where dtype is bf16, in 64 bits where it
  * is fp32 (an fp32 H decides the next code).  Shape limits as in moe.h, and
- * T * top_k < 2^27, d_model and d_ff < 2^17. */
+ * T * top_k < 2^27, d_model and d_ff < 2^17, T * d_model < 2^31 - 2^16. */
 int moe_expert_ffn_i8(const moe_shape* shape, const moe_ffn_i8_io* io, void* ws, void* stream);
 
 /* ---- norms around a block ------------------------------------------------ */

@@ -60,19 +60,20 @@ int launch_select_bwd(const SelectBwdArgs& a, hipStream_t st);
 int launch_quantize(int dtype, const void* x, int64_t ldx, int M, int K, int8_t* q, int64_t ldq,
                     float* scale, const int32_t* m_used, hipStream_t st);
 
-// Codes and scales of the FFN rows, sorted by expert: for p < offsets[n_ffn],
-// row perm[p] / k.
-int launch_gather_i8(const int8_t* xq, const float* xs, const int32_t* perm, const int32_t* offsets,
-                     int n_ffn, int Tk, int k, int d, int8_t* rows, float* row_scale,
-                     hipStream_t st);
+// The FFN rows, sorted by expert: for p < offsets[n_ffn], the token perm[p] / k
+// and its scale.
+int launch_row_tokens(const float* xs, const int32_t* perm, const int32_t* offsets, int n_ffn, int Tk,
+                      int k, int32_t* tok, float* row_scale, hipStream_t st);
 
 // out[p, j] = (sum_r a[p, r] b_e[j, r]) sa[p] sb[e, j]; with b2, SwiGLU of the
-// products by b (gate) and b2 (up).
+// products by b (gate) and b2 (up), a's row for p being tok[p].
 struct I8Args {
   const int8_t* a;
   const float* sa;
   const int8_t *b, *b2;
   const float *sb, *sb2;
+  const int32_t* tok;      // with b2
+  uint32_t a_bytes;        // of a, with b2: less than 2^31 - 2^16
   void* out;
   const int32_t* offsets;  // may be null with one group
   int64_t lda, ldo;

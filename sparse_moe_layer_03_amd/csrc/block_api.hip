@@ -136,7 +136,7 @@ static int run_i8(int out_dtype, const I8Args& g, hipStream_t st) {
 // ---- the experts' FFN in 8-bit integers: workspace
 
 struct FfnLayout {
-  size_t xq, xs, rows, rs, h, hq, hs, total;
+  size_t xq, xs, tok, rs, h, hq, hs, total;
 };
 
 static FfnLayout ffn_layout(const moe_shape* s) {
@@ -150,7 +150,7 @@ static FfnLayout ffn_layout(const moe_shape* s) {
   };
   w.xq = take((size_t)s->T * d);
   w.xs = take((size_t)s->T * 4);
-  w.rows = take(rows * d);
+  w.tok = take(rows * 4);
   w.rs = take(rows * 4);
   w.h = take(rows * f * elem_size(s->dtype));
   w.hq = take(rows * f);
@@ -162,7 +162,9 @@ static FfnLayout ffn_layout(const moe_shape* s) {
 static int check_ffn(const moe_shape* s) {
   const int rc = check_shape(s);
   if (rc) return rc;
-  return (long)s->T * s->top_k < kGmmMaxRows && s->d_model < (1 << 17) && s->d_ff < (1 << 17)
+  // (the tokens' codes are addressed by 31-bit offsets)
+  return (long)s->T * s->top_k < kGmmMaxRows && s->d_model < (1 << 17) && s->d_ff < (1 << 17) &&
+                 (long)s->T * s->d_model < (1l << 31) - (1 << 16)
              ? MOE_OK
              : MOE_EUNSUPPORTED;
 }
@@ -384,12 +386,14 @@ int moe_expert_ffn_i8(const moe_shape* s, const moe_ffn_i8_io* io, void* ws, voi
     xq = q;
     xs = qs;
   }
-  int8_t *rows = (int8_t*)(base + w.rows), *hq = (int8_t*)(base + w.hq);
+  int8_t* hq = (int8_t*)(base + w.hq);
+  int32_t* tok = (int32_t*)(base + w.tok);
   float *rs = (float*)(base + w.rs), *hs = (float*)(base + w.hs);
-  if ((rc = launch_gather_i8(xq, xs, io->perm, io->offsets, s->n_ffn, Tk, s->top_k, d, rows, rs, st)))
-    return rc;
+  if ((rc = launch_row_tokens(xs, io->perm, io->offsets, s->n_ffn, Tk, s->top_k, tok, rs, st))) return rc;
   I8Args g{};
-  g.a = rows;
+  g.a = xq;
+  g.a_bytes = (uint32_t)((size_t)s->T * d);
+  g.tok = tok;
   g.sa = rs;
   g.b = io->w_gate;
   g.b2 = io->w_up;

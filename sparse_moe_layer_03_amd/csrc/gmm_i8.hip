@@ -143,7 +143,11 @@ gmm_i8_kernel(I8Args g) {
   // A load instruction brings RPI rows; a lane's place in them, and what chunk of
   // its row it fetches, are the same for all of a wave's instructions.
   const uint32_t chunk = (uint32_t)TA::chunk(0, wave, lane) * 16;
-  const uint32_t a_off = (uint32_t)(lane / (KS / 16)) * lda + chunk;
+  // SwiGLU: a's rows lie in the tokens' order; what they are is asked for with
+  // the tile's place, a tile ahead, and becomes the offsets of its loads.
+  uint32_t a_off[SW ? A_PW : 1];
+  int tok[SW ? A_PW : 1];
+  a_off[0] = (uint32_t)(lane / (KS / 16)) * lda + chunk;
   const uint32_t b_off = (uint32_t)(lane / (KS / 16)) * ldb + chunk;
 
   // Tile number k of this workgroup; false behind the last one.
@@ -179,8 +183,18 @@ gmm_i8_kernel(I8Args g) {
     const int per = g.nsplit > 1 ? (steps + g.nsplit - 1) / g.nsplit : steps;
     t.k_lo = min(t.split * per, steps), t.k_hi = min(steps, t.k_lo + per);
     t.r_end = min(g.K, t.k_hi * KS);
-    t.a_base = uni((const char*)g.a + (t.row0 + t.i0) * (int64_t)lda);
-    t.a_bytes = t.i_end > t.i0 ? (uint32_t)(t.i_end - t.i0 - 1) * lda + (uint32_t)g.K : 0u;
+    if constexpr (SW) {
+      t.a_base = (const char*)g.a;
+      t.a_bytes = g.a_bytes;
+#pragma unroll
+      for (int q = 0; q < A_PW; ++q) {
+        const int r = t.i0 + (wave + q * NW) * TA::RPI + lane / (KS / 16);
+        tok[q] = r < t.i_end ? g.tok[t.row0 + r] : -1;
+      }
+    } else {
+      t.a_base = uni((const char*)g.a + (t.row0 + t.i0) * (int64_t)lda);
+      t.a_bytes = t.i_end > t.i0 ? (uint32_t)(t.i_end - t.i0 - 1) * lda + (uint32_t)g.K : 0u;
+    }
     const int64_t at = ((int64_t)t.e * g.N + t.j0) * ldb;
     t.b_base = uni((const char*)g.b + at);
     t.b_base2 = SW ? uni((const char*)g.b2 + at) : nullptr;
@@ -206,10 +220,10 @@ gmm_i8_kernel(I8Args g) {
     const int i = wave + q * NW;
     const int left = t.r_end - ks * KS;
     const auto rs = descriptor(t.a_base, left > 0 ? t.a_bytes : 0u);
-    uint32_t off = a_off;
+    uint32_t off = a_off[SW ? q : 0];
     if (left < KS) off = (int)chunk < left ? off : kOutside;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(stage_a(sc) + i * 1024), 16, (int)off,
-                                             ks * KS + i * TA::RPI * (int)lda, 0, 0);
+                                             ks * KS + (SW ? 0 : i * TA::RPI * (int)lda), 0, 0);
   };
   auto load_b1 = [&](const Place& t, auto sc, int ks, int q, auto cache) {
     constexpr int AUX = decltype(cache)::value;
@@ -241,6 +255,10 @@ gmm_i8_kernel(I8Args g) {
   // A tile's first DA and DB steps, in the order in which the loop would
   // have asked for them.
   auto prologue = [&](const Place& t) {
+    if constexpr (SW) {
+#pragma unroll
+      for (int q = 0; q < A_PW; ++q) a_off[q] = tok[q] < 0 ? kOutside : (uint32_t)tok[q] * lda + chunk;
+    }
     auto one = [&](auto vc) {  // what step V of -DB .. -1 would load
       constexpr int V = decltype(vc)::value - DB;
       if constexpr (V + DA >= 0) {

@@ -1,5 +1,5 @@
-// 8-bit codes of rows, with a scale for each row; and the experts' rows of
-// codes gathered from the tokens'.
+// 8-bit codes of rows, with a scale for each row; and which token each of the
+// experts' rows is.
 //
 // A row is read once: it waits in registers while its largest magnitude is
 // found, one wave for short rows, a workgroup for long ones (the longest are
@@ -102,40 +102,26 @@ int launch_quantize(int dtype, const void* x, int64_t ldx, int M, int K, int8_t*
              : launch_quantize_t((const float*)x, ldx, M, K, q, ldq, scale, used, st);
 }
 
-// One wave per row, four 16-byte pieces in flight a lane (d is a multiple of
-// 64).
 __global__ void __launch_bounds__(256)
-gather_i8_kernel(const int8_t* __restrict__ xq, const float* __restrict__ xs,
-                 const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets, int n_ffn,
-                 int Tk, int k, int d, int8_t* __restrict__ rows, float* __restrict__ row_scale) {
-  const int lane = lane_id();
-  const int used = min(offsets[n_ffn], Tk), T = Tk / k;
-  for (int p = blockIdx.x * 4 + (threadIdx.x >> 6); p < used; p += gridDim.x * 4) {
+row_tokens_kernel(const float* __restrict__ xs, const int32_t* __restrict__ perm,
+                  const int32_t* __restrict__ offsets, int n_ffn, int Tk, int k,
+                  int32_t* __restrict__ tok, float* __restrict__ row_scale) {
+  const int used = min(offsets[n_ffn], Tk);
+  for (int p = blockIdx.x * 256 + threadIdx.x; p < used; p += gridDim.x * 256) {
     const int a = perm[p];
     const bool inside = (unsigned)a < (unsigned)Tk;
     MOE_CHECK(inside, MOE_CHECK_GEMM_ROW);
     const int t = inside ? a / k : 0;
-    const int8_t* from = xq + (size_t)t * d;
-    int8_t* to = rows + (size_t)p * d;
-    if (lane == 0) row_scale[p] = xs[t];
-    for (int c = lane * 16; c < d; c += 4096) {
-      u32x4_t v[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (c + u * 1024 < d) v[u] = ld16(from + c + u * 1024);
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (c + u * 1024 < d) st16(to + c + u * 1024, v[u]);
-    }
+    tok[p] = t;
+    row_scale[p] = xs[t];
   }
 }
 
-int launch_gather_i8(const int8_t* xq, const float* xs, const int32_t* perm, const int32_t* offsets,
-                     int n_ffn, int Tk, int k, int d, int8_t* rows, float* row_scale,
-                     hipStream_t st) {
-  const int blocks = (int)std::min<long>(((long)Tk + 3) / 4, 8192);
-  hipLaunchKernelGGL(gather_i8_kernel, dim3(blocks), dim3(256), 0, st, xq, xs, perm, offsets, n_ffn,
-                     Tk, k, d, rows, row_scale);
+int launch_row_tokens(const float* xs, const int32_t* perm, const int32_t* offsets, int n_ffn, int Tk,
+                      int k, int32_t* tok, float* row_scale, hipStream_t st) {
+  const int blocks = (int)std::min<long>(((long)Tk + 255) / 256, 2048);
+  hipLaunchKernelGGL(row_tokens_kernel, dim3(blocks), dim3(256), 0, st, xs, perm, offsets, n_ffn, Tk, k,
+                     tok, row_scale);
   return check_launch();
 }
 

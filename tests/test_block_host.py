@@ -186,11 +186,12 @@ def test_ffn_refuses():
     assert ffn(s, x=None, xq=A + 8, x_scale=A) == EALIGN
     assert K.lib().moe_expert_ffn_i8(ref(s), None, P(A), None) == EINVAL
     for bad, code in ((layer(T_=0), EINVAL), (layer(d=100), EUNSUPPORTED), (layer(T_=1 << 24), EUNSUPPORTED),
-                      (layer(d=1 << 17), EUNSUPPORTED), (layer(f=1 << 17), EUNSUPPORTED)):
+                      (layer(d=1 << 17), EUNSUPPORTED), (layer(f=1 << 17), EUNSUPPORTED),
+                      (layer(T_=1 << 20, d=2048, k=1), EUNSUPPORTED)):
         assert ffn(bad) == code
         assert K.moe_expert_ffn_i8_workspace_bytes(bad) == 0
     rows = 16 * 8
-    assert K.moe_expert_ffn_i8_workspace_bytes(s) >= 16 * 128 + rows * 128 + rows * 64 * 3
+    assert K.moe_expert_ffn_i8_workspace_bytes(s) >= 16 * 128 + rows * 64 * 3
 
 
 # ---- norms

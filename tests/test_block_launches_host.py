@@ -21,7 +21,7 @@ QUANT = [(1, 1), ((1 << 27) - 1, 131071), ((1 << 27) - 1, 64), (0, 8)]
 PRODUCT = [(1, 1, 1, 1), (1, (1 << 27) - 1, 1 << 20, 131071), (1024, (1 << 27) - 1, 1 << 20, 131056), (7, 0, 64, 64), (1, 3, 64, 131056),
            (1024, 5, 1 << 20, 15)]
 # T, d, n, z, f, k
-FFN = [(1, 64, 1, 0, 64, 1), ((1 << 27) - 1, 64, 1, 0, 64, 1), ((1 << 23) - 1, 131008, 700, 300, 131008, 16)]
+FFN = [(1, 64, 1, 0, 64, 1), ((1 << 25) - 1025, 64, 3, 0, 64, 3), (16380, 131008, 700, 300, 131008, 16)]
 # T, d, tokens a gate row
 NORM = [(1, 1, 1), ((1 << 27) - 1, 32768, 1), ((1 << 27) - 1, 1, (1 << 31) - 1), ((1 << 27) - 1, 32761, 3), (0, 64, 1)]
 
