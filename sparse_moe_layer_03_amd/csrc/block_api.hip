@@ -111,15 +111,17 @@ static int check_i8(const moe_i8_shape* s) {
   return MOE_OK;
 }
 
-// A product with too few tiles to fill the chip has its reduction cut into this
-// many ranges of at least 512 codes each; their sums are joined by a second
-// kernel.  A function of the sizes and the device's CU count only: it sizes the
-// workspace.
+// A product with too few tiles to give every second CU one has its reduction cut
+// into as many ranges, of at least 512 codes each, as make two tiles a CU; their
+// sums are joined by a second kernel.  A function of the sizes and the device's CU
+// count only: it sizes the workspace.
 static int i8_nsplit(const moe_i8_shape* s, int cus) {
-  const long G = s->n_groups, M = s->M, jt = ((long)s->N + 127) / 128;
-  const long tiles = (M / 128 + std::min(G, M)) * jt;
-  if (tiles < 1) return 1;
-  return (int)std::max(1l, std::min({32l, cus / tiles, (long)s->K / 512}));
+  const long G = s->n_groups, M = s->M;
+  // the smallest tiles of the kernels
+  const long wide = i8_mfma_ok(s->N, s->K, s->lda, s->ldc) ? 128 : 64;
+  const long tiles = (M / 64 + std::min(G, M)) * ((s->N + wide - 1) / wide);
+  if (tiles < 1 || 2 * tiles > cus) return 1;
+  return (int)std::max(1l, std::min({32l, 2l * cus / tiles, (long)s->K / 512}));
 }
 
 static size_t i8_part_bytes(const moe_i8_shape* s, int nsplit) {

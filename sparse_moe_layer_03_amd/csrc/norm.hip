@@ -16,12 +16,27 @@
 // group's first gate row) or 1 (its last).
 
 #include <algorithm>
+#include <type_traits>
 
 #include "block.h"
 #include "common.h"
 #include "row_io.h"
 
 namespace moe {
+
+// f(type, rows of whole chunks, rows that are not kept in the caches): arrays that
+// L2 (4 MiB an XCD) cannot hold for the next kernel anyway are loaded and stored
+// non-temporally (16384 rows of 6144: 153 -> 145 us).
+template <typename F>
+static int dispatch(const moe_norm_shape& s, F f) {
+  const bool bf16 = s.dtype == MOE_BF16, whole = s.d_model % kChunk == 0;
+  const bool once = (size_t)s.T * s.d_model * (bf16 ? 2 : 4) > (32u << 20);
+  const std::true_type yes;
+  const std::false_type no;
+  if (!whole) return bf16 ? f((__bf16)0.f, no, no) : f(0.f, no, no);
+  if (once) return bf16 ? f((__bf16)0.f, yes, yes) : f(0.f, yes, yes);
+  return bf16 ? f((__bf16)0.f, yes, no) : f(0.f, yes, no);
+}
 
 struct NormArgs {
   const char *x, *y, *w_post, *gate, *w_pre;
@@ -34,7 +49,7 @@ struct NormArgs {
 };
 
 // N chunks a thread; ALONE: one wave per row.
-template <typename T, int N, bool ALONE, int NT, bool WHOLE>
+template <typename T, int N, bool ALONE, int NT, bool WHOLE, bool ONCE>
 __global__ void __launch_bounds__(NT) norm_kernel(NormArgs a) {
   __shared__ uint32_t s[96];
   int turn = 0;
@@ -50,8 +65,8 @@ __global__ void __launch_bounds__(NT) norm_kernel(NormArgs a) {
   auto load = [&](int row) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (y != nullptr) ry[i] = load_chunk<WHOLE>(y + row * a.ldy, tid + i * nt, d);
-      if (x != nullptr) rx[i] = load_chunk<WHOLE>(x + row * a.ldx, tid + i * nt, d);
+      if (y != nullptr) ry[i] = load_chunk<WHOLE, ONCE>(y + row * a.ldy, tid + i * nt, d);
+      if (x != nullptr) rx[i] = load_chunk<WHOLE, ONCE>(x + row * a.ldx, tid + i * nt, d);
     }
   };
   load(t);
@@ -115,7 +130,7 @@ __global__ void __launch_bounds__(NT) norm_kernel(NormArgs a) {
     if (a.r != nullptr) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if ((tid + i * nt) * kChunk < d) store_chunk<WHOLE>((T*)a.r + t * a.ldr, tid + i * nt, d, out[i]);
+        if ((tid + i * nt) * kChunk < d) store_chunk<WHOLE, ONCE>((T*)a.r + t * a.ldr, tid + i * nt, d, out[i]);
     }
     if (a.w_pre != nullptr) {
       sum = row_sum<ALONE, NT>(sum, s, turn);
@@ -130,7 +145,7 @@ __global__ void __launch_bounds__(NT) norm_kernel(NormArgs a) {
         for (int k = 0; k < 8; ++k) v[k] = v[k] * inv * f[k];
         out[i] = raw_of(v, (T*)nullptr);
         if (a.h != nullptr && (tid + i * nt) * kChunk < d)
-          store_chunk<WHOLE>((T*)a.h + t * a.ldh, tid + i * nt, d, out[i]);
+          store_chunk<WHOLE, ONCE>((T*)a.h + t * a.ldh, tid + i * nt, d, out[i]);
         if (a.q != nullptr) {
           floats(out[i], v);
 #pragma unroll
@@ -153,7 +168,7 @@ __global__ void __launch_bounds__(NT) norm_kernel(NormArgs a) {
   }
 }
 
-template <typename T, bool WHOLE>
+template <typename T, bool WHOLE, bool ONCE>
 static int launch_norm_t(const NormArgs& a, hipStream_t st) {
   const int cus = stream_cu_count(st);
   if (cus <= 0) return MOE_EHIP;
@@ -162,7 +177,7 @@ static int launch_norm_t(const NormArgs& a, hipStream_t st) {
   do {                                                                                          \
     const int per = ALONE ? NT / 64 : 1;                                                        \
     const long blocks = std::min<long>(((long)a.T + per - 1) / per, (long)cus * (2048 / NT));   \
-    hipLaunchKernelGGL((norm_kernel<T, N, ALONE, NT, WHOLE>), dim3((unsigned)blocks), dim3(NT), 0, st, a); \
+    hipLaunchKernelGGL((norm_kernel<T, N, ALONE, NT, WHOLE, ONCE>), dim3((unsigned)blocks), dim3(NT), 0, st, a); \
   } while (0)
   if (chunks <= 64) MOE_NORM(1, true, 256);
   else if (chunks <= 128) MOE_NORM(2, true, 256);
@@ -197,10 +212,9 @@ int launch_norm(const moe_norm_shape& s, const moe_norm_io& io, hipStream_t st) 
   a.T = s.T;
   a.d = s.d_model;
   a.per_gate = s.rows_per_gate;
-  const bool whole = s.d_model % kChunk == 0;
-  if (s.dtype == MOE_BF16)
-    return whole ? launch_norm_t<__bf16, true>(a, st) : launch_norm_t<__bf16, false>(a, st);
-  return whole ? launch_norm_t<float, true>(a, st) : launch_norm_t<float, false>(a, st);
+  return dispatch(s, [&](auto type, auto whole, auto once) {
+    return launch_norm_t<decltype(type), decltype(whole)::value, decltype(once)::value>(a, st);
+  });
 }
 
 // ---- backward
@@ -215,7 +229,7 @@ struct NormBwdArgs {
   int accumulate;
 };
 
-template <typename T, int N, bool ALONE, int NT, bool WHOLE>
+template <typename T, int N, bool ALONE, int NT, bool WHOLE, bool ONCE>
 __global__ void __launch_bounds__(NT, N == 1 && NT <= 512 ? 4 : 1) norm_bwd_kernel(NormBwdArgs a) {
   __shared__ uint32_t s[96];
   int turn = 0;
@@ -236,19 +250,28 @@ __global__ void __launch_bounds__(NT, N == 1 && NT <= 512 ? 4 : 1) norm_bwd_kern
       for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
   };
   clear(s_pre), clear(s_post), clear(s_gate);
-  auto load = [&](int row) {
+  // (each as soon as its registers are free: a row behind the last one is not
+  // asked for)
+  auto load_r = [&](int row) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = tid + i * nt;
       if (pre) {
-        rr[i] = load_chunk<WHOLE>((const T*)a.r + row * a.ldr, c, d);
-        rdh[i] = load_chunk<WHOLE>((const T*)a.dh + row * a.lddh, c, d);
+        rr[i] = load_chunk<WHOLE, ONCE>((const T*)a.r + row * a.ldr, c, d);
+        rdh[i] = load_chunk<WHOLE, ONCE>((const T*)a.dh + row * a.lddh, c, d);
       }
-      if (y != nullptr) ry[i] = load_chunk<WHOLE>(y + row * a.ldy, c, d);
-      if (a.dr != nullptr) rdr[i] = load_chunk<WHOLE>((const T*)a.dr + row * a.lddr, c, d);
+      if (a.dr != nullptr) rdr[i] = load_chunk<WHOLE, ONCE>((const T*)a.dr + row * a.lddr, c, d);
     }
   };
-  if (lo < hi) load(lo);
+  auto load_y = [&](int row) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (y != nullptr) ry[i] = load_chunk<WHOLE, ONCE>(y + row * a.ldy, tid + i * nt, d);
+  };
+  if (lo < hi) {
+    load_r(lo);
+    load_y(lo);
+  }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     if (post) wp[i] = load_chunk<WHOLE>((const T*)a.w_post, tid + i * nt, d);
@@ -318,7 +341,7 @@ __global__ void __launch_bounds__(NT, N == 1 && NT <= 512 ? 4 : 1) norm_bwd_kern
         float v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = a.res_scale * g[i][k];
-        store_chunk<WHOLE>((T*)a.dx + t * a.lddx, tid + i * nt, d, raw_of(v, (T*)nullptr));
+        store_chunk<WHOLE, ONCE>((T*)a.dx + t * a.lddx, tid + i * nt, d, raw_of(v, (T*)nullptr));
       }
       if (y != nullptr) {
         float v[8], w[8], q[8];
@@ -342,6 +365,7 @@ __global__ void __launch_bounds__(NT, N == 1 && NT <= 512 ? 4 : 1) norm_bwd_kern
         }
       }
     }
+    if (t + 1 < hi) load_r(t + 1);
     if (y != nullptr) {
       float mean = 0.f;
       if (post) mean = row_sum<ALONE, NT>(cn, s, turn) * over;
@@ -357,10 +381,10 @@ __global__ void __launch_bounds__(NT, N == 1 && NT <= 512 ? 4 : 1) norm_bwd_kern
           for (int k = 0; k < 8; ++k) v[k] = g[i][k];
         }
         if ((tid + i * nt) * kChunk < d)
-          store_chunk<WHOLE>((T*)a.dy + t * a.lddy, tid + i * nt, d, raw_of(v, (T*)nullptr));
+          store_chunk<WHOLE, ONCE>((T*)a.dy + t * a.lddy, tid + i * nt, d, raw_of(v, (T*)nullptr));
       }
     }
-    if (t + 1 < hi) load(t + 1);
+    if (t + 1 < hi) load_y(t + 1);
     // the end of a gate row, or of this group
     if (a.dgate != nullptr) {
       const int at = t / a.per_gate;
@@ -487,13 +511,13 @@ size_t norm_bwd_ws_bytes(const moe_norm_shape& s, int cus) {
   return 256 + 4 * up256((size_t)norm_bwd_groups(s.T, s.d_model, cus) * s.d_model * 4);
 }
 
-template <typename T, bool WHOLE>
+template <typename T, bool WHOLE, bool ONCE>
 static int launch_norm_bwd_t(const NormBwdArgs& a, hipStream_t st) {
   const int chunks = (a.d + kChunk - 1) / kChunk;
 #define MOE_NORM_BWD(N, ALONE, NT)                                                                 \
   do {                                                                                             \
     const int per = ALONE ? NT / 64 : 1;                                                           \
-    hipLaunchKernelGGL((norm_bwd_kernel<T, N, ALONE, NT, WHOLE>),                                        \
+    hipLaunchKernelGGL((norm_bwd_kernel<T, N, ALONE, NT, WHOLE, ONCE>),                                        \
                        dim3((unsigned)((a.groups + per - 1) / per)), dim3(NT), 0, st, a);                                                        \
   } while (0)
   if (chunks <= 64) MOE_NORM_BWD(1, true, 256);
@@ -542,12 +566,9 @@ int launch_norm_bwd(const moe_norm_shape& s, const moe_norm_grad_io& io, void* w
   a.p_post = io.dw_post ? base + each / 4 : nullptr;
   a.p_gate = base + each / 2;
   if (s.T > 0) {
-    const bool whole = s.d_model % kChunk == 0;
-    int rc;
-    if (s.dtype == MOE_BF16)
-      rc = whole ? launch_norm_bwd_t<__bf16, true>(a, st) : launch_norm_bwd_t<__bf16, false>(a, st);
-    else
-      rc = whole ? launch_norm_bwd_t<float, true>(a, st) : launch_norm_bwd_t<float, false>(a, st);
+    const int rc = dispatch(s, [&](auto type, auto whole, auto once) {
+      return launch_norm_bwd_t<decltype(type), decltype(whole)::value, decltype(once)::value>(a, st);
+    });
     if (rc) return rc;
   }
   NormSumArgs b{};

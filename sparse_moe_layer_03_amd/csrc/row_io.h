@@ -3,6 +3,8 @@
 // kernels of the norms and of the 8-bit codes.
 #pragma once
 
+#include <type_traits>
+
 #include "../../include/moe.h"
 #include "common.h"
 #include "wave.h"
@@ -66,23 +68,32 @@ __device__ __forceinline__ Raw<T> zero_raw() {
   return r;
 }
 
-template <typename T>
+// ONCE: rows that one kernel reads or writes once need not stay in the caches.
+template <bool ONCE = false, typename T>
 __device__ __forceinline__ Raw<T> load_raw(const T* p) {
   Raw<T> r;
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-    r.v[i] = *reinterpret_cast<const u32x4_any_t*>((const char*)p + 16 * i);
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+    const u32x4_any_t* q = reinterpret_cast<const u32x4_any_t*>((const char*)p + 16 * i);
+    r.v[i] = ONCE ? __builtin_nontemporal_load(q) : *q;
+  }
   return r;
 }
 
 // Chunk c of a row of n values, zeros behind its end: the row's last chunk is
 // loaded from its last 8 values, and what it has too much in front dropped.
-// WHOLE: rows of whole chunks.
-template <bool WHOLE = false, typename T>
+// WHOLE: rows of whole chunks.  (Unsigned byte offsets from the row's start,
+// which is the same for all lanes, take one register; an index takes two.)
+template <typename T>
+__device__ __forceinline__ T* chunk_at(T* row, int c) {
+  typedef typename std::conditional<std::is_const<T>::value, const char, char>::type B;
+  return (T*)((B*)row + (uint32_t)c * (uint32_t)(kChunk * sizeof(T)));
+}
+template <bool WHOLE = false, bool ONCE = false, typename T>
 __device__ __forceinline__ Raw<T> load_chunk(const T* row, int c, int n) {
   const int at = c * kChunk;
-  if (WHOLE) return at < n ? load_raw(row + at) : zero_raw<T>();
-  if (at + kChunk <= n) return load_raw(row + at);
+  if (WHOLE) return at < n ? load_raw<ONCE>(chunk_at(row, c)) : zero_raw<T>();
+  if (at + kChunk <= n) return load_raw<ONCE>(chunk_at(row, c));
   if (at >= n) return zero_raw<T>();
   if (n >= kChunk) return drop(load_raw(row + n - kChunk), at + kChunk - n);
   T e[kChunk];
@@ -111,13 +122,16 @@ __device__ __forceinline__ Raw<float> raw_of(const float* f, float*) {
 }
 
 // (c begins inside the row)
-template <bool WHOLE = false, typename T>
+template <bool WHOLE = false, bool ONCE = false, typename T>
 __device__ __forceinline__ void store_chunk(T* row, int c, int n, const Raw<T>& r) {
   const int at = c * kChunk;
   if (WHOLE || at + kChunk <= n) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-      *reinterpret_cast<u32x4_any_t*>((char*)(row + at) + 16 * i) = r.v[i];
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      u32x4_any_t* q = reinterpret_cast<u32x4_any_t*>((char*)chunk_at(row, c) + 16 * i);
+      if (ONCE) __builtin_nontemporal_store(r.v[i], q);
+      else *q = r.v[i];
+    }
   } else {
     T e[kChunk];
     __builtin_memcpy(e, &r, sizeof r);
@@ -162,7 +176,7 @@ __device__ __forceinline__ u32x2_t codes_of(const float* f, float scale) {
 __device__ __forceinline__ void store_codes(int8_t* row, int c, int n, u32x2_t v) {
   const int at = c * kChunk;
   if (at + kChunk <= n) {
-    *reinterpret_cast<u32x2_byte_t*>(row + at) = v;
+    *reinterpret_cast<u32x2_byte_t*>(chunk_at(row, c)) = v;
   } else {
 #pragma unroll
     for (int k = 0; k < kChunk - 1; ++k)
