@@ -68,7 +68,8 @@ typedef struct {
  *         renorm_eps) (0 where that divisor is 0)
  * The selection is that of keys computed in 64 bits: keys too close for fp32
  * to tell apart are computed again.  Scores and gates are fp32.
- *   logits [T, E] fp32, ld_logits >= E elements from row to row; bias [E] fp32.
+ *   logits [T, E] fp32, E <= ld_logits < 2^24 elements from row to row; bias
+ *   [E] fp32.
  * An expert with bias -inf is taken only where the kept groups have fewer than
  * top_k others, and does not count in its group's sum; one with +inf comes
  * before all others, its group before other groups.  A NaN key ranks as -inf.  A logit of -inf has p = 0, also in
@@ -97,7 +98,7 @@ int moe_route_select(const moe_shape* shape, const moe_select_params* params, co
  * selection that moe_select did not make), 0 for other experts.  Selection
  * and bias have no gradient.  A slot whose id is outside [0, E) counts as an
  * expert of score 0.
- *   logits [T, E] fp32, ld_logits >= E; topk_idx, dgate [T, top_k];
+ *   logits [T, E] fp32, ld_logits as there; topk_idx, dgate [T, top_k];
  *   dlogits [T, E] fp32, contiguous. */
 int moe_select_backward(const moe_shape* shape, const moe_select_params* params,
                         const float* logits, int64_t ld_logits, const int32_t* topk_idx,
@@ -233,7 +234,9 @@ typedef struct {
  * in fp32; r is rounded to dtype and h is the norm of the rounded r.  Absent
  * parts fall out: without y the call is the norm before the first block, h =
  * x rstd(x) w_pre (x needed, res_scale 1, w_post, gate and r absent); without
- * x the residual term is missing.  q and q_scale are moe_quantize_rows of h.
+ * x the residual term is missing.  The sums of squares are fp32: they overflow
+ * in rows of values beyond some 1e19 / sqrt(d_model), and with eps 0 a row of
+ * zeros has no rstd.  q and q_scale are moe_quantize_rows of h.
  * r may be x itself (same p and ld).  16-byte aligned arrays, any strides. */
 int moe_norm_residual(const moe_norm_shape* shape, const moe_norm_io* io, void* stream);
 

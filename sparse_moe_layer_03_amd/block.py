@@ -251,7 +251,7 @@ def make_quant_shape(dtype, M, K, ldx=None, ldq=None) -> MoeQuantShape:
 def _strided(name, t, dtype, rows, width, ld, dev):
     """The address of rows x width values, `ld` elements between rows."""
     p, have = _matrix(name, t, dtype, rows, width, dev)
-    if have != ld and t.shape[0] > 1:
+    if t is not None and have != ld and t.shape[0] > 1:
         _refuse(name, t, f"{ld} elements between rows", dev)
     return p
 

@@ -24,26 +24,35 @@ static int elem_size(int dtype) { return dtype == MOE_BF16 ? 2 : 4; }
 struct Arrays {
   struct Span {
     uintptr_t from, to;
-    int64_t ld;
+    size_t step, width;  // bytes between rows and of a row; 0: one piece
     bool written, may_alias;
   };
   Span s[16];
   int n = 0;
-  void add(const void* p, size_t bytes, bool written, int64_t ld = 0, bool may_alias = false) {
+  void add(const void* p, size_t bytes, bool written) {
     if (p == nullptr || bytes == 0) return;
-    s[n++] = Span{(uintptr_t)p, (uintptr_t)p + bytes, ld, written, may_alias};
+    s[n++] = Span{(uintptr_t)p, (uintptr_t)p + bytes, 0, 0, written, false};
   }
-  void rows(const moe_rows& r, int M, int width, int size, bool written, bool may_alias) {
-    if (M > 0) add(r.p, ((size_t)(M - 1) * r.ld + width) * size, written, r.ld, may_alias);
+  void rows(const void* p, int64_t ld, int M, int width, int size, bool written, bool may_alias) {
+    if (p == nullptr || M == 0) return;
+    const size_t step = (size_t)ld * size, wide = (size_t)width * size;
+    s[n++] = Span{(uintptr_t)p, (uintptr_t)p + (size_t)(M - 1) * step + wide, step, wide, written, may_alias};
+  }
+  static bool apart(const Span& a, const Span& b) {
+    if (a.from >= b.to || b.from >= a.to) return true;
+    // columns of one wider matrix
+    if (a.step == 0 || a.step != b.step) return false;
+    const Span &lo = a.from <= b.from ? a : b, &hi = a.from <= b.from ? b : a;
+    const size_t at = (hi.from - lo.from) % a.step;
+    return at >= lo.width && at + hi.width <= a.step;
   }
   int check() const {
     for (int i = 0; i < n; ++i)
       for (int j = 0; j < i; ++j) {
-        if (!s[i].written && !s[j].written) continue;
-        if (s[i].from >= s[j].to || s[j].from >= s[i].to) continue;
+        if ((!s[i].written && !s[j].written) || apart(s[i], s[j])) continue;
         // an output in an input's place
         if (s[i].written != s[j].written && s[i].may_alias && s[j].may_alias &&
-            s[i].from == s[j].from && s[i].ld == s[j].ld)
+            s[i].from == s[j].from && s[i].step == s[j].step)
           continue;
         return MOE_EINVAL;
       }
@@ -202,10 +211,11 @@ int moe_select(const moe_shape* s, const moe_select_params* p, const float* logi
   const int rc = check_select(s, p);
   if (rc) return rc;
   if (!logits || !topk_idx || !topk_gate || ld_logits < s->n_ffn + s->n_zero) return MOE_EINVAL;
+  if (ld_logits >= (1 << 24)) return MOE_EUNSUPPORTED;
   if (!al4(logits) || !al4(bias) || !al4(topk_idx) || !al4(topk_gate)) return MOE_EALIGN;
   const size_t T = s->T, E = (size_t)s->n_ffn + s->n_zero;
   Arrays v;
-  v.add(logits, ((T - 1) * ld_logits + E) * 4, false);
+  v.rows(logits, ld_logits, s->T, (int)E, 4, false, false);
   v.add(bias, E * 4, false);
   v.add(topk_idx, T * s->top_k * 4, true);
   v.add(topk_gate, T * s->top_k * 4, true);
@@ -247,10 +257,11 @@ int moe_select_backward(const moe_shape* s, const moe_select_params* p, const fl
   if (rc) return rc;
   if (!logits || !topk_idx || !dgate || !dlogits || ld_logits < s->n_ffn + s->n_zero)
     return MOE_EINVAL;
+  if (ld_logits >= (1 << 24)) return MOE_EUNSUPPORTED;
   if (!al4(logits) || !al4(topk_idx) || !al4(dgate) || !al4(dlogits)) return MOE_EALIGN;
   const size_t T = s->T, E = (size_t)s->n_ffn + s->n_zero;
   Arrays v;
-  v.add(logits, ((T - 1) * ld_logits + E) * 4, false);
+  v.rows(logits, ld_logits, s->T, (int)E, 4, false, false);
   v.add(topk_idx, T * s->top_k * 4, false);
   v.add(dgate, T * s->top_k * 4, false);
   v.add(dlogits, T * E * 4, true);
@@ -286,8 +297,8 @@ int moe_quantize_rows(const moe_quant_shape* s, const void* x, int8_t* q, float*
   if (s->M > 0 && (!x || !q || !scale)) return MOE_EINVAL;
   if (!al16(x) || !al16(q) || !al4(scale)) return MOE_EALIGN;
   Arrays v;
-  v.rows(moe_rows{(void*)x, s->ldx}, s->M, s->K, elem_size(s->dtype), false, false);
-  v.rows(moe_rows{(void*)q, s->ldq}, s->M, s->K, 1, true, false);
+  v.rows(x, s->ldx, s->M, s->K, elem_size(s->dtype), false, false);
+  v.rows(q, s->ldq, s->M, s->K, 1, true, false);
   v.add(scale, (size_t)s->M * 4, true);
   if (const int bad = v.check()) return bad;
   return launch_quantize(s->dtype, x, s->ldx, s->M, s->K, q, s->ldq, scale, nullptr,
@@ -317,12 +328,12 @@ int moe_matmul_i8(const moe_i8_shape* s, const int32_t* offsets, const int8_t* a
   if (g.nsplit > 1 && !ws) return MOE_EINVAL;
   if (none) return MOE_OK;
   Arrays v;
-  v.rows(moe_rows{(void*)a, s->lda}, s->M, s->K, 1, false, false);
+  v.rows(a, s->lda, s->M, s->K, 1, false, false);
   v.add(a_scale, (size_t)s->M * 4, false);
   v.add(w, (size_t)s->n_groups * s->N * s->K, false);
   v.add(w_scale, (size_t)s->n_groups * s->N * 4, false);
   v.add(offsets, ((size_t)s->n_groups + 1) * 4, false);
-  v.rows(moe_rows{c, s->ldc}, s->M, s->N, elem_size(s->out_dtype), true, false);
+  v.rows(c, s->ldc, s->M, s->N, elem_size(s->out_dtype), true, false);
   v.add(ws, i8_part_bytes(s, g.nsplit), true);
   if (const int bad = v.check()) return bad;
   g.a = a;
@@ -447,10 +458,10 @@ int moe_norm_residual(const moe_norm_shape* s, const moe_norm_io* io, void* stre
   const int T = s->T, d = s->d_model, es = elem_size(s->dtype);
   const size_t vec = (size_t)d * es, gates = ((size_t)T + s->rows_per_gate - 1) / s->rows_per_gate;
   Arrays v;
-  v.rows(io->x, T, d, es, false, true);
-  v.rows(io->r, T, d, es, true, true);
-  v.rows(io->y, T, d, es, false, false);
-  v.rows(io->h, T, d, es, true, false);
+  v.rows(io->x.p, io->x.ld, T, d, es, false, true);
+  v.rows(io->r.p, io->r.ld, T, d, es, true, true);
+  v.rows(io->y.p, io->y.ld, T, d, es, false, false);
+  v.rows(io->h.p, io->h.ld, T, d, es, true, false);
   v.add(io->w_post, vec, false);
   v.add(io->gate, gates * vec, false);
   v.add(io->w_pre, vec, false);
@@ -491,12 +502,12 @@ int moe_norm_residual_backward(const moe_norm_shape* s, const moe_norm_grad_io* 
   const int T = s->T, d = s->d_model, es = elem_size(s->dtype);
   const size_t vec = (size_t)d * es, gates = ((size_t)T + s->rows_per_gate - 1) / s->rows_per_gate;
   Arrays v;
-  v.rows(io->r, T, d, es, false, true);
-  v.rows(io->y, T, d, es, false, true);
-  v.rows(io->dr, T, d, es, false, true);
-  v.rows(io->dh, T, d, es, false, true);
-  v.rows(io->dx, T, d, es, true, true);
-  v.rows(io->dy, T, d, es, true, true);
+  v.rows(io->r.p, io->r.ld, T, d, es, false, true);
+  v.rows(io->y.p, io->y.ld, T, d, es, false, true);
+  v.rows(io->dr.p, io->dr.ld, T, d, es, false, true);
+  v.rows(io->dh.p, io->dh.ld, T, d, es, false, true);
+  v.rows(io->dx.p, io->dx.ld, T, d, es, true, true);
+  v.rows(io->dy.p, io->dy.ld, T, d, es, true, true);
   v.add(io->w_post, vec, false);
   v.add(io->gate, gates * vec, false);
   v.add(io->w_pre, vec, false);

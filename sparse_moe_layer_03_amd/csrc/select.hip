@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(256, PL <= 12 ? 5 : 2) select_kernel(SelectArg
   // which grows with p up to p = P, where |l - m| <= -log P (or 1); the sum's
   // PL + 6 additions and a few steps more.
   auto margin = [&](float cut) {
-    const float P = fabsf(cut) + top;
+    const float P = fmaxf(fabsf(cut) + top, 1e-30f);  // (its logarithm is finite)
     const float steps = softmax ? fmaxf(1.f, -0.6931472f * __builtin_amdgcn_logf(P)) + (PL + 14) : 8.f;
     return steps * 0x1p-23f * P + 1e-36f;  // (scores below fp32's normal numbers)
   };
@@ -391,16 +391,18 @@ __global__ void __launch_bounds__(256, PL <= 12 ? 5 : 2) select_kernel(SelectArg
     for (int b = 0; b < 5; ++b)  // (at most 16)
       pos += __popcll(__ballot(__popc(chosen) >> b & 1) & lanemask_lt()) << b;
     while (chosen != 0) {
-      if (MOE_GUARD(pos < a.k, MOE_CHECK_ROUTE_ID)) s_id[wave][pos] = w.expert(__ffs(chosen) - 1);
+      MOE_CHECK(pos < a.k, MOE_CHECK_ROUTE_ID);
+      if (pos < a.k) s_id[wave][pos] = w.expert(__ffs(chosen) - 1);
       ++pos;
       chosen &= chosen - 1;
     }
     __builtin_amdgcn_wave_barrier();
-    const int id = lane < a.k ? s_id[wave][lane] : 0;
+    int id = lane < a.k ? s_id[wave][lane] : 0;
     __builtin_amdgcn_wave_barrier();
     int at = 0;
     for (int q = 0; q < a.k; ++q) at += (int)lane_value((uint32_t)id, q) < id;
-    MOE_CHECK(id < a.E, MOE_CHECK_ROUTE_ID);
+    MOE_CHECK((unsigned)id < (unsigned)a.E, MOE_CHECK_ROUTE_ID);
+    id = min(max(id, 0), a.E - 1);
     const float l = row[id];
     float f = softmax ? exp_fast(l - m) * inv : __builtin_amdgcn_rcpf(1.f + exp_fast(-l));
     if (a.renorm) {

@@ -96,6 +96,7 @@ def test_selection_refuses_shapes_and_pointers():
         assert route(s, K.make_select()) == code
     p = rule()
     assert select(layer(), p, ld=95) == EINVAL and select_bwd(layer(), p, ld=95) == EINVAL
+    assert select(layer(), p, ld=1 << 24) == EUNSUPPORTED and select_bwd(layer(), p, ld=1 << 24) == EUNSUPPORTED
     for n in ("logits", "idx", "gate"):
         assert select(layer(), p, **{n: 0}) == EINVAL and select(layer(), p, **{n: A + 2}) == EALIGN, n
     assert select(layer(), p, bias=A + 2) == EALIGN
@@ -302,6 +303,18 @@ def test_norm_refuses_overlaps(out, other):
     assert norm(**{n: R(v) if n in rows else v for n, v in at.items()}) == EINVAL
     at[out] = at[other] + bytes_[other] - 16
     assert norm(**{n: R(v) if n in rows else v for n, v in at.items()}) == EINVAL
+
+
+def test_columns_of_one_matrix_do_not_overlap():
+    """x, y, r and h side by side in rows of 4 * 64 elements: no overlap; one
+    element too wide, or another stride: refused.  (EHIP: there is no GPU here.)"""
+    side = {n: R(A + i * 128, 256) for i, n in enumerate(("x", "y", "r", "h"))}
+    far = dict(w_post=1 << 40, gate=2 << 40, w_pre=3 << 40, q=4 << 40, q_scale=5 << 40)
+    assert norm(**side, **far) == EHIP
+    assert norm(**{**side, "r": R(A + 240, 256)}, **far) == EINVAL
+    assert norm(**{**side, "r": R(A + 256, 264)}, **far) == EINVAL
+    assert norm(**{**side, "r": R(A, 256)}, **far) == EHIP              # in the residual's place
+    assert norm(**{**side, "r": R(A + 128, 256)}, **far) == EINVAL      # not in y's
 
 
 def test_products_and_selections_refuse_overlaps():

@@ -134,6 +134,20 @@ def test_masked_logits(r, low):
         assert (gate[3] == 0).all()
 
 
+@pytest.mark.parametrize("r", RULES)
+def test_masked_logits_without_a_bias(r):
+    """Fewer experts than slots are left: the others' keys are all 0."""
+    T, E, k = 64, 96, 8
+    g = torch.Generator(device="cuda").manual_seed(13)
+    logits = torch.full((T, E), -math.inf, device="cuda")
+    for t in range(T):
+        n = t % 9
+        logits[t, torch.randperm(E, generator=g, device="cuda")[:n]] = torch.randn(n, generator=g, device="cuda")
+    check(T, E, k, r, logits=logits, bias=None)
+    check(T, E, k, r, logits=logits, bias=torch.zeros(E, device="cuda"))
+    check(T, E, k, r, logits=logits, bias=torch.full((E,), 1e38, device="cuda"))
+
+
 def test_non_finite_logits():
     T, E, k = 6, 32, 4
     logits = torch.randn((T, E), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
