@@ -497,7 +497,12 @@ __global__ void __launch_bounds__(256) select_bwd_kernel(SelectBwdArgs a) {
       const float whole = wave_sum_f(sel) + a.eps;
       const float r = whole == 0.f ? 0.f : 1.f / whole;
       const float f = wave_sum_f(dg * sel) * r;
-      d = lane < a.k ? a.scaling * (dg - f) * r : 0.f;
+      // D (dg_j - f) = sum_i p_i (dg_j - dg_i) + eps dg_j: what dg has in common
+      // over the slots falls out of the differences and leaves no rounding
+      // behind (one slot and eps 0: the gate is a constant, its gradient 0)
+      float apart = a.eps * dg;
+      for (int q = 0; q < a.k; ++q) apart += lane_value(sel, q) * (dg - lane_value(dg, q));
+      d = lane < a.k ? a.scaling * (apart * r) * r : 0.f;
       // sum_j p_j dp_j without its cancellation: sum p (dg - f) = f (D - sum p)
       c = a.scaling * f * (a.eps * r);
     } else {

@@ -253,6 +253,35 @@ def test_gradient_of_odd_selections(r):
     assert (out[5] == 0).all()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k", [(70, 96, 1), (33, 700, 1), (50, 96, 2), (300, 768, 12)])
+def test_gradient_of_renormalised_gates_with_a_common_part(score, T, E, k):
+    """Gates that sum to a constant: what dgate has in common over a token's
+    slots has no gradient, and of one slot's nothing is left."""
+    say(f"[select_backward, common part] T={T} E={E} k={k} {score}")
+    g = torch.Generator(device="cuda").manual_seed(13)
+    logits = torch.randn((T, E), generator=g, device="cuda")
+    p = K.make_select(score, renorm=True)
+    idx = select_ref(p, logits, None, k, 2.5)[0]
+    dgate = 1000 + torch.randn((T, k), generator=g, device="cuda")
+    out = torch.full((T, E), math.nan, device="cuda")
+    K.moe_select_backward(shape(T, E, k, 2.5), p, logits, idx.to(torch.int32), dgate, out)
+    x, dg = logits.double(), dgate.double()
+    s = torch.sigmoid(x) if p.score else torch.softmax(x, 1)
+    f = s.gather(1, idx)
+    apart = dg[:, :, None] - dg[:, None, :]
+    whole = f.sum(1, keepdim=True)
+    d, mag = ((v * f[:, None, :]).sum(2) * 2.5 / whole ** 2 for v in (apart, apart.abs()))
+    by = f * (1 - f) if p.score else f
+    ref = torch.zeros_like(x).scatter_(1, idx, by * d)
+    bound = torch.zeros_like(x).scatter_(1, idx, by * mag)
+    # each score's error in p and in the two factors 1 / D, in every term of
+    # the sum; the differences' and the sum's roundings are a few of the 8
+    assert ((out.double() - ref).abs() <= 8 * score_error(p, logits) * bound).all()
+    if k == 1:
+        assert (out == 0).all()
+
+
 # ---- router, streams, graphs
 
 
