@@ -121,16 +121,19 @@ static int check_i8(const moe_i8_shape* s) {
 }
 
 // A product with too few tiles to give every second CU one has its reduction cut
-// into as many ranges, of at least 512 codes each, as make two tiles a CU; their
-// sums are joined by a second kernel.  A function of the sizes and the device's CU
-// count only: it sizes the workspace.
+// into as many ranges, of at least 512 codes each, as make three tiles for two
+// CUs; their sums are joined by a second kernel.  us without, and with 4, 8 and 16
+// ranges: 128 x 2048 of K 8192 39, 20.9, 19.2, 22.5; 256 x 1024 of 16384 68, 29,
+// 22.5, 25; 16 x 2048 of 8192 41, 17, 13.5, 12.6; 128 x 4096 of 4096 23, 19, 22,
+// 22; and with more tiles 512 x 2048 of 4096 24, 24, 30, 29.  A function of the
+// sizes and the device's CU count only: it sizes the workspace.
 static int i8_nsplit(const moe_i8_shape* s, int cus) {
   const long G = s->n_groups, M = s->M;
   // the smallest tiles of the kernels
   const long wide = i8_mfma_ok(s->N, s->K, s->lda, s->ldc) ? 128 : 64;
   const long tiles = (M / 64 + std::min(G, M)) * ((s->N + wide - 1) / wide);
   if (tiles < 1 || 2 * tiles > cus) return 1;
-  return (int)std::max(1l, std::min({32l, 2l * cus / tiles, (long)s->K / 512}));
+  return (int)std::max(1l, std::min({32l, 3l * cus / (2 * tiles), (long)s->K / 512}));
 }
 
 static size_t i8_part_bytes(const moe_i8_shape* s, int nsplit) {

@@ -15,8 +15,8 @@
 // those that it needs only (load_a below).
 //
 // Measured for 16384 tokens, 12 of 512 + 256 experts, d_model 6144, d_ff 2048:
-// gate and up 3.7 ms (1.8 PFLOP/s), down 2.1 ms; 65536 tokens 10.9 and 6.6 ms
-// (2.4 and 2.0; a library product of 8192^3 2.1); 128 tokens 1.62 and 0.81 ms
+// gate and up 3.5 ms (1.9 POP/s), down 2.1 ms (1.6); 65536 tokens 10.9 and 6.6 ms
+// (2.4 and 2.0; a library product of 8192^3 2.1); 128 tokens 1.62 and 0.83 ms
 // (6.9 TB/s).
 
 #include <algorithm>

@@ -4,6 +4,9 @@
 // A row is read once: it waits in registers while its largest magnitude is
 // found, one wave for short rows, a workgroup for long ones (the longest are
 // read twice).  The codes are those of the exact quotient, see code_of().
+//
+// Bound by memory: 16384 rows of 6144 in bf16 68 us (300 MB, 4.4 TB/s), 196608
+// rows of 2048 184 us (1.2 GB, 6.6 TB/s), 128 rows 5.3 us.
 
 #include <algorithm>
 
@@ -83,6 +86,9 @@ static int launch_quantize_t(const T* x, int64_t ldx, int M, int K, int8_t* q, i
     hipLaunchKernelGGL((quantize_kernel<T, N, ALONE, NT>), dim3((unsigned)blocks), dim3(NT), 0, st, x, \
                        ldx, M, K, q, ldq, scale, used);                                           \
   } while (0)
+  // a wave for a row up to 1024 columns: 8192 rows of 512 6.6 us, 10.7 with a
+  // workgroup; 32768 of 1024 24 and 37; of 1536 no difference.  As few threads as
+  // hold a row: 8192 rows of 6144 36 us with 256, 57 with 1024
   if (chunks <= 64) MOE_QUANT(1, true, 256);
   else if (chunks <= 128) MOE_QUANT(2, true, 256);
   else if (chunks <= 256) MOE_QUANT(1, false, 256);

@@ -422,8 +422,7 @@ int launch_select(const SelectArgs& a, hipStream_t st) {
   int groups = 1;
   while (groups < a.n_groups) groups *= 2;
   const int lanes = 64 / groups, slots = (a.E / a.n_groups + lanes - 1) / lanes;
-  // few tokens: a wave per workgroup, over more CUs
-  const int waves = a.T < 4 * cus ? 1 : 4;
+  const int waves = 4;  // (one, over more CUs, is no faster for few tokens: 128 9.6 us, not 9.3)
   const dim3 block(64 * waves);
   const dim3 grid((unsigned)std::min<long>(((long)a.T + waves - 1) / waves, (long)cus * 5));
 #define MOE_SELECT(PL) hipLaunchKernelGGL(select_kernel<PL>, grid, block, 0, st, a)
@@ -543,7 +542,7 @@ template <typename T>
 static int launch_select_bwd_t(const SelectBwdArgs& a, hipStream_t st) {
   const int cus = stream_cu_count(st);
   if (cus <= 0) return MOE_EHIP;
-  const int waves = a.T < 4 * cus ? 1 : 4;
+  const int waves = 4;  // (one is no faster for few tokens: 128 5.7 us, not 5.8; 1 8.6, not 5.5)
   const dim3 block(64 * waves);
   const dim3 grid((unsigned)std::min<long>(((long)a.T + waves - 1) / waves, (long)cus * 16));
   const int slots = (std::max(a.E, a.dl ? a.ep : 0) + 63) / 64;
