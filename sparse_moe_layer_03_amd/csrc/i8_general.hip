@@ -9,7 +9,7 @@
 // tiles of all groups, which it finds from the offsets itself.
 //
 // Bound by the loads' address work beside the MFMAs: 8191 rows by [2047, 2049]
-// 105 us (0.65 POP/s); 389 rows by [1001, 2049] 11.6 us in 4 ranges of K, and 4.1
+// 105 us (0.65 POP/s); 389 rows by [1001, 2049] 12.6 us in 3 ranges of K, and 4.4
 // to join them.
 
 #include <algorithm>

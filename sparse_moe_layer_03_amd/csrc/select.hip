@@ -18,7 +18,7 @@
 //
 // The kernel reads 4 bytes an expert and is bound by its instructions (some 800
 // a token and wave at 768 experts) and their latencies: 16384 tokens over 768
-// experts in 8 groups 39 us (50 MB), 128 tokens 10.5 us, of which an empty
+// experts in 8 groups 39 us (50 MB), 128 tokens 10 us, of which an empty
 // kernel takes 2.5.  The gradient reads and writes 8 bytes: 8192 tokens over 384
 // experts 8.8 us.
 
@@ -422,7 +422,7 @@ int launch_select(const SelectArgs& a, hipStream_t st) {
   int groups = 1;
   while (groups < a.n_groups) groups *= 2;
   const int lanes = 64 / groups, slots = (a.E / a.n_groups + lanes - 1) / lanes;
-  const int waves = 4;  // (one, over more CUs, is no faster for few tokens: 128 9.6 us, not 9.3)
+  const int waves = 4;  // (one, over more CUs, is no faster for few tokens: 128 9.6 us, with four 9.3)
   const dim3 block(64 * waves);
   const dim3 grid((unsigned)std::min<long>(((long)a.T + waves - 1) / waves, (long)cus * 5));
 #define MOE_SELECT(PL) hipLaunchKernelGGL(select_kernel<PL>, grid, block, 0, st, a)
@@ -542,7 +542,7 @@ template <typename T>
 static int launch_select_bwd_t(const SelectBwdArgs& a, hipStream_t st) {
   const int cus = stream_cu_count(st);
   if (cus <= 0) return MOE_EHIP;
-  const int waves = 4;  // (one is no faster for few tokens: 128 5.7 us, not 5.8; 1 8.6, not 5.5)
+  const int waves = 4;  // (one is no faster for few tokens: 128 5.7 us, with four 5.8; 1 8.6 and 5.5)
   const dim3 block(64 * waves);
   const dim3 grid((unsigned)std::min<long>(((long)a.T + waves - 1) / waves, (long)cus * 16));
   const int slots = (std::max(a.E, a.dl ? a.ep : 0) + 63) / 64;
