@@ -13,6 +13,7 @@ layer's own calls, as the blocks of a model use them.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -263,11 +264,25 @@ def moe_quantize_rows(shape: MoeQuantShape, x, q, scale, stream=None):
          _strided("q", q, torch.int8, s.M, s.K, s.ldq, dev), _flat("scale", scale, torch.float32, s.M, dev))
 
 
+def _allocating_on(stream, device):
+    """Tensors made inside belong to `stream` (torch's allocator hands out memory
+    in the order of one stream's work); None: to the current one."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 def quantize_rows(x, stream=None):
     """Codes and scales of x [..., K], contiguous, in new tensors: weights
-    [n, out, in] get a scale for each output channel."""
-    q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-    scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    [n, out, in] get a scale for each output channel.  The tensors belong to
+    `stream`, as if made with it as the current one: another stream that reads
+    them waits for it first and marks its use (Tensor.record_stream)."""
+    _device("x", x)
+    with _allocating_on(stream, x.device):
+        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     K = x.shape[-1]
     moe_quantize_rows(make_quant_shape(x.dtype, x.numel() // K, K), x.view(-1, K), q.view(-1, K),
                       scale.view(-1), stream)
@@ -385,7 +400,7 @@ def moe_norm_residual_backward(shape: MoeNormShape, ws, *, r=None, y=None, w_pos
 
 class I8Experts:
     """The experts' weights in 8 bits: codes and the scales of their output
-    channels, laid out once (moe_quantize_rows)."""
+    channels, laid out once (quantize_rows, on `stream`, to which they belong)."""
 
     def __init__(self, w_gate, w_up, w_down, stream=None):
         (self.w_gate, self.s_gate), (self.w_up, self.s_up), (self.w_down, self.s_down) = (
