@@ -226,8 +226,13 @@ def layer_forward(buf: LayerBuffers, x, w_router, bias, w_gate, w_up, w_down, lo
                   logits_out=None, stream=None, select=None):
     """route -> dispatch -> expert FFN -> combine; outputs land in ``buf``.
     select: another selection rule than moe_route's (``block.make_select``;
-    logits_out is needed then)."""
+    logits_out is needed then, and all calls run on x's device, as that one does;
+    without it on the current one)."""
     s = buf.shape
+    if select is not None and x.get_device() not in (-1, torch.cuda.current_device()):
+        with torch.cuda.device(x.device):
+            return layer_forward(buf, x, w_router, bias, w_gate, w_up, w_down, logit_bias, logits_out,
+                                 stream, select)
     if select is None:
         moe_route(s, x, w_router, logit_bias, bias, buf.topk_idx, buf.topk_gate, logits_out, buf.ws,
                   stream)

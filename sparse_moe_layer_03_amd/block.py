@@ -437,6 +437,11 @@ def block_forward(buf: BlockBuffers, params: MoeSelectParams, norm: MoeNormShape
     (I8Experts, or w_gate, w_up, w_down) and combine, then r = res_scale x + gate
     norm(y, w_post) and the next block's input h = norm(r, w_pre), in ``buf``."""
     s, L, h = buf.shape, buf.layer, before.h
+    dev = _device("before.h", h)
+    if dev != torch.cuda.current_device():      # (the layer's own calls go by the current device)
+        with torch.cuda.device(dev):
+            return block_forward(buf, params, norm, x, before, w_router, bias, experts, w_post=w_post, gate=gate,
+                                 w_pre=w_pre, logit_bias=logit_bias, stream=stream)
     moe_route_select(s, params, h, w_router, logit_bias, bias, L.topk_idx, L.topk_gate, buf.logits, L.ws, stream)
     B.moe_dispatch(s, L.topk_idx, h, L.counts, L.offsets, L.perm, L.inv_perm, L.x_perm, L.ws, stream)
     if isinstance(experts, I8Experts):

@@ -88,3 +88,66 @@ def test_codes_are_allocated_on_the_stream_that_writes_them(monkeypatch, stream,
     m.made.clear()
     K.I8Experts(x, x, x, stream=stream)
     assert m.made == [handle] * 6
+
+
+class Library:
+    """Writes down each call, the current device and the stream it was given."""
+
+    def __init__(self, m):
+        self.m = m
+
+    def __getattr__(self, name):
+        def call(*args):
+            if name.endswith("_bytes"):
+                return 0
+            handle = args[-1]
+            self.m.calls.append((name, self.m.device, handle.value if hasattr(handle, "value") else handle))
+            return 0
+        return call
+
+
+@pytest.mark.parametrize("stream,handle", [(None, 7), (Stream("cuda:1", 64), 64)])
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("what", ["block_forward", "layer_forward"])
+def test_all_calls_of_a_block_run_on_its_tensors_device(monkeypatch, what, i8, stream, handle):
+    """Tensors on cuda:1 while cuda:0 is current: a call on each device would leave
+    them without an order."""
+    m = Machine(monkeypatch)
+    m.streams[1] = 7
+    monkeypatch.setattr(K, "lib", lambda: Library(m))
+    monkeypatch.setattr(B, "lib", lambda: Library(m))
+    s = B.make_shape(4, 64, 6, 2, 64, 2, "f32")
+
+    def new(*n, dtype=torch.float32):
+        return on_gpu(torch.empty(n, dtype=dtype), 1)
+
+    class Some:
+        pass
+
+    L = Some()
+    for n, t in (("topk_idx", new(4, 2, dtype=torch.int32)), ("topk_gate", new(4, 2)), ("perm", new(8, dtype=torch.int32)),
+                 ("inv_perm", new(8, dtype=torch.int32)), ("counts", new(8, dtype=torch.int32)),
+                 ("offsets", new(9, dtype=torch.int32)), ("x_perm", new(8, 64)), ("y_perm", new(8, 64)), ("y", new(4, 64)),
+                 ("ws", new(256, dtype=torch.uint8)), ("shape", s)):
+        setattr(L, n, t)
+    x, w, router, logits, rule = new(4, 64), new(6, 64, 64), new(8, 64), new(4, 8), K.make_select("sigmoid")
+    if what == "layer_forward":
+        if i8:
+            pytest.skip("the layer's own weights")
+        B.layer_forward(L, x, router, None, w, w, w, logits_out=logits, stream=stream, select=rule)
+        want = ["moe_route_select", "moe_dispatch", "moe_expert_ffn", "moe_combine"]
+    else:
+        buf, before, e = Some(), Some(), (w, w, w)
+        buf.shape, buf.layer, buf.logits, buf.r, buf.h, buf.ws = s, L, logits, new(4, 64), new(4, 64), L.ws
+        buf.q = buf.q_scale = before.q = None
+        before.h = new(4, 64)
+        if i8:
+            e = K.I8Experts.__new__(K.I8Experts)
+            for n in ("gate", "up", "down"):
+                setattr(e, "w_" + n, new(6, 64, 64, dtype=torch.int8))
+                setattr(e, "s_" + n, new(6, 64))
+        K.block_forward(buf, rule, K.make_norm_shape(4, 64, "f32"), x, before, router, None, e, stream=stream)
+        want = ["moe_route_select", "moe_dispatch", "moe_expert_ffn_i8" if i8 else "moe_expert_ffn", "moe_combine",
+                "moe_norm_residual"]
+    assert m.calls == [(n, 1, handle) for n in want]
+    assert m.device == 0
