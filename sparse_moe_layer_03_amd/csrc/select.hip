@@ -60,11 +60,12 @@ __device__ __forceinline__ uint64_t ordered(double key) {
   return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
 }
 
-// A group's score from its two best keys: a second one of -inf (switched off, or
-// none) does not count.
+// Half of a group's score from its two best keys (the sum of two finite ones may
+// pass fp32's range): a second one of -inf (switched off, or none) does not count.
 template <typename F>
 __device__ __forceinline__ F group_score(F best, F best2, bool two) {
-  return two && best != (F)INFINITY && best2 != -(F)INFINITY ? best + best2 : best;
+  const F h = (F)0.5 * best;
+  return two && best != (F)INFINITY && best2 != -(F)INFINITY ? fma((F)0.5, best2, h) : h;
 }
 
 // What a lane knows about its place.
@@ -313,10 +314,11 @@ __global__ void __launch_bounds__(256, PL <= 12 ? 5 : 2) select_kernel(SelectArg
       }
       bool kept = w.g < w.G && rank < a.top_groups;
       // Another group within the margin below the last one that stays: again in
-      // 64 bits.  (Each of the sum's two keys has a score of at most P.)
+      // 64 bits.  (Each of the sum's two keys has a score of at most P, and the
+      // half of both margins is one.)
       const uint64_t last = __ballot(w.g < w.G && rank == a.top_groups - 1);
       const float cut = lane_value(s, __ffsll((unsigned long long)last) - 1);
-      const float low = cut - 2.f * margin(fabsf(cut) + top);
+      const float low = cut - margin(2.f * fabsf(cut) + top);
       if (__ballot(w.g < w.G && !kept && s >= low && s > -INFINITY) != 0)
         kept = kept64(a, exact_scores(row, m, softmax, w), s_bias, w);
 #pragma unroll
