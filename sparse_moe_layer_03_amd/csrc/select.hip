@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(256) select_bwd_kernel(SelectBwdArgs a) {
       else e = -1;
     }
     float p[PL];
-    float sel;  // the slots' scores
+    float sel, other = 1.f;  // the slots' scores p, and 1 - p of a sigmoid
     if (softmax) {
       float m = -INFINITY;
 #pragma unroll
@@ -492,6 +492,8 @@ __global__ void __launch_bounds__(256) select_bwd_kernel(SelectBwdArgs a) {
       sel = e >= 0 ? exp_fast(l - m) * inv : 0.f;
     } else {
       sel = e >= 0 ? 1.f / (1.f + exp_fast(-l)) : 0.f;
+      // (not from p: for a logit of 16 it is 2 steps of p, above 17 less than one)
+      other = 1.f / (1.f + exp_fast(l));
     }
     float d = a.scaling * dg, c;
     if (a.renorm) {
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(256) select_bwd_kernel(SelectBwdArgs a) {
       const float o = lane_value(d, q);
       both += (int)lane_value((uint32_t)e, q) == e ? o : 0.f;
     }
-    if (e >= 0) dp[e] = softmax ? both : both * sel * (1.f - sel);
+    if (e >= 0) dp[e] = softmax ? both : both * sel * other;
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
