@@ -67,7 +67,8 @@ typedef struct {
  *   f_j = p[t, idx_j], or with renorm p[t, idx_j] / (sum_i p[t, idx_i] +
  *         renorm_eps) (0 where that divisor is 0)
  * The selection is that of keys computed in 64 bits: keys too close for fp32
- * to tell apart are computed again.  Scores and gates are fp32.
+ * to tell apart are computed again.  Scores and gates are fp32, scores below its
+ * normal numbers 0; in a renormalised gate they count as 64 bits hold them.
  *   logits [T, E] fp32, E <= ld_logits < 2^24 elements from row to row; bias
  *   [E] fp32.
  * An expert with bias -inf is taken only where the kept groups have fewer than

@@ -68,6 +68,28 @@ __device__ __forceinline__ F group_score(F best, F best2, bool two) {
   return two && best != (F)INFINITY && best2 != -(F)INFINITY ? fma((F)0.5, best2, h) : h;
 }
 
+// The slots' scores (in lanes, of the logits l; none where `slot` is not set)
+// divided by their sum + eps, and eps by it, for a sum so small that scores below
+// fp32's normal numbers, which the kernels flush, weigh in it: with a power of 2
+// of their own, down to where 64 bits hold 0.  (inv: 1 / softmax's sum; sigmoid:
+// its denominator is 1 here.)
+constexpr float kSmallSum = 0x1p-64f;
+struct Shares {
+  float f, eps;
+};
+__device__ __forceinline__ Shares small_shares(bool slot, float l, float m, float inv, float eps) {
+  constexpr double kLog2e = 1.4426950408889634;
+  const double t = fmax(((double)l - (double)m) * kLog2e, -1100.0), n = rint(t);
+  const float e = __builtin_amdgcn_exp2f((float)(t - n)) * inv;
+  const int k = (int)n;
+  slot = slot && k >= -1074;
+  const int top = (int)wave_max_u(slot ? (uint32_t)(k + 1100) : 0u) - 1100;
+  const float f = slot ? ldexpf(e, k - top) : 0.f;
+  const float sum = wave_sum_f(f), rest = (float)ldexp((double)eps, -top), whole = sum + rest;
+  if (whole == 0.f) return Shares{0.f, 0.f};
+  return Shares{f / whole, rest == 0.f ? 0.f : 1.f / (1.f + sum / rest)};  // (rest may be infinite)
+}
+
 // What a lane knows about its place.
 struct Lanes {
   int g, j, L, each, G;   // group, place in it, lanes and experts a group, groups
@@ -409,7 +431,8 @@ __global__ void __launch_bounds__(256, PL <= 12 ? 5 : 2) select_kernel(SelectArg
     float f = softmax ? exp_fast(l - m) * inv : __builtin_amdgcn_rcpf(1.f + exp_fast(-l));
     if (a.renorm) {
       const float whole = wave_sum_f(lane < a.k ? f : 0.f) + a.eps;
-      f = whole == 0.f ? 0.f : f / whole;
+      if (whole < kSmallSum) f = small_shares(lane < a.k, l, m, inv, a.eps).f;
+      else f /= whole;
     }
     if (lane < a.k) {
       a.idx[(size_t)t * a.k + at] = id;
@@ -470,8 +493,9 @@ __global__ void __launch_bounds__(256) select_bwd_kernel(SelectBwdArgs a) {
     }
     float p[PL];
     float sel, other = 1.f;  // the slots' scores p, and 1 - p of a sigmoid
+    float m = 0.f, inv = 1.f;
     if (softmax) {
-      float m = -INFINITY;
+      m = -INFINITY;
 #pragma unroll
       for (int i = 0; i < PL; ++i) {
         p[i] = lane + 64 * i < a.E ? row[lane + 64 * i] : -INFINITY;
@@ -486,28 +510,37 @@ __global__ void __launch_bounds__(256) select_bwd_kernel(SelectBwdArgs a) {
         sum += p[i];
       }
       sum = wave_sum_f(sum);
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
       for (int i = 0; i < PL; ++i) p[i] *= inv;
       sel = e >= 0 ? exp_fast(l - m) * inv : 0.f;
     } else {
-      sel = e >= 0 ? 1.f / (1.f + exp_fast(-l)) : 0.f;
+      const float x = exp_fast(-l);
+      sel = e >= 0 ? 1.f / (1.f + x) : 0.f;
       // (not from p: for a logit of 16 it is 2 steps of p, above 17 less than one)
-      other = 1.f / (1.f + exp_fast(l));
+      other = fminf(x, 3.4028234663852886e38f) * sel;
     }
     float d = a.scaling * dg, c;
+    bool small = false;  // scores' shares of D in their places, and 1 in D's
     if (a.renorm) {
-      const float whole = wave_sum_f(sel) + a.eps;
-      const float r = whole == 0.f ? 0.f : 1.f / whole;
+      float eps = a.eps, r = 1.f;
+      const float whole = wave_sum_f(sel) + eps;
+      if (whole < kSmallSum) {
+        const Shares s = small_shares(e >= 0, l, m, inv, eps);
+        small = true;
+        sel = s.f, eps = s.eps, other = 1.f;
+      } else {
+        r = 1.f / whole;
+      }
       const float f = wave_sum_f(dg * sel) * r;
       // D (dg_j - f) = sum_i p_i (dg_j - dg_i) + eps dg_j: what dg has in common
       // over the slots falls out of the differences and leaves no rounding
       // behind (one slot and eps 0: the gate is a constant, its gradient 0)
-      float apart = a.eps * dg;
+      float apart = eps * dg;
       for (int q = 0; q < a.k; ++q) apart += lane_value(sel, q) * (dg - lane_value(dg, q));
       d = lane < a.k ? a.scaling * (apart * r) * r : 0.f;
       // sum_j p_j dp_j without its cancellation: sum p (dg - f) = f (D - sum p)
-      c = a.scaling * f * (a.eps * r);
+      c = a.scaling * f * (eps * r);
     } else {
       c = wave_sum_f(sel * d);
     }
@@ -517,12 +550,9 @@ __global__ void __launch_bounds__(256) select_bwd_kernel(SelectBwdArgs a) {
       const float o = lane_value(d, q);
       both += (int)lane_value((uint32_t)e, q) == e ? o : 0.f;
     }
-    if (e >= 0) dp[e] = softmax ? both : both * sel * other;
+    if (e >= 0) dp[e] = !softmax ? both * sel * other : small ? both * sel : both;
     __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      const int x = lane + 64 * i;
-      const float v = softmax ? p[i] * (dp[x] - c) : dp[x];
+    auto put = [&](int x, float v) {
       if (x < a.E && a.dlogits != nullptr) a.dlogits[(size_t)t * a.E + x] = v;
       if (a.dl != nullptr && x < a.ep) {
         const float w = x < a.E ? v : 0.f;
@@ -535,6 +565,16 @@ __global__ void __launch_bounds__(256) select_bwd_kernel(SelectBwdArgs a) {
           to[a.ep + x] = (__bf16)(w - (float)hi);
         }
       }
+    };
+    if (!softmax) {
+#pragma unroll
+      for (int i = 0; i < PL; ++i) put(lane + 64 * i, dp[lane + 64 * i]);
+    } else if (!small) {
+#pragma unroll
+      for (int i = 0; i < PL; ++i) put(lane + 64 * i, p[i] * (dp[lane + 64 * i] - c));
+    } else {
+#pragma unroll
+      for (int i = 0; i < PL; ++i) put(lane + 64 * i, dp[lane + 64 * i] - p[i] * c);
     }
     __builtin_amdgcn_wave_barrier();
     if (e >= 0) dp[e] = 0.f;

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from sparse_moe_layer_03_amd import block as K
-from tests.block_util import say, score_error, select_ref
+from tests.block_util import say, score_error, scores, select_ref
 from tests.test_gpu_select import check, shape
 
 pytestmark = pytest.mark.gpu
@@ -81,3 +81,68 @@ def test_gradient_of_saturated_sigmoids(T, E, k, renorm, eps):
     assert ((out.double() - ref).abs() <= 8 * score_error(p, logits) * bound).all()
     if not renorm:
         assert ((out != 0).sum(1) == k).all()
+
+
+def tiny_scores(score, T, E, seed):
+    """Logits whose scores, but for softmax's first expert, reach from 2^-60 down
+    to 1e-260; rows whose scores are 0 in 64 bits as well."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    depth = torch.rand((T, 1), generator=g, device="cuda") * 550 + 42
+    logits = -depth - torch.rand((T, E), generator=g, device="cuda") * torch.rand((T, 1), generator=g, device="cuda") * 40
+    logits[1] = -math.inf
+    logits[2] = -800.0
+    logits[3, 4:] = -800.0
+    if score == "softmax":
+        logits[:, 0] = 0.0
+    return logits
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-30, 1e-20])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k", [(400, 96, 8), (60, 768, 12), (70, 7, 1)])
+def test_renormalised_gates_of_scores_below_fp32s_normal_numbers(T, E, k, score, eps):
+    bias = None
+    if score == "softmax":                  # the experts behind the one that holds all
+        bias = torch.zeros(E, device="cuda")
+        bias[0] = -math.inf
+    logits = tiny_scores(score, T, E, 5)
+    _, gate = check(T, E, k, (score, 1, 1, 1, True, eps), logits=logits, bias=bias)
+    if eps == 0:
+        have = [t for t in range(T) if t not in (1, 2)]
+        assert ((gate[have].sum(1) - 2.5).abs() < 1e-5).all() and (gate[1:3] == 0).all()
+    if E % 4 == 0:
+        check(T, E, k, (score, 4, 3, 2, True, eps), logits=logits, bias=bias)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-30, 1e-20])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k", [(400, 96, 8), (60, 768, 12), (70, 7, 1)])
+def test_gradient_of_renormalised_gates_of_scores_below_fp32s_normal_numbers(T, E, k, score, eps):
+    """With f_j = p_j / D: p_e dp_e = s f_e (eps / D dg_e + sum_i f_i (dg_e - dg_i)), and
+    sum_j p_j dp_j = s sum_i f_i dg_i eps / D."""
+    say(f"[select_backward, small scores] T={T} E={E} k={k} {score} {eps}")
+    logits = tiny_scores(score, T, E, 6)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    p = K.make_select(score, renorm=True, renorm_eps=eps)
+    first = int(score == "softmax" and E > 7)
+    idx = torch.argsort(torch.rand((T, E - first), generator=g, device="cuda"), 1)[:, :k].sort(1).values + first
+    if score == "softmax" and k > 1:
+        idx[5:9, 0] = 0                     # (with the one that holds all)
+    dgate = torch.randn((T, k), generator=g, device="cuda")
+    out = torch.full((T, E), math.nan, device="cuda")
+    K.moe_select_backward(shape(T, E, k, 2.5), p, logits, idx.to(torch.int32), dgate, out)
+    torch.cuda.synchronize()
+    s, dg = scores(p, logits), dgate.double()
+    f = s.gather(1, idx)
+    D = f.sum(1, keepdim=True) + p.renorm_eps
+    f = torch.where(D == 0, f, f / D)
+    e = torch.where(D == 0, D, p.renorm_eps / D)
+    by = torch.sigmoid(-logits.double().gather(1, idx)) if p.score else 1.0
+    apart = dg[:, :, None] - dg[:, None, :]
+    ref, bound = (torch.zeros_like(s).scatter_(1, idx, 2.5 * by * f * ((v * f[:, None, :]).sum(2) + e * d))
+                  for v, d in ((apart, dg), (apart.abs(), dg.abs())))
+    if not p.score:
+        ref = ref - s * 2.5 * (f * dg).sum(1, keepdim=True) * e
+        bound = bound + s * 2.5 * (f * dg.abs()).sum(1, keepdim=True) * e
+    # every score's error in its own share, in the others' and in D; what is held as 0 below 2^-126
+    assert ((out.double() - ref).abs() <= 8 * score_error(p, logits) * bound + 2.0 ** -120).all()
