@@ -107,7 +107,8 @@ int moe_select_backward(const moe_shape* shape, const moe_select_params* params,
 
 /* moe_layer_backward_select -- moe_layer_backward of a layer whose experts
  * moe_select chose: the same, with dlogits as moe_select_backward gives it.
- * io->logits is needed; ws: moe_layer_backward_workspace_bytes(shape). */
+ * io->logits is needed; ws: moe_layer_backward_workspace_bytes(shape).  Overlaps
+ * are refused here, which moe_layer_backward leaves to its caller. */
 int moe_layer_backward_select(const moe_shape* shape, const moe_select_params* params,
                               const moe_backward_io* io, void* ws, void* stream);
 

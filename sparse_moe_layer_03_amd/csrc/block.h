@@ -9,6 +9,48 @@
 
 namespace moe {
 
+// The arrays of a call.  A written one must not overlap any other, but for
+// pairs that may be one and the same memory: rows of the same kind at the same
+// start and stride, each element read before it is written, by one thread.
+struct Arrays {
+  struct Span {
+    uintptr_t from, to;
+    size_t step, width;  // bytes between rows and of a row; 0: one piece
+    bool written, may_alias;
+  };
+  Span s[24];
+  int n = 0;
+  void add(const void* p, size_t bytes, bool written) {
+    if (p == nullptr || bytes == 0) return;
+    s[n++] = Span{(uintptr_t)p, (uintptr_t)p + bytes, 0, 0, written, false};
+  }
+  void rows(const void* p, int64_t ld, int M, int width, int size, bool written, bool may_alias) {
+    if (p == nullptr || M == 0) return;
+    const size_t step = (size_t)ld * size, wide = (size_t)width * size;
+    s[n++] = Span{(uintptr_t)p, (uintptr_t)p + (size_t)(M - 1) * step + wide, step, wide, written, may_alias};
+  }
+  static bool apart(const Span& a, const Span& b) {
+    if (a.from >= b.to || b.from >= a.to) return true;
+    // columns of one wider matrix
+    if (a.step == 0 || a.step != b.step) return false;
+    const Span &lo = a.from <= b.from ? a : b, &hi = a.from <= b.from ? b : a;
+    const size_t at = (hi.from - lo.from) % a.step;
+    return at >= lo.width && at + hi.width <= a.step;
+  }
+  int check() const {
+    for (int i = 0; i < n; ++i)
+      for (int j = 0; j < i; ++j) {
+        if ((!s[i].written && !s[j].written) || apart(s[i], s[j])) continue;
+        // an output in an input's place
+        if (s[i].written != s[j].written && s[i].may_alias && s[j].may_alias &&
+            s[i].from == s[j].from && s[i].step == s[j].step)
+          continue;
+        return MOE_EINVAL;
+      }
+    return MOE_OK;
+  }
+};
+
 // ---- selection (select.hip)
 
 struct SelectArgs {

@@ -151,6 +151,35 @@ static int check_backward(const moe_shape* s, const moe_backward_io* io) {
   return MOE_OK;
 }
 
+// Written arrays and the workspace lie apart from all others.
+static int check_backward_overlaps(const moe_shape* s, const moe_backward_io* io, const void* ws,
+                                   size_t ws_bytes) {
+  const size_t T = s->T, rows = T * s->top_k, d = s->d_model, es = elem_size(s->dtype);
+  const size_t E = (size_t)s->n_ffn + s->n_zero, w = (size_t)s->n_ffn * s->d_ff * d * es;
+  Arrays v;
+  v.add(io->x, T * d * es, false);
+  v.add(io->w_router, E * d * es, false);
+  v.add(io->logits, T * E * 4, false);
+  v.add(io->topk_idx, rows * 4, false);
+  v.add(io->topk_gate, rows * 4, false);
+  v.add(io->offsets, (E + 1) * 4, false);
+  v.add(io->perm, rows * 4, false);
+  v.add(io->inv_perm, rows * 4, false);
+  v.add(io->w_gate, w, false);
+  v.add(io->w_up, w, false);
+  v.add(io->w_down, w, false);
+  v.add(io->dy, T * d * es, false);
+  v.add(io->dx, T * d * es, true);
+  v.add(io->dgate, rows * 4, true);
+  v.add(io->dlogits, T * E * 4, true);
+  v.add(io->dw_router, E * d * es, true);
+  v.add(io->dw_gate, w, true);
+  v.add(io->dw_up, w, true);
+  v.add(io->dw_down, w, true);
+  v.add(ws, ws_bytes, true);
+  return v.check();
+}
+
 int run_layer_backward(const moe_shape* s, const moe_select_params* select,
                        const moe_backward_io* io, void* ws, hipStream_t st) {
   int rc = check_backward(s, io);
@@ -158,6 +187,8 @@ int run_layer_backward(const moe_shape* s, const moe_select_params* select,
   if (!ws) return MOE_EINVAL;
   if (!al16(ws)) return MOE_EALIGN;
   const BwdLayout w = bwd_layout(s);
+  // (moe_layer_backward leaves this to its caller)
+  if (select && (rc = check_backward_overlaps(s, io, ws, w.total))) return rc;
   char* base = (char*)ws;
   const int E = s->n_ffn + s->n_zero, Tk = s->T * s->top_k;
   const int d = s->d_model, f = s->d_ff, dt = s->dtype, es = elem_size(dt);
