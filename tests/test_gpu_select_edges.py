@@ -146,3 +146,22 @@ def test_gradient_of_renormalised_gates_of_scores_below_fp32s_normal_numbers(T, 
         bound = bound + s * 2.5 * (f * dg.abs()).sum(1, keepdim=True) * e
     # every score's error in its own share, in the others' and in D; what is held as 0 below 2^-126
     assert ((out.double() - ref).abs() <= 8 * score_error(p, logits) * bound + 2.0 ** -120).all()
+
+
+def test_infinite_logits():
+    """A softmax over +inf is NaN throughout and, its keys being equal, takes the
+    lowest ids; a sigmoid of +inf is 1."""
+    T, E, k = 5, 96, 4
+    logits = logits_of(T, E, 4)
+    logits[1, 9] = math.inf
+    logits[2, 9] = logits[2, 80] = math.inf
+    logits[3, 40], logits[3, 41] = math.inf, math.nan
+    for renorm in (False, True):
+        idx, gate = check(T, E, k, ("softmax", 1, 1, 1, renorm, 0.0), logits=logits, bias=None)
+        assert gate[1:4].isnan().all() and (idx[1:4] == torch.arange(k, device="cuda")).all()
+        assert torch.isfinite(gate[[0, 4]]).all()
+        idx, gate = check(T, E, k, ("sigmoid", 4, 2, 2, renorm, 0.0), logits=logits, bias=None)
+        assert (idx[1] == 9).any() and (idx[2] == 9).any() and (idx[2] == 80).any() and (idx[3] == 40).any()
+        assert not (idx[3] == 41).any() and torch.isfinite(gate).all()
+        if not renorm:
+            assert (gate[2][(idx[2] == 9) | (idx[2] == 80)] == 2.5).all()
