@@ -68,14 +68,16 @@ typedef struct {
  *         renorm_eps) (0 where that divisor is 0)
  * The selection is that of keys computed in 64 bits: keys too close for fp32
  * to tell apart are computed again.  Scores and gates are fp32, scores below its
- * normal numbers 0; in a renormalised gate they count as 64 bits hold them.
+ * normal numbers 0, but where a renormalised gate's divisor is below 2^-64: there
+ * they count as 64 bits hold them.
  *   logits [T, E] fp32, E <= ld_logits < 2^24 elements from row to row; bias
- *   [E] fp32.
+ *   [E] fp32.  Shape limits as in moe.h, and T * top_k < 2^27 (here and in the
+ *   calls below that take moe_select_params).
  * An expert with bias -inf is taken only where the kept groups have fewer than
  * top_k others, and does not count in its group's sum; one with +inf comes
- * before all others, its group before other groups.  A NaN key ranks as -inf.  A logit of -inf has p = 0, also in
- * a row that holds nothing else; a softmax over a row with a NaN or +inf is
- * NaN throughout.  Any alignment of 4 bytes. */
+ * before all others, its group before other groups.  A NaN key ranks as -inf.  A
+ * logit of -inf has p = 0, also in a row that holds nothing else; a softmax over a
+ * row with a NaN or +inf is NaN throughout.  Any alignment of 4 bytes. */
 int moe_select(const moe_shape* shape, const moe_select_params* params, const float* logits,
                int64_t ld_logits, const float* bias, int32_t* topk_idx, float* topk_gate,
                void* stream);
@@ -138,8 +140,9 @@ int moe_quantize_rows(const moe_quant_shape* shape, const void* x, int8_t* q, fl
  *   and its scales [n_groups, N] contiguous, c [M, N] with ldc.
  * Limits: 1 <= n_groups <= 1024; 0 <= M < 2^27; 1 <= N <= 2^20; 1 <= K < 2^17
  * (a sum of K products of codes stays inside 32 bits); K <= lda < 2^24;
- * N <= ldc < 2^24.  Any sizes and strides within them; K and lda that are
- * multiples of 16 take the fast kernels. */
+ * N <= ldc < 2^24.  Any sizes and strides within them; the fast kernels take K
+ * and lda that are multiples of 16 with N and ldc that are multiples of 4, and
+ * lda and ldc up to 2^20. */
 typedef struct {
   int32_t out_dtype; /* moe_dtype of c                                       */
   int32_t n_groups;

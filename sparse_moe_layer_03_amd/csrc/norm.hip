@@ -8,8 +8,17 @@
 // the next row's loads in flight.  The vectors (w_post, w_pre) stay in
 // registers over all rows, in their own type.  Bound by memory: 4 arrays (x,
 // y, r, h) forward, 6 backward.  16384 rows of 6144 in bf16 145 us (805 MB, 5.6
-// TB/s), 128 rows 5.8; backward 8192 rows of 4096 89 us and 12 for the sums (403
-// MB, 4.0 TB/s).
+// TB/s), with h's codes besides 177 and with the codes alone 150, 128 rows 5.6;
+// backward 8192 rows of 4096 89 us and 12 for the sums (403 MB, 4.0 TB/s).
+//
+// Not bound by memory are the gradients of short and of the longest rows.  Up to
+// 2048 columns there are one or two waves a SIMD, each a row group with partial
+// sums of its own, whose loads and reductions nothing covers (8192 rows of 512: 29
+// us, 7 of them vector issue, 50 MB and 6 for the sums).  Beyond 8192 columns a
+// workgroup of 1024 threads has 128 registers a lane and the row does not fit: by
+// counters 4096 rows of 16384 write 1.19 GB where dx and dy are 0.27, and load 8
+// times as often, from scratch memory (spilled registers, bf16: 29 up to 8192
+// columns, 215 up to 16384, 617 beyond; the forward kernel 54 beyond 16384).
 //
 // Backward, a row group walks over neighbouring rows and keeps its sums of
 // the vectors' gradients in fp32 registers; a second kernel adds the groups'
@@ -28,7 +37,8 @@ namespace moe {
 
 // f(type, rows of whole chunks, rows that are not kept in the caches): arrays that
 // L2 (4 MiB an XCD) cannot hold for the next kernel anyway are loaded and stored
-// non-temporally (16384 rows of 6144: 153 -> 145 us).
+// non-temporally (16384 rows of 6144: 153 -> 145 us; measured by itself, not with
+// the router and experts that read h next).
 template <typename F>
 static int dispatch(const moe_norm_shape& s, F f) {
   const bool bf16 = s.dtype == MOE_BF16, whole = s.d_model % kChunk == 0;
