@@ -16,7 +16,7 @@
 // sums of its own, whose loads and reductions nothing covers (8192 rows of 512: 29
 // us, 7 of them vector issue, 50 MB and 6 for the sums).  Beyond 8192 columns a
 // workgroup of 1024 threads has 128 registers a lane and the row does not fit: by
-// counters 4096 rows of 16384 write 1.19 GB where dx and dy are 0.27, and load 8
+// counters 4096 rows of 16384 write 1.2 GB where dx and dy are 0.27, and load 8
 // times as often, from scratch memory (spilled registers, bf16: 29 up to 8192
 // columns, 215 up to 16384, 617 beyond; the forward kernel 54 beyond 16384).
 //
