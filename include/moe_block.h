@@ -77,7 +77,9 @@ typedef struct {
  * top_k others, and does not count in its group's sum; one with +inf comes
  * before all others, its group before other groups.  A NaN key ranks as -inf.  A
  * logit of -inf has p = 0, also in a row that holds nothing else; a softmax over a
- * row with a NaN or +inf is NaN throughout.  Any alignment of 4 bytes. */
+ * row with a NaN or +inf is NaN throughout.  Experts are switched off with -inf: a
+ * finite bias far beyond all scores costs every token the 64-bit keys (fp32 cannot
+ * tell what it is added to).  Any alignment of 4 bytes. */
 int moe_select(const moe_shape* shape, const moe_select_params* params, const float* logits,
                int64_t ld_logits, const float* bias, int32_t* topk_idx, float* topk_gate,
                void* stream);
@@ -241,7 +243,7 @@ typedef struct {
  * x rstd(x) w_pre (x needed, res_scale 1, w_post, gate and r absent); without
  * x the residual term is missing.  The sums of squares are fp32: they overflow
  * in rows of values beyond some 1e19 / sqrt(d_model), and with eps 0 a row of
- * zeros has no rstd.  q and q_scale are moe_quantize_rows of h.
+ * zeros, or of values below some 1e-19, has no rstd.  q and q_scale are moe_quantize_rows of h.
  * r may be x itself (same p and ld).  16-byte aligned arrays, any strides. */
 int moe_norm_residual(const moe_norm_shape* shape, const moe_norm_io* io, void* stream);
 
